@@ -53,8 +53,17 @@ typedef enum {
 
 /* Element type of the KV pools.  With PA_KV_FP16 the query, the pools and the
  * output are all fp16 (q, k, v share one type, as MATE's forward requires);
- * otherwise the query and output are bf16. */
-typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_FP16 = 2 } pa_kv_dtype;
+ * otherwise the query and output are bf16.
+ *
+ * PA_KV_FP4_E2M1, the 4-bit pages: a pool is uint8 [num_pool_pages, Hk, slab]
+ * with slab = pa_page_slab_bytes(D, PA_KV_FP4_E2M1) = 64 * (D / 2 + D / 16)
+ * bytes.  A slab holds 64 rows of D / 2 code bytes (e2m1 codes, element 2i of
+ * the row in the low nibble of byte i), then 64 rows of D / 16 scale bytes (one
+ * e4m3 scale per 16 elements).  An element stands for
+ *   code * block scale * k_scale[g]   (values: v_scale[g]),
+ * k_scale, v_scale fp32 [Hk], positive and finite.  pa_append_kv writes such
+ * pages, pa_decode attends over them, pa_gather_kv reads them back. */
+typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_FP16 = 2, PA_KV_FP4_E2M1 = 3 } pa_kv_dtype;
 
 #define PA_PAGE_SIZE 64
 #define PA_MAX_SPLITS 64
@@ -73,7 +82,7 @@ typedef struct {
     int32_t num_pool_pages;    /* pages in k_pool / v_pool */
     int32_t kv_dtype;          /* pa_kv_dtype */
     int32_t num_sms;           /* SMs of the device (cudaDevAttrMultiProcessorCount) */
-    int32_t ctas_per_sm;       /* persistent decode CTAs per SM; 0 = library default (1) */
+    int32_t ctas_per_sm;       /* persistent decode CTAs per SM; 0 = library default (1; 3 with 4-bit pages) */
     int32_t forced_splits;     /* split-KV count per sequence; 0 = choose automatically */
 } pa_decode_shapes;
 
@@ -153,9 +162,10 @@ pa_status pa_get_metadata_device(const pa_decode_shapes* shapes, const pa_decode
  *
  *   q            bf16 [B, Hq, D] (fp16 with PA_KV_FP16)
  *   k_pool       [num_pool_pages, Hk, 64, D], bf16, e4m3 or fp16 per shapes->kv_dtype
+ *                (4-bit pages: uint8 slabs, see pa_kv_dtype)
  *   v_pool       same layout and type as k_pool
- *   k_scale      fp32 [Hk] per-KV-head dequantisation scale (e4m3 only, else NULL)
- *   v_scale      fp32 [Hk] (e4m3 only, else NULL); an e4m3 element x of head g
+ *   k_scale      fp32 [Hk] per-KV-head dequantisation scale (e4m3 and 4-bit, else NULL)
+ *   v_scale      fp32 [Hk] (e4m3 and 4-bit, else NULL); an e4m3 element x of head g
  *                stands for x * k_scale[g] (keys) or x * v_scale[g] (values)
  *   block_table  int32 [B, max_pages_per_seq]; slots past ceil(len/64) never read
  *   seq_lens     int32 [B] (device copy of the lengths given to pa_get_metadata)
@@ -174,7 +184,9 @@ pa_status pa_get_metadata_device(const pa_decode_shapes* shapes, const pa_decode
  *                calls that may overlap.
  *
  * With fp8 KV the query is used in fp16 (exact for |q| in [2^-14, 65504];
- * smaller magnitudes round to fp16 subnormals).
+ * smaller magnitudes round to fp16 subnormals).  With 4-bit KV it is used in
+ * fp16 after division by a power of two per head (exact for elements above
+ * 2^-14 of the head's largest).
  *
  * Stream order: the call is asynchronous on `stream`.  For every page type
  * but e4m3 at D = 128 (which has a kernel of its own, launched plainly) the
@@ -463,8 +475,16 @@ typedef struct {
  *                   that the new positions fall in
  *   k_pool, v_pool  [num_pool_pages, Hk, 64, D]: bf16 or fp16 (values copied bit
  *                   for bit), or e4m3 with k_scale / v_scale fp32 [Hk]: the stored
- *                   code is e4m3(x / scale) in fp32, nearest even, saturating
+ *                   code is e4m3(x / scale) in fp32, nearest even, saturating; or
+ *                   4-bit slabs (see pa_kv_dtype) with k_scale / v_scale: of every
+ *                   16 elements x, in fp32 with every rounding to nearest even,
+ *                     bs   = e4m3(max |x| / (6 * scale)), saturating at 448
+ *                     code = e2m1(x / (bs * scale)), saturating at 6
+ *                   (codes 0 where bs is 0).  A NaN makes its block's scale NaN,
+ *                   an infinity saturates.
  *   workspace       >= PA_STATUS_BYTES (status word)
+ * With 4-bit pools total_new may exceed cu_seqlens_new[B]: the tokens past it
+ * are padding, and are not read.
  * A position outside the block table or a page id outside the pool is skipped
  * and recorded as PA_ERR_DEVICE_BOUNDS.  Rows of different calls or tokens
  * must not collide (two writers to one row race).
@@ -473,6 +493,106 @@ pa_status pa_append_kv(const pa_append_shapes* shapes, const void* k_new, const 
                        const int32_t* cu_seqlens_new, const int32_t* start_pos, const int32_t* block_table,
                        void* k_pool, void* v_pool, const float* k_scale, const float* v_scale, void* workspace,
                        size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of one (page, KV head) slab of a pool: 64 rows of head_dim elements
+ * (0 for a head_dim or kv_dtype the library does not have). */
+size_t pa_page_slab_bytes(int32_t head_dim, int32_t kv_dtype);
+
+/*
+ * pa_gather_kv -- read rows of a paged cache back into the ragged tensors a
+ * prefill over ragged keys takes: the inverse of pa_append_kv, for pages of
+ * every type.  Row i of sequence b is logical position p = start_pos[b] + i:
+ * row p % 64 of page block_table[b, p / 64].
+ *
+ *   shapes          as for pa_append_kv; total_new = rows of k_out and v_out
+ *   k_pool, v_pool, k_scale, v_scale   as for pa_decode
+ *   cu_seqlens      int32 [B+1] running offsets of the rows to read
+ *   start_pos       int32 [B] first position read of each sequence
+ *   block_table     int32 [B, max_pages_per_seq]
+ *   k_out, v_out    [total_new, Hk, D], fp16 for fp16 pools, else bf16.  16-bit
+ *                   pages are copied bit for bit; an e4m3 element reads back as
+ *                   bf16(x * scale), a 4-bit one as bf16(code * (bs * scale)),
+ *                   the products in fp32
+ *   workspace       >= PA_STATUS_BYTES (status word)
+ * total_new may exceed cu_seqlens[B]: rows past it are left as they were.  A
+ * position outside the block table or a page id outside the pool is skipped
+ * (its row left as it was) and recorded as PA_ERR_DEVICE_BOUNDS.
+ */
+pa_status pa_gather_kv(const pa_append_shapes* shapes, const void* k_pool, const void* v_pool, const float* k_scale,
+                       const float* v_scale, const int32_t* cu_seqlens, const int32_t* start_pos,
+                       const int32_t* block_table, void* k_out, void* v_out, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+
+/* ----------------------------------------------------------------- head norms and rotation */
+
+typedef struct {
+    int32_t total_tokens;  /* T */
+    int32_t num_q_heads;   /* Hq; 0: keys only */
+    int32_t num_kv_heads;  /* Hk; 0: queries only (pa_qk_norm_rope) */
+    int32_t head_dim;      /* D: 64 or 128; 256 with pa_qk_norm_rope */
+    int32_t rope_dim;      /* leading elements of a head that turn, a multiple of 8 in [0, D]; 0: none */
+    int32_t interleaved;   /* pairs: 0 = (i, i + rope_dim / 2), 1 = (2i, 2i + 1) */
+    int32_t num_axes;      /* position axes, 1 to 3 (for instance time, height, width) */
+    int32_t sections[3];   /* pairs per axis, in order; they sum to rope_dim / 2 */
+    int32_t max_position;  /* rows of cos_sin */
+    int32_t dtype;         /* PA_KV_BF16 or PA_KV_FP16: q, k, v, weights and outputs */
+    int32_t norm;          /* 1: RMS norm of every head first, 0: rotation only */
+    float eps;             /* of the norm */
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride; /* elements from one token to the next,
+                                                                         multiples of 8; heads are contiguous */
+} pa_rope_shapes;
+
+/*
+ * pa_qk_norm_rope -- RMS norm of every query and key head, then the rotary
+ * position rotation, in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * weight                  over the D elements
+ *   (a, b) -> (a cos - b sin, b cos + a sin)                for pair i of the first
+ *                                                           rope_dim elements
+ * with cos, sin of pair i at the position of its axis: the first sections[0]
+ * pairs turn with axis 0, the next sections[1] with axis 1, and so on.  fp32
+ * inside, rounded once.
+ *
+ *   q, k             [T, Hq, D], [T, Hk, D], token strides q_stride, k_stride (they
+ *                    may be slices of one packed projection)
+ *   q_weight, k_weight  [D], or NULL for ones
+ *   positions        int32 [num_axes, T]; a negative entry of axis 0 marks a padding
+ *                    token, whose outputs are left as they were
+ *   cos_sin          fp32 [max_position, rope_dim]: rope_dim / 2 cosines, then as many
+ *                    sines (pair i in column i of each half)
+ *   q_out, k_out     [T, Hq, D], [T, Hk, D]; may be q and k themselves (same strides),
+ *                    otherwise must not overlap them
+ *   workspace        >= PA_STATUS_BYTES (status word)
+ * positions and cos_sin may be NULL when rope_dim is 0.  A position at or past
+ * max_position (or a negative one of axis 1 or 2) is recorded as
+ * PA_ERR_DEVICE_BOUNDS and its token left as it was.
+ */
+pa_status pa_qk_norm_rope(const pa_rope_shapes* shapes, const void* q, const void* k, const void* q_weight,
+                          const void* k_weight, const int32_t* positions, const float* cos_sin, void* q_out,
+                          void* k_out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * pa_norm_rope_append_kv -- pa_qk_norm_rope followed by pa_append_kv in one
+ * launch: queries to q_out, normed and turned keys and unchanged values
+ * straight into their pages (of any type).  The pages hold, bit for bit, what
+ * the two calls would leave.
+ *
+ *   rope_shapes, q, k, q_weight, k_weight, cos_sin, q_out   as above (D 64 or 128;
+ *                    k_out_stride unused)
+ *   append_shapes, cu_seqlens_new, start_pos, block_table, pools, scales   as for
+ *                    pa_append_kv; tokens, KV heads and head_dim of the two shapes
+ *                    agree; fp16 tokens go to fp16 pools, bf16 tokens to the others
+ *   v                [T, Hk, D], token stride v_stride
+ *   positions        as above, or NULL: every axis at the token's cache position
+ * T may exceed cu_seqlens_new[B]: the tokens past it are padding, and nothing
+ * of them is read or written.  A token whose position, page or page id is out
+ * of range is skipped (queries too) and recorded as PA_ERR_DEVICE_BOUNDS.
+ */
+pa_status pa_norm_rope_append_kv(const pa_rope_shapes* rope_shapes, const pa_append_shapes* append_shapes,
+                                 const void* q, const void* k, const void* v, const void* q_weight,
+                                 const void* k_weight, const int32_t* positions, const float* cos_sin,
+                                 const int32_t* cu_seqlens_new, const int32_t* start_pos, const int32_t* block_table,
+                                 void* q_out, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
+                                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ----------------------------------------------------------------- status */
 

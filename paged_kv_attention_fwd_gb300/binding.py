@@ -20,7 +20,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "pa.h")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA, PA_ERR_TIMEOUT, \
     PA_ERR_DEVICE_BOUNDS = range(7)
-PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_FP16 = 0, 1, 2
+PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_FP16, PA_KV_FP4_E2M1 = 0, 1, 2, 3
 PA_STATUS_BYTES = 256
 STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_WORKSPACE",
                 4: "PA_ERR_CUDA", 5: "PA_ERR_TIMEOUT", 6: "PA_ERR_DEVICE_BOUNDS"}
@@ -65,6 +65,14 @@ class pa_append_shapes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "batch", "num_kv_heads", "head_dim", "page_size", "max_pages_per_seq", "num_pool_pages", "total_new",
         "kv_dtype")]
+
+
+class pa_rope_shapes(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("total_tokens", "num_q_heads", "num_kv_heads", "head_dim", "rope_dim",
+                                               "interleaved", "num_axes")]
+                + [("sections", ctypes.c_int32 * 3)]
+                + [(n, ctypes.c_int32) for n in ("max_position", "dtype", "norm")] + [("eps", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride", "k_out_stride")])
 
 
 _lib = None
@@ -115,6 +123,15 @@ def lib() -> ctypes.CDLL:
         L.pa_mixed.restype = ctypes.c_int
         L.pa_append_kv.argtypes = [ctypes.POINTER(pa_append_shapes), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]
         L.pa_append_kv.restype = ctypes.c_int
+        L.pa_page_slab_bytes.argtypes = [i32, i32]
+        L.pa_page_slab_bytes.restype = sz
+        L.pa_gather_kv.argtypes = [ctypes.POINTER(pa_append_shapes), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]
+        L.pa_gather_kv.restype = ctypes.c_int
+        L.pa_qk_norm_rope.argtypes = [ctypes.POINTER(pa_rope_shapes), _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]
+        L.pa_qk_norm_rope.restype = ctypes.c_int
+        L.pa_norm_rope_append_kv.argtypes = [ctypes.POINTER(pa_rope_shapes), ctypes.POINTER(pa_append_shapes), _P, _P,
+                                             _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]
+        L.pa_norm_rope_append_kv.restype = ctypes.c_int
         L.pa_prefill_workspace_size.argtypes = [ctypes.POINTER(pa_prefill_shapes)]
         L.pa_prefill_workspace_size.restype = ctypes.c_size_t
         L.pa_check_status.argtypes = [_P, _P]
@@ -339,6 +356,40 @@ def pa_append_kv(shapes: pa_append_shapes, k_new, v_new, cu_seqlens_new, start_p
     _check(lib().pa_append_kv(ctypes.byref(shapes), _ptr(k_new), _ptr(v_new), _ptr(cu_seqlens_new), _ptr(start_pos),
                               _ptr(block_table), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
                               _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def pa_page_slab_bytes(head_dim: int, kv_dtype: int) -> int:
+    return int(lib().pa_page_slab_bytes(int(head_dim), int(kv_dtype)))
+
+
+def pa_gather_kv(shapes: pa_append_shapes, k_pool, v_pool, k_scale, v_scale, cu_seqlens, start_pos, block_table, k_out,
+                 v_out, workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_gather_kv(ctypes.byref(shapes), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+                              _ptr(cu_seqlens), _ptr(start_pos), _ptr(block_table), _ptr(k_out), _ptr(v_out),
+                              _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def pa_qk_norm_rope(shapes: pa_rope_shapes, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, workspace,
+                    workspace_bytes: Optional[int] = None, stream=None) -> None:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_qk_norm_rope(ctypes.byref(shapes), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+                                 _ptr(positions), _ptr(cos_sin), _ptr(q_out), _ptr(k_out), _ptr(workspace),
+                                 int(workspace_bytes), _stream(stream)))
+
+
+def pa_norm_rope_append_kv(rope_shapes: pa_rope_shapes, append_shapes: pa_append_shapes, q, k, v, q_weight, k_weight,
+                           positions, cos_sin, cu_seqlens_new, start_pos, block_table, q_out, k_pool, v_pool, k_scale,
+                           v_scale, workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_norm_rope_append_kv(ctypes.byref(rope_shapes), ctypes.byref(append_shapes), _ptr(q), _ptr(k),
+                                        _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(cos_sin),
+                                        _ptr(cu_seqlens_new), _ptr(start_pos), _ptr(block_table), _ptr(q_out),
+                                        _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(workspace),
+                                        int(workspace_bytes), _stream(stream)))
 
 
 def pa_prefill_workspace_size(shapes: pa_prefill_shapes) -> int:

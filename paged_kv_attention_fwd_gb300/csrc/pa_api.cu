@@ -163,6 +163,12 @@ struct SchedItem {
     int cost, index, b, s, kvh;
 };
 
+// persistent decode CTAs per SM: the caller's count, or what the page type's kernel is built for
+int resolve_ctas_per_sm(const pa_decode_shapes* sh) {
+    if (sh->ctas_per_sm != 0) return sh->ctas_per_sm;
+    return sh->kv_dtype == PA_KV_FP4_E2M1 ? pa::kFp4CtasPerSm : 1;
+}
+
 }  // namespace
 
 namespace pa {
@@ -199,7 +205,7 @@ pa_status pa_get_metadata(const int32_t* seq_lens_host, const int32_t* block_tab
     if (sh->num_sms <= 0) return fail(PA_ERR_INVALID_ARG, "num_sms must be positive (got %d)", sh->num_sms);
     if (sh->ctas_per_sm < 0) return fail(PA_ERR_INVALID_ARG, "ctas_per_sm must be >= 0");
     if (sh->forced_splits < 0) return fail(PA_ERR_INVALID_ARG, "forced_splits must be >= 0");
-    const int cps = sh->ctas_per_sm == 0 ? 1 : sh->ctas_per_sm;
+    const int cps = resolve_ctas_per_sm(sh);
 
     std::vector<int> pages(B);
     int64_t units = 0;
@@ -362,16 +368,18 @@ pa_status check_decode_call(const pa_decode_shapes* sh, const pa_decode_plan* pl
     pa_status st = validate_decode_common(sh, plan, out, meta_dev, workspace, workspace_bytes);
     if (st != PA_OK || sh->batch == 0) return st;
     const int Hk = sh->num_kv_heads;
-    if (sh->kv_dtype != PA_KV_BF16 && sh->kv_dtype != PA_KV_FP8_E4M3 && sh->kv_dtype != PA_KV_FP16)
+    if (sh->kv_dtype < PA_KV_BF16 || sh->kv_dtype > PA_KV_FP4_E2M1)
         return fail(PA_ERR_INVALID_ARG, "unknown kv_dtype %d", sh->kv_dtype);
-    const bool fp8 = sh->kv_dtype == PA_KV_FP8_E4M3;
+    const bool scaled = sh->kv_dtype == PA_KV_FP8_E4M3 || sh->kv_dtype == PA_KV_FP4_E2M1;
     if (sh->max_pages_per_seq <= 0 || sh->num_pool_pages <= 0)
         return fail(PA_ERR_INVALID_ARG, "max_pages_per_seq and num_pool_pages must be positive");
     if ((int64_t)sh->num_pool_pages * Hk * pa::kPage >= ((int64_t)1 << 31))
         return fail(PA_ERR_UNSUPPORTED, "pool rows (pages * Hk * 64) must be below 2^31");
     if (!q || !k_pool || !v_pool || !block_table || !seq_lens)
         return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
-    if (fp8 && (!k_scale || !v_scale)) return fail(PA_ERR_INVALID_ARG, "e4m3 KV needs k_scale and v_scale");
+    if (scaled && (!k_scale || !v_scale))
+        return fail(PA_ERR_INVALID_ARG, "%s KV needs k_scale and v_scale",
+                    sh->kv_dtype == PA_KV_FP8_E4M3 ? "e4m3" : "4-bit");
     if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool))
         return fail(PA_ERR_INVALID_ARG, "q, pools, out and workspace must be 16-byte aligned");
     if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale must be finite");
@@ -391,6 +399,7 @@ pa_status decode_launch(bool fused, const pa_decode_shapes* sh, const pa_decode_
     if (st != PA_OK || sh->batch == 0) return st;
     const int B = sh->batch, Hq = sh->num_q_heads, Hk = sh->num_kv_heads, D = sh->head_dim;
     const bool fp8 = sh->kv_dtype == PA_KV_FP8_E4M3;
+    const bool fp4 = sh->kv_dtype == PA_KV_FP4_E2M1;
     const bool f16 = sh->kv_dtype == PA_KV_FP16;
 
     pa::DecodeArgs a;
@@ -427,7 +436,9 @@ pa_status decode_launch(bool fused, const pa_decode_shapes* sh, const pa_decode_
     std::memset(&mk, 0, sizeof mk);
     std::memset(&mv, 0, sizeof mv);
     std::memset(&mq, 0, sizeof mq);
-    if (!fp8) {
+    if (fp4) {
+        // whole slabs move by untiled bulk copies: no tensor maps
+    } else if (!fp8) {
         const uint64_t dims[2] = {(uint64_t)D, (uint64_t)sh->num_pool_pages * Hk * pa::kPage};
         const uint64_t strides[1] = {(uint64_t)D * 2};
         const uint32_t box[2] = {64, 64};
@@ -450,7 +461,8 @@ pa_status decode_launch(bool fused, const pa_decode_shapes* sh, const pa_decode_
         st = make_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, &mv, v_pool, 2, dims, strides, box);
         if (st != PA_OK) return st;
     }
-    cudaError_t e = pa::launch_decode(D, fp8, a, &mk, &mv, &mq, plan->grid, stream);
+    cudaError_t e = fp4 ? pa::launch_decode_fp4(D, a, plan->grid, stream)
+                        : pa::launch_decode(D, fp8, a, &mk, &mv, &mq, plan->grid, stream);
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
     if (fused && plan->total_splits > B && !a.counters) {
         // no room for the arrival counters: merge in a second kernel
@@ -648,6 +660,46 @@ pa_status pa_prefill(const pa_prefill_shapes* sh, const void* q, const void* k, 
     return PA_OK;
 }
 
+namespace {
+// The checks that writing and reading rows of a paged cache share.  `rows`:
+// what the 16-bit rows are called in messages.
+pa_status check_cache_call(const pa_append_shapes* sh, const void* k_rows, const void* v_rows, const char* rows,
+                           const int32_t* cu_seqlens, const int32_t* start_pos, const int32_t* block_table,
+                           const void* k_pool, const void* v_pool, const float* k_scale, const float* v_scale,
+                           const void* workspace, size_t workspace_bytes) {
+    if (sh->num_kv_heads <= 0 || sh->num_kv_heads > 65535)
+        return fail(PA_ERR_INVALID_ARG, "num_kv_heads must be in [1, 65535] (got %d)", sh->num_kv_heads);
+    if (sh->head_dim != 64 && sh->head_dim != 128)
+        return fail(PA_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", sh->head_dim);
+    if (sh->page_size != pa::kPage) return fail(PA_ERR_INVALID_ARG, "page_size must be 64 (got %d)", sh->page_size);
+    if (sh->max_pages_per_seq <= 0 || sh->num_pool_pages <= 0)
+        return fail(PA_ERR_INVALID_ARG, "max_pages_per_seq and num_pool_pages must be positive");
+    if (sh->kv_dtype < PA_KV_BF16 || sh->kv_dtype > PA_KV_FP4_E2M1)
+        return fail(PA_ERR_INVALID_ARG, "unknown kv_dtype %d", sh->kv_dtype);
+    if (!k_rows || !v_rows || !cu_seqlens || !start_pos || !block_table || !k_pool || !v_pool || !workspace)
+        return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+    if ((sh->kv_dtype == PA_KV_FP8_E4M3 || sh->kv_dtype == PA_KV_FP4_E2M1) && (!k_scale || !v_scale))
+        return fail(PA_ERR_INVALID_ARG, "%s pools need k_scale and v_scale",
+                    sh->kv_dtype == PA_KV_FP8_E4M3 ? "e4m3" : "4-bit");
+    if (!aligned16(k_rows) || !aligned16(v_rows) || !aligned16(k_pool) || !aligned16(v_pool))
+        return fail(PA_ERR_INVALID_ARG, "%s and the pools must be 16-byte aligned", rows);
+    if (workspace_bytes < PA_STATUS_BYTES)
+        return fail(PA_ERR_WORKSPACE, "workspace needs %d bytes, got %zu", PA_STATUS_BYTES, workspace_bytes);
+    return PA_OK;
+}
+}  // namespace
+
+size_t pa_page_slab_bytes(int32_t head_dim, int32_t kv_dtype) {
+    if (head_dim != 64 && head_dim != 128) return 0;
+    switch (kv_dtype) {
+        case PA_KV_BF16:
+        case PA_KV_FP16: return (size_t)pa::kPage * head_dim * 2;
+        case PA_KV_FP8_E4M3: return (size_t)pa::kPage * head_dim;
+        case PA_KV_FP4_E2M1: return (size_t)pa::kPage * (head_dim / 2 + head_dim / 16);
+        default: return 0;
+    }
+}
+
 pa_status pa_append_kv(const pa_append_shapes* sh, const void* k_new, const void* v_new,
                        const int32_t* cu_seqlens_new, const int32_t* start_pos, const int32_t* block_table,
                        void* k_pool, void* v_pool, const float* k_scale, const float* v_scale, void* workspace,
@@ -656,23 +708,9 @@ pa_status pa_append_kv(const pa_append_shapes* sh, const void* k_new, const void
     if (!sh) return fail(PA_ERR_INVALID_ARG, "shapes must not be NULL");
     if (sh->batch < 0 || sh->total_new < 0) return fail(PA_ERR_INVALID_ARG, "batch and total_new must be >= 0");
     if (sh->batch == 0 || sh->total_new == 0) return PA_OK;
-    if (sh->num_kv_heads <= 0 || sh->num_kv_heads > 65535)
-        return fail(PA_ERR_INVALID_ARG, "num_kv_heads must be in [1, 65535] (got %d)", sh->num_kv_heads);
-    if (sh->head_dim != 64 && sh->head_dim != 128)
-        return fail(PA_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", sh->head_dim);
-    if (sh->page_size != pa::kPage) return fail(PA_ERR_INVALID_ARG, "page_size must be 64 (got %d)", sh->page_size);
-    if (sh->max_pages_per_seq <= 0 || sh->num_pool_pages <= 0)
-        return fail(PA_ERR_INVALID_ARG, "max_pages_per_seq and num_pool_pages must be positive");
-    if (sh->kv_dtype != PA_KV_BF16 && sh->kv_dtype != PA_KV_FP8_E4M3 && sh->kv_dtype != PA_KV_FP16)
-        return fail(PA_ERR_INVALID_ARG, "unknown kv_dtype %d", sh->kv_dtype);
-    const bool fp8 = sh->kv_dtype == PA_KV_FP8_E4M3;
-    if (!k_new || !v_new || !cu_seqlens_new || !start_pos || !block_table || !k_pool || !v_pool || !workspace)
-        return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
-    if (fp8 && (!k_scale || !v_scale)) return fail(PA_ERR_INVALID_ARG, "e4m3 pools need k_scale and v_scale");
-    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool))
-        return fail(PA_ERR_INVALID_ARG, "k_new, v_new and the pools must be 16-byte aligned");
-    if (workspace_bytes < PA_STATUS_BYTES)
-        return fail(PA_ERR_WORKSPACE, "workspace needs %d bytes, got %zu", PA_STATUS_BYTES, workspace_bytes);
+    pa_status st = check_cache_call(sh, k_new, v_new, "k_new, v_new", cu_seqlens_new, start_pos, block_table, k_pool,
+                                    v_pool, k_scale, v_scale, workspace, workspace_bytes);
+    if (st != PA_OK) return st;
     pa::AppendArgs a;
     a.k_new = static_cast<const uint16_t*>(k_new);
     a.v_new = static_cast<const uint16_t*>(v_new);
@@ -690,9 +728,182 @@ pa_status pa_append_kv(const pa_append_shapes* sh, const void* k_new, const void
     a.max_pages = sh->max_pages_per_seq;
     a.num_pool_pages = sh->num_pool_pages;
     a.total_new = sh->total_new;
-    a.fp8 = fp8;
-    cudaError_t e = pa::launch_append(a, stream);
+    a.fp8 = sh->kv_dtype == PA_KV_FP8_E4M3;
+    cudaError_t e = sh->kv_dtype == PA_KV_FP4_E2M1 ? pa::launch_append_fp4(a, stream) : pa::launch_append(a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "append launch");
+    return PA_OK;
+}
+
+pa_status pa_gather_kv(const pa_append_shapes* sh, const void* k_pool, const void* v_pool, const float* k_scale,
+                       const float* v_scale, const int32_t* cu_seqlens, const int32_t* start_pos,
+                       const int32_t* block_table, void* k_out, void* v_out, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+    pa::NvtxRange nvtx_range("pa_gather_kv");
+    if (!sh) return fail(PA_ERR_INVALID_ARG, "shapes must not be NULL");
+    if (sh->batch < 0 || sh->total_new < 0) return fail(PA_ERR_INVALID_ARG, "batch and total_new must be >= 0");
+    if (sh->batch == 0 || sh->total_new == 0) return PA_OK;
+    pa_status st = check_cache_call(sh, k_out, v_out, "k_out, v_out", cu_seqlens, start_pos, block_table, k_pool,
+                                    v_pool, k_scale, v_scale, workspace, workspace_bytes);
+    if (st != PA_OK) return st;
+    pa::GatherArgs a;
+    a.k_pool = static_cast<const uint8_t*>(k_pool);
+    a.v_pool = static_cast<const uint8_t*>(v_pool);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.cu = cu_seqlens;
+    a.start_pos = start_pos;
+    a.block_table = block_table;
+    a.k_out = static_cast<uint16_t*>(k_out);
+    a.v_out = static_cast<uint16_t*>(v_out);
+    a.status = static_cast<int*>(workspace);
+    a.batch = sh->batch;
+    a.num_kv_heads = sh->num_kv_heads;
+    a.max_pages = sh->max_pages_per_seq;
+    a.num_pool_pages = sh->num_pool_pages;
+    a.total = sh->total_new;
+    cudaError_t e = pa::launch_gather(a, sh->head_dim, sh->kv_dtype, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "gather launch");
+    return PA_OK;
+}
+
+namespace {
+pa_status check_rope_stride(int64_t stride, int heads, int head_dim, const char* name) {
+    if (heads > 0 && (stride < (int64_t)heads * head_dim || stride % 8 != 0))
+        return fail(PA_ERR_INVALID_ARG, "%s (%lld) must be a multiple of 8 and at least heads * head_dim = %lld", name,
+                    (long long)stride, (long long)heads * head_dim);
+    return PA_OK;
+}
+
+// Shapes and the pointers that both forms of the call have; fills `a`.
+pa_status fill_rope_args(const pa_rope_shapes* sh, const void* q, const void* k, const void* q_weight,
+                         const void* k_weight, const int32_t* positions, const float* cos_sin, void* q_out,
+                         void* workspace, size_t workspace_bytes, pa::NormRopeArgs* a) {
+    const int Hq = sh->num_q_heads, Hk = sh->num_kv_heads, D = sh->head_dim;
+    if (Hq < 0 || Hk < 0 || Hq > 65535 || Hk > 65535 || Hq + Hk == 0)
+        return fail(PA_ERR_INVALID_ARG, "num_q_heads (%d) and num_kv_heads (%d) must be in [0, 65535], not both 0", Hq, Hk);
+    if (D != 64 && D != 128 && D != 256) return fail(PA_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", D);
+    if (sh->dtype != PA_KV_BF16 && sh->dtype != PA_KV_FP16)
+        return fail(PA_ERR_INVALID_ARG, "dtype must be PA_KV_BF16 or PA_KV_FP16 (got %d)", sh->dtype);
+    if (sh->rope_dim < 0 || sh->rope_dim > D || sh->rope_dim % 8 != 0)
+        return fail(PA_ERR_INVALID_ARG, "rope_dim must be a multiple of 8 in [0, head_dim] (got %d)", sh->rope_dim);
+    if (sh->norm != 0 && sh->norm != 1) return fail(PA_ERR_INVALID_ARG, "norm must be 0 or 1 (got %d)", sh->norm);
+    if (sh->norm && !(std::isfinite(sh->eps) && sh->eps >= 0.f))
+        return fail(PA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (sh->rope_dim > 0) {
+        if (sh->num_axes < 1 || sh->num_axes > 3)
+            return fail(PA_ERR_INVALID_ARG, "num_axes must be 1, 2 or 3 (got %d)", sh->num_axes);
+        int64_t pairs = 0;
+        for (int i = 0; i < 3; ++i) {
+            if (sh->sections[i] < 0 || (i >= sh->num_axes && sh->sections[i] != 0))
+                return fail(PA_ERR_INVALID_ARG, "sections[%d] = %d: must be >= 0, and 0 past num_axes", i, sh->sections[i]);
+            pairs += sh->sections[i];
+        }
+        if (pairs != sh->rope_dim / 2)
+            return fail(PA_ERR_INVALID_ARG, "the sections hold %lld pairs, rope_dim has %d", (long long)pairs,
+                        sh->rope_dim / 2);
+        if (sh->max_position <= 0) return fail(PA_ERR_INVALID_ARG, "max_position must be positive");
+        if (!cos_sin) return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+    }
+    pa_status st = check_rope_stride(sh->q_stride, Hq, D, "q_stride");
+    if (st == PA_OK) st = check_rope_stride(sh->k_stride, Hk, D, "k_stride");
+    if (st == PA_OK) st = check_rope_stride(sh->q_out_stride, Hq, D, "q_out_stride");
+    if (st != PA_OK) return st;
+    if ((Hq > 0 && (!q || !q_out)) || (Hk > 0 && !k) || !workspace)
+        return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(q_weight) || !aligned16(k_weight) ||
+        !aligned16(cos_sin))
+        return fail(PA_ERR_INVALID_ARG, "q, k, the weights, cos_sin and the outputs must be 16-byte aligned");
+    if (workspace_bytes < PA_STATUS_BYTES)
+        return fail(PA_ERR_WORKSPACE, "workspace needs %d bytes, got %zu", PA_STATUS_BYTES, workspace_bytes);
+    // one warp per 4 head rows of a token at least, 4 warps to a CTA
+    if ((int64_t)sh->total_tokens * ((Hq + 2 * (int64_t)Hk) / 4 + 1) > ((int64_t)1 << 32))
+        return fail(PA_ERR_UNSUPPORTED, "total_tokens * heads is too large for one launch");
+    std::memset(a, 0, sizeof *a);
+    a->q = static_cast<const uint16_t*>(q);
+    a->k = static_cast<const uint16_t*>(k);
+    a->q_weight = static_cast<const uint16_t*>(q_weight);
+    a->k_weight = static_cast<const uint16_t*>(k_weight);
+    a->positions = positions;
+    a->cos_sin = cos_sin;
+    a->q_out = static_cast<uint16_t*>(q_out);
+    a->status = static_cast<int*>(workspace);
+    a->q_stride = sh->q_stride;
+    a->k_stride = sh->k_stride;
+    a->q_out_stride = sh->q_out_stride;
+    a->total_tokens = sh->total_tokens;
+    a->num_q_heads = Hq;
+    a->num_kv_heads = Hk;
+    a->rope_dim = sh->rope_dim;
+    a->interleaved = sh->interleaved != 0;
+    a->num_axes = sh->num_axes;
+    a->max_position = sh->max_position;
+    a->f16 = sh->dtype == PA_KV_FP16;
+    a->norm = sh->norm;
+    a->sections[0] = sh->sections[0];
+    a->sections[1] = sh->sections[1];
+    a->eps = sh->eps;
+    return PA_OK;
+}
+}  // namespace
+
+pa_status pa_qk_norm_rope(const pa_rope_shapes* sh, const void* q, const void* k, const void* q_weight,
+                          const void* k_weight, const int32_t* positions, const float* cos_sin, void* q_out,
+                          void* k_out, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    pa::NvtxRange nvtx_range("pa_qk_norm_rope");
+    if (!sh) return fail(PA_ERR_INVALID_ARG, "shapes must not be NULL");
+    if (sh->total_tokens < 0) return fail(PA_ERR_INVALID_ARG, "total_tokens must be >= 0");
+    if (sh->total_tokens == 0) return PA_OK;
+    pa::NormRopeArgs a;
+    pa_status st = fill_rope_args(sh, q, k, q_weight, k_weight, positions, cos_sin, q_out, workspace, workspace_bytes, &a);
+    if (st == PA_OK) st = check_rope_stride(sh->k_out_stride, sh->num_kv_heads, sh->head_dim, "k_out_stride");
+    if (st != PA_OK) return st;
+    if ((sh->rope_dim > 0 && !positions) || (sh->num_kv_heads > 0 && !k_out))
+        return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned16(k_out))
+        return fail(PA_ERR_INVALID_ARG, "q, k, the weights, cos_sin and the outputs must be 16-byte aligned");
+    a.k_out = static_cast<uint16_t*>(k_out);
+    a.k_out_stride = sh->k_out_stride;
+    cudaError_t e = pa::launch_norm_rope(a, sh->head_dim, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
+    return PA_OK;
+}
+
+pa_status pa_norm_rope_append_kv(const pa_rope_shapes* sh, const pa_append_shapes* ap, const void* q, const void* k,
+                                 const void* v, const void* q_weight, const void* k_weight, const int32_t* positions,
+                                 const float* cos_sin, const int32_t* cu_seqlens_new, const int32_t* start_pos,
+                                 const int32_t* block_table, void* q_out, void* k_pool, void* v_pool,
+                                 const float* k_scale, const float* v_scale, void* workspace, size_t workspace_bytes,
+                                 cudaStream_t stream) {
+    pa::NvtxRange nvtx_range("pa_norm_rope_append_kv");
+    if (!sh || !ap) return fail(PA_ERR_INVALID_ARG, "shapes must not be NULL");
+    if (sh->total_tokens < 0 || ap->batch < 0) return fail(PA_ERR_INVALID_ARG, "total_tokens and batch must be >= 0");
+    if (sh->total_tokens != ap->total_new || sh->num_kv_heads != ap->num_kv_heads || sh->head_dim != ap->head_dim)
+        return fail(PA_ERR_INVALID_ARG, "the two shapes differ in tokens (%d, %d), KV heads (%d, %d) or head_dim (%d, %d)",
+                    sh->total_tokens, ap->total_new, sh->num_kv_heads, ap->num_kv_heads, sh->head_dim, ap->head_dim);
+    if ((sh->dtype == PA_KV_FP16) != (ap->kv_dtype == PA_KV_FP16))
+        return fail(PA_ERR_INVALID_ARG, "fp16 tokens go to fp16 pools, bf16 tokens to the others");
+    if (ap->batch == 0 || sh->total_tokens == 0) return PA_OK;
+    pa_status st = check_cache_call(ap, k, v, "k, v", cu_seqlens_new, start_pos, block_table, k_pool, v_pool, k_scale,
+                                    v_scale, workspace, workspace_bytes);
+    pa::NormRopeArgs a;
+    if (st == PA_OK)
+        st = fill_rope_args(sh, q, k, q_weight, k_weight, positions, cos_sin, q_out, workspace, workspace_bytes, &a);
+    if (st == PA_OK) st = check_rope_stride(sh->v_stride, sh->num_kv_heads, sh->head_dim, "v_stride");
+    if (st != PA_OK) return st;
+    a.v = static_cast<const uint16_t*>(v);
+    a.v_stride = sh->v_stride;
+    a.cu_new = cu_seqlens_new;
+    a.start_pos = start_pos;
+    a.block_table = block_table;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.batch = ap->batch;
+    a.max_pages = ap->max_pages_per_seq;
+    a.num_pool_pages = ap->num_pool_pages;
+    cudaError_t e = pa::launch_norm_rope_append(a, sh->head_dim, ap->kv_dtype, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "norm, rotation and append launch");
     return PA_OK;
 }
 
@@ -985,7 +1196,7 @@ pa_status pa_get_static_plan(const pa_decode_shapes* sh, pa_decode_plan* plan) {
     if (sh->max_pages_per_seq <= 0) return fail(PA_ERR_INVALID_ARG, "max_pages_per_seq must be positive");
     if (sh->num_sms <= 0 || sh->ctas_per_sm < 0 || sh->forced_splits < 0)
         return fail(PA_ERR_INVALID_ARG, "num_sms must be positive, ctas_per_sm and forced_splits >= 0");
-    const int cps = sh->ctas_per_sm == 0 ? 1 : sh->ctas_per_sm;
+    const int cps = resolve_ctas_per_sm(sh);
     const int64_t cap = (int64_t)sh->num_sms * cps;
     const int64_t splits = sh->forced_splits > 0 ? (int64_t)B * std::min(sh->forced_splits, PA_MAX_SPLITS)
                                                  : B + cdiv(2 * cap, Hk);

@@ -15,6 +15,10 @@ import torch
 from . import binding as B
 
 
+KV_DTYPES = {"bf16": B.PA_KV_BF16, "e4m3": B.PA_KV_FP8_E4M3, "f16": B.PA_KV_FP16, "fp4": B.PA_KV_FP4_E2M1}
+_POOL_TORCH = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "f16": torch.float16, "fp4": torch.uint8}
+
+
 def num_sms(device=None) -> int:
     return torch.cuda.get_device_properties(device or torch.cuda.current_device()).multi_processor_count
 
@@ -54,7 +58,7 @@ def plan_decode(seq_lens_host, block_table_host, num_q_heads: int, num_kv_heads:
     sh = B.pa_decode_shapes(batch=len(seq_lens_host), num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
                             head_dim=head_dim, page_size=64, max_pages_per_seq=max_pages,
                             num_pool_pages=num_pool_pages,
-                            kv_dtype={"bf16": B.PA_KV_BF16, "e4m3": B.PA_KV_FP8_E4M3, "f16": B.PA_KV_FP16}[kv_dtype],
+                            kv_dtype=KV_DTYPES[kv_dtype],
                             num_sms=sms if sms is not None else num_sms(device), ctas_per_sm=ctas_per_sm,
                             forced_splits=forced_splits)
     meta, plan = B.pa_get_metadata(seq_lens_host, block_table_host, sh)
@@ -139,3 +143,101 @@ def prefill(sh: B.pa_prefill_shapes, q, k, v, cu_seqlens_q, cu_seqlens_k, scale:
     B.pa_prefill(sh, q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k, block_table, qo_offset, causal, scale, out, lse,
                  workspace, stream=stream)
     return out, lse, workspace
+
+
+def kv_pool(num_pages: int, num_kv_heads: int, head_dim: int, kv_dtype: str = "bf16", device="cuda") -> torch.Tensor:
+    """A zero-filled K or V pool: [num_pages, Hk, 64, D], or uint8
+    [num_pages, Hk, slab bytes] for 4-bit pages."""
+    tail = ((B.pa_page_slab_bytes(head_dim, B.PA_KV_FP4_E2M1),) if kv_dtype == "fp4" else (64, head_dim))
+    return torch.zeros((num_pages, num_kv_heads, *tail), dtype=_POOL_TORCH[kv_dtype], device=device)
+
+
+def append_shapes(batch: int, num_kv_heads: int, head_dim: int, max_pages: int, num_pool_pages: int, total_new: int,
+                  kv_dtype: str = "bf16") -> B.pa_append_shapes:
+    return B.pa_append_shapes(batch=batch, num_kv_heads=num_kv_heads, head_dim=head_dim, page_size=64,
+                              max_pages_per_seq=max_pages, num_pool_pages=num_pool_pages, total_new=total_new,
+                              kv_dtype=KV_DTYPES[kv_dtype])
+
+
+def _status(workspace, device):
+    return torch.zeros(B.PA_STATUS_BYTES, dtype=torch.uint8, device=device) if workspace is None else workspace
+
+
+def append_kv(sh: B.pa_append_shapes, k_new, v_new, cu_seqlens_new, start_pos, block_table, k_pool, v_pool,
+              k_scale=None, v_scale=None, workspace=None, stream=None):
+    """Write new tokens' keys and values into their pages.  Returns the workspace."""
+    workspace = _status(workspace, k_new.device)
+    B.pa_append_kv(sh, k_new, v_new, cu_seqlens_new, start_pos, block_table, k_pool, v_pool, k_scale, v_scale,
+                   workspace, stream=stream)
+    return workspace
+
+
+def gather_kv(sh: B.pa_append_shapes, k_pool, v_pool, cu_seqlens, start_pos, block_table, k_scale=None, v_scale=None,
+              k_out=None, v_out=None, workspace=None, stream=None):
+    """Rows of a paged cache as ragged [total_new, Hk, D] tensors (fp16 for
+    fp16 pools, else bf16).  Returns (k_out, v_out, workspace)."""
+    dt = torch.float16 if sh.kv_dtype == B.PA_KV_FP16 else torch.bfloat16
+    shape = (sh.total_new, sh.num_kv_heads, sh.head_dim)
+    k_out = torch.empty(shape, dtype=dt, device=k_pool.device) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=dt, device=k_pool.device) if v_out is None else v_out
+    workspace = _status(workspace, k_pool.device)
+    B.pa_gather_kv(sh, k_pool, v_pool, k_scale, v_scale, cu_seqlens, start_pos, block_table, k_out, v_out, workspace,
+                   stream=stream)
+    return k_out, v_out, workspace
+
+
+def rope_table(max_position: int, rope_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """cos_sin for pa_qk_norm_rope: fp32 [max_position, rope_dim], angles
+    position * theta^(-2i / rope_dim) taken in fp64."""
+    pairs = rope_dim // 2
+    freq = theta ** (-torch.arange(pairs, dtype=torch.float64) / max(pairs, 1))
+    angle = torch.arange(max_position, dtype=torch.float64)[:, None] * freq
+    return torch.cat((angle.cos(), angle.sin()), -1).float().to(device)
+
+
+def rope_shapes(q, k, v=None, rope_dim: int = 0, max_position: int = 0, interleaved: bool = False, sections=None,
+                norm: bool = True, eps: float = 1e-6, q_out=None, k_out=None) -> B.pa_rope_shapes:
+    """Shapes of pa_qk_norm_rope for q [T, Hq, D], k and v [T, Hk, D] (slices of
+    a packed projection keep their token stride); outputs not given are
+    contiguous.  sections: pairs per position axis (default: one axis)."""
+    t, hq, d = q.shape
+    hk = k.shape[1]
+    for name, x in (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out)):
+        if x is not None and (x.shape[0] != t or x.shape[2] != d or (x.shape[1] > 1 and x.stride(1) != d)
+                              or x.stride(2) != 1 or x.dtype != q.dtype):
+            raise ValueError(f"{name}: heads must be contiguous rows of q's head_dim and type, one per token")
+    sections = list(sections) if sections is not None else [rope_dim // 2]
+
+    def step(x, heads):  # a single token's stride is never used
+        return heads * d if x is None or t <= 1 else x.stride(0)
+
+    sh = B.pa_rope_shapes(total_tokens=t, num_q_heads=hq, num_kv_heads=hk, head_dim=d, rope_dim=rope_dim,
+                          interleaved=int(interleaved), num_axes=len(sections), max_position=max_position,
+                          dtype={torch.bfloat16: B.PA_KV_BF16, torch.float16: B.PA_KV_FP16}[q.dtype], norm=int(norm),
+                          eps=eps, q_stride=step(q, hq), k_stride=step(k, hk), v_stride=step(v, hk),
+                          q_out_stride=step(q_out, hq), k_out_stride=step(k_out, hk))
+    for i, n in enumerate(sections[:3]):
+        sh.sections[i] = n
+    return sh
+
+
+def qk_norm_rope(sh: B.pa_rope_shapes, q, k, q_weight=None, k_weight=None, positions=None, cos_sin=None, q_out=None,
+                 k_out=None, workspace=None, stream=None):
+    """RMS norm of every head, then the rotation.  Returns (q_out, k_out, workspace)."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    workspace = _status(workspace, q.device)
+    B.pa_qk_norm_rope(sh, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, workspace, stream=stream)
+    return q_out, k_out, workspace
+
+
+def norm_rope_append_kv(sh: B.pa_rope_shapes, append: B.pa_append_shapes, q, k, v, cu_seqlens_new, start_pos,
+                        block_table, k_pool, v_pool, q_weight=None, k_weight=None, positions=None, cos_sin=None,
+                        k_scale=None, v_scale=None, q_out=None, workspace=None, stream=None):
+    """qk_norm_rope with the keys and values going straight into their pages.
+    Returns (q_out, workspace)."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    workspace = _status(workspace, q.device)
+    B.pa_norm_rope_append_kv(sh, append, q, k, v, q_weight, k_weight, positions, cos_sin, cu_seqlens_new, start_pos,
+                             block_table, q_out, k_pool, v_pool, k_scale, v_scale, workspace, stream=stream)
+    return q_out, workspace

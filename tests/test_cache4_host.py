@@ -1,0 +1,205 @@
+"""Host-side checks of the 4-bit page type, the read-back and the norm with
+rotation: bad arguments are refused with the documented status before
+anything is enqueued (no GPU)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import scheduler as S
+from paged_kv_attention_fwd_gb300 import binding as B
+from paged_kv_attention_fwd_gb300 import ops
+from paged_kv_attention_fwd_gb300.build import build
+
+from .test_abi import _Fake, _decode_call, shapes
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build()
+
+
+def test_slab_bytes():
+    assert [B.pa_page_slab_bytes(128, t) for t in range(4)] == [16384, 8192, 16384, 4608]
+    assert [B.pa_page_slab_bytes(64, t) for t in range(4)] == [8192, 4096, 8192, 2304]
+    assert B.pa_page_slab_bytes(96, 3) == 0 and B.pa_page_slab_bytes(128, 4) == 0
+
+
+def test_plan_uses_three_ctas_per_sm_by_default():
+    lens = np.array([10, 3000, 0, 777], np.int32)
+    for cps, want in ((0, 3), (1, 1), (5, 5)):
+        meta, plan = B.pa_get_metadata(lens, None, shapes(4, sms=7, cps=cps, kv=B.PA_KV_FP4_E2M1))
+        assert plan.ctas_per_sm == want and meta.tolist() == S.schedule(lens.tolist(), 8, 7, want, 0)
+    assert B.pa_get_static_plan(shapes(4, cps=0, kv=B.PA_KV_FP4_E2M1)).ctas_per_sm == 3
+    assert B.pa_get_static_plan(shapes(4, cps=0)).ctas_per_sm == 1
+
+
+@pytest.mark.parametrize("over,status,needle", [
+    ({}, B.PA_ERR_INVALID_ARG, "k_scale"),
+    ({"k_scale": _Fake()}, B.PA_ERR_INVALID_ARG, "4-bit"),
+    ({"k_scale": _Fake(), "v_scale": _Fake(), "k_pool": _Fake(addr=(1 << 20) + 8)}, B.PA_ERR_INVALID_ARG, "aligned"),
+])
+def test_decode_refusals(over, status, needle):
+    sh = shapes(2, kv=B.PA_KV_FP4_E2M1)
+    _, plan = B.pa_get_metadata(np.array([100, 300], np.int32), None, sh)
+    with pytest.raises(B.PaError) as e:
+        _decode_call(sh, plan, **over)
+    assert e.value.status == status and needle in str(e.value)
+
+
+def test_unknown_page_type_is_refused():
+    sh = shapes(2, kv=4)
+    _, plan = B.pa_get_metadata(np.array([100, 300], np.int32), None, sh)
+    with pytest.raises(B.PaError, match="kv_dtype"):
+        _decode_call(sh, plan)
+
+
+def test_mixed_batches_refuse_4_bit_pools():
+    sh = B.pa_mixed_shapes(batch=1, num_q_heads=8, num_kv_heads=8, head_dim=128, page_size=64, max_pages_per_seq=4,
+                           num_pool_pages=9, kv_dtype=B.PA_KV_FP4_E2M1, num_sms=152, ctas_per_sm=0, forced_splits=0)
+    with pytest.raises(B.PaError) as e:
+        B.pa_get_mixed_plan(np.array([0, 1], np.int32), np.array([5], np.int32), None, sh)
+    assert e.value.status == B.PA_ERR_UNSUPPORTED
+
+
+def cache_call(name, sh, **over):
+    f = _Fake()
+    a = dict(k_rows=f, v_rows=f, cu=f, start=f, table=f, k_pool=f, v_pool=f, k_scale=f, v_scale=f, ws=f)
+    a.update(over)
+    if name == "append":
+        B.pa_append_kv(sh, a["k_rows"], a["v_rows"], a["cu"], a["start"], a["table"], a["k_pool"], a["v_pool"],
+                       a["k_scale"], a["v_scale"], a["ws"], stream=1)
+    else:
+        B.pa_gather_kv(sh, a["k_pool"], a["v_pool"], a["k_scale"], a["v_scale"], a["cu"], a["start"], a["table"],
+                       a["k_rows"], a["v_rows"], a["ws"], stream=1)
+
+
+@pytest.mark.parametrize("name", ["append", "gather"])
+@pytest.mark.parametrize("change,over,status,needle", [
+    ({"kv_dtype": 4}, {}, B.PA_ERR_INVALID_ARG, "kv_dtype"),
+    ({"head_dim": 96}, {}, B.PA_ERR_UNSUPPORTED, "head_dim"),
+    ({"page_size": 16}, {}, B.PA_ERR_INVALID_ARG, "page_size"),
+    ({"num_kv_heads": 0}, {}, B.PA_ERR_INVALID_ARG, "num_kv_heads"),
+    ({"num_pool_pages": 0}, {}, B.PA_ERR_INVALID_ARG, "num_pool_pages"),
+    ({"total_new": -1}, {}, B.PA_ERR_INVALID_ARG, "total_new"),
+    ({}, {"k_scale": None}, B.PA_ERR_INVALID_ARG, "4-bit"),
+    ({"kv_dtype": 1}, {"v_scale": None}, B.PA_ERR_INVALID_ARG, "e4m3"),
+    ({}, {"table": None}, B.PA_ERR_INVALID_ARG, "NULL"),
+    ({}, {"v_rows": _Fake(addr=(1 << 20) + 2)}, B.PA_ERR_INVALID_ARG, "aligned"),
+    ({}, {"ws": _Fake(n=100)}, B.PA_ERR_WORKSPACE, "workspace"),
+])
+def test_cache_refusals(name, change, over, status, needle):
+    sh = ops.append_shapes(2, 4, 128, 4, 9, 10, "fp4")
+    for k, v in change.items():
+        setattr(sh, k, v)
+    with pytest.raises(B.PaError) as e:
+        cache_call(name, sh, **over)
+    assert e.value.status == status and needle in str(e.value)
+
+
+def test_empty_cache_calls_do_nothing():
+    for name in ("append", "gather"):
+        cache_call(name, ops.append_shapes(0, 4, 128, 4, 9, 10, "fp4"), k_rows=None)
+        cache_call(name, ops.append_shapes(3, 4, 128, 4, 9, 0, "fp4"), k_rows=None)
+
+
+def rope(**change):
+    sh = B.pa_rope_shapes(total_tokens=3, num_q_heads=8, num_kv_heads=2, head_dim=128, rope_dim=128, interleaved=0,
+                          num_axes=2, max_position=100, dtype=B.PA_KV_BF16, norm=1, eps=1e-6, q_stride=1536,
+                          k_stride=1536, v_stride=1536, q_out_stride=1024, k_out_stride=256)
+    sh.sections[0], sh.sections[1] = 40, 24
+    for k, v in change.items():
+        if k == "sections":
+            for i in range(3):
+                sh.sections[i] = v[i]
+        else:
+            setattr(sh, k, v)
+    return sh
+
+
+def rope_call(sh, **over):
+    f = _Fake()
+    a = dict(q=f, k=f, qw=None, kw=None, pos=f, cs=f, qo=f, ko=f, ws=f)
+    a.update(over)
+    B.pa_qk_norm_rope(sh, *(a[n] for n in ("q", "k", "qw", "kw", "pos", "cs", "qo", "ko", "ws")), stream=1)
+
+
+ROPE_REFUSALS = [
+    ({"head_dim": 96}, {}, B.PA_ERR_UNSUPPORTED, "head_dim"),
+    ({"dtype": 1}, {}, B.PA_ERR_INVALID_ARG, "dtype"),
+    ({"rope_dim": 130}, {}, B.PA_ERR_INVALID_ARG, "rope_dim"),
+    ({"rope_dim": 60}, {}, B.PA_ERR_INVALID_ARG, "rope_dim"),
+    ({"num_axes": 4}, {}, B.PA_ERR_INVALID_ARG, "num_axes"),
+    ({"sections": (40, 23, 0)}, {}, B.PA_ERR_INVALID_ARG, "pairs"),
+    ({"sections": (40, 20, 4)}, {}, B.PA_ERR_INVALID_ARG, "sections[2]"),
+    ({"sections": (65, -1, 0)}, {}, B.PA_ERR_INVALID_ARG, "sections[1]"),
+    ({"max_position": 0}, {}, B.PA_ERR_INVALID_ARG, "max_position"),
+    ({"norm": 2}, {}, B.PA_ERR_INVALID_ARG, "norm"),
+    ({"eps": -1.0}, {}, B.PA_ERR_INVALID_ARG, "eps"),
+    ({"eps": float("nan")}, {}, B.PA_ERR_INVALID_ARG, "eps"),
+    ({"q_stride": 1000}, {}, B.PA_ERR_INVALID_ARG, "q_stride"),
+    ({"q_stride": 1540}, {}, B.PA_ERR_INVALID_ARG, "q_stride"),
+    ({"num_q_heads": 0, "num_kv_heads": 0}, {}, B.PA_ERR_INVALID_ARG, "num_q_heads"),
+    ({"total_tokens": -1}, {}, B.PA_ERR_INVALID_ARG, "total_tokens"),
+    ({}, {"q": None}, B.PA_ERR_INVALID_ARG, "NULL"),
+    ({}, {"cs": None}, B.PA_ERR_INVALID_ARG, "NULL"),
+    ({}, {"kw": _Fake(addr=(1 << 20) + 4)}, B.PA_ERR_INVALID_ARG, "aligned"),
+    ({}, {"ws": _Fake(n=8)}, B.PA_ERR_WORKSPACE, "workspace"),
+]
+
+
+@pytest.mark.parametrize("change,over,status,needle", ROPE_REFUSALS + [
+    ({"k_out_stride": 8}, {}, B.PA_ERR_INVALID_ARG, "k_out_stride"),
+    ({}, {"pos": None}, B.PA_ERR_INVALID_ARG, "NULL"),
+    ({}, {"ko": None}, B.PA_ERR_INVALID_ARG, "NULL"),
+    ({}, {"ko": _Fake(addr=(1 << 20) + 4)}, B.PA_ERR_INVALID_ARG, "aligned"),
+])
+def test_norm_rope_refusals(change, over, status, needle):
+    with pytest.raises(B.PaError) as e:
+        rope_call(rope(**change), **over)
+    assert e.value.status == status and needle in str(e.value)
+
+
+def fused_call(sh, ap, **over):
+    f = _Fake()
+    a = dict(q=f, k=f, v=f, qw=None, kw=None, pos=f, cs=f, cu=f, start=f, table=f, qo=f, kp=f, vp=f, ks=None, vs=None, ws=f)
+    a.update(over)
+    B.pa_norm_rope_append_kv(sh, ap, *a.values(), stream=1)
+
+
+@pytest.mark.parametrize("change,over,status,needle", ROPE_REFUSALS[1:-6] + [
+    ({"v_stride": 8}, {}, B.PA_ERR_INVALID_ARG, "v_stride"),
+    ({"head_dim": 64}, {}, B.PA_ERR_INVALID_ARG, "differ"),
+    ({"total_tokens": 4}, {}, B.PA_ERR_INVALID_ARG, "differ"),
+    ({"num_kv_heads": 1}, {}, B.PA_ERR_INVALID_ARG, "differ"),
+    ({"dtype": B.PA_KV_FP16}, {}, B.PA_ERR_INVALID_ARG, "fp16 pools"),
+    ({}, {"v": None}, B.PA_ERR_INVALID_ARG, "NULL"),
+    ({}, {"kp": _Fake(addr=(1 << 20) + 8)}, B.PA_ERR_INVALID_ARG, "aligned"),
+])
+def test_norm_rope_append_refusals(change, over, status, needle):
+    if "num_q_heads" in change:
+        pytest.skip("the two shapes differ first")
+    with pytest.raises(B.PaError) as e:
+        fused_call(rope(**change), ops.append_shapes(2, 2, 128, 4, 9, 3), **over)
+    assert e.value.status == status and needle in str(e.value)
+
+
+def test_norm_rope_append_needs_scales_and_a_cache_head_dim():
+    with pytest.raises(B.PaError, match="4-bit"):
+        fused_call(rope(), ops.append_shapes(2, 2, 128, 4, 9, 3, "fp4"))
+    with pytest.raises(B.PaError, match="head_dim"):
+        fused_call(rope(head_dim=256, q_stride=4096, k_stride=4096, v_stride=4096, q_out_stride=4096),
+                   ops.append_shapes(2, 2, 256, 4, 9, 3))
+
+
+def test_python_shapes():
+    qkv = torch.zeros((5, 12 * 64), dtype=torch.bfloat16)
+    q, k, v = (x.unflatten(-1, (-1, 64)) for x in qkv.split([8 * 64, 2 * 64, 2 * 64], -1))
+    sh = ops.rope_shapes(q, k, v, rope_dim=32, max_position=7, sections=[6, 6, 4])
+    assert (sh.q_stride, sh.k_stride, sh.v_stride, sh.q_out_stride, sh.k_out_stride) == (768, 768, 768, 512, 128)
+    assert list(sh.sections) == [6, 6, 4] and sh.num_axes == 3
+    with pytest.raises(ValueError, match="k"):
+        ops.rope_shapes(q, k.transpose(1, 2).contiguous().transpose(1, 2), rope_dim=0)
+    with pytest.raises(ValueError, match="v"):
+        ops.rope_shapes(q, k, v.float(), rope_dim=0)
+    t = ops.rope_table(10, 8, theta=100.0, device="cpu")
+    assert t.shape == (10, 8) and torch.allclose(t[3, 1], torch.tensor(3 * 100 ** -0.25).cos())
