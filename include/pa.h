@@ -82,7 +82,8 @@ typedef struct {
     int32_t num_pool_pages;    /* pages in k_pool / v_pool */
     int32_t kv_dtype;          /* pa_kv_dtype */
     int32_t num_sms;           /* SMs of the device (cudaDevAttrMultiProcessorCount) */
-    int32_t ctas_per_sm;       /* persistent decode CTAs per SM; 0 = library default (1; 3 with 4-bit pages) */
+    int32_t ctas_per_sm;       /* persistent decode CTAs per SM; 0 = library default (1; 4-bit pages:
+                                  3, or 2 where Hq / Hk > 8) */
     int32_t forced_splits;     /* split-KV count per sequence; 0 = choose automatically */
 } pa_decode_shapes;
 

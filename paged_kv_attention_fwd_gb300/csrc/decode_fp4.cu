@@ -6,33 +6,41 @@
 // has about 100 cycles for 16 keys (K and V, D = 128): 4096 elements to turn
 // into fp16.  That conversion, not the products, is what the kernel is built
 // around.  It runs in registers, straight into the fragments of
-// mma.m16n8k16: measured per SM and cycle, 64 lanes of e2m1x2 -> f16x2
-// conversion, 64 of byte permutes, 64 of f16x2 products and half an MMA, so
-// 16 keys need about 50 (conversions and permutes), 32 (scale products) and
-// 32 (MMA, up to 8 heads) cycles on three different pipes.  Converting into
-// shared memory for tcgen05 instead would write and read back 2 bytes per
-// element, 4 times what the page itself takes, through a port of 128 bytes
-// per cycle.
+// mma.m16n8k16: measured per SM and cycle, 2 warp-wide e2m1x2 -> f16x2
+// conversions, byte permutes or other integer operations in all, 2 f16x2
+// products and half an MMA.  Converting into shared memory for tcgen05 instead
+// would write and read back 2 bytes per element, 4 times what the page itself
+// takes, through a port of 128 bytes per cycle.
 //
 // Keys are the M dimension of S^T and dims that of O^T, so a page element is
 // always an A operand (256 elements per MMA, where it would be 128 as a B
-// operand) and up to 8 query heads of a KV group fill N = 8 (two tiles up to
-// 16 heads).  The order of the dims within a product and of the keys within
-// a 16-key block is free, and chosen so that a lane's share is contiguous:
+// operand), and query heads fill N = 8.  The order of the dims within a
+// product and of the keys within a 16-key block is free, and chosen so that a
+// lane's share is contiguous:
 //   K   lane (g, t) of row g takes dims [t D/4, (t + 1) D/4): one or two
 //       scale blocks, one load per row;
 //   V   lane (g, t) takes dims [g D/8, (g + 1) D/8) of 4 keys: inside one
 //       scale block, one load per key.
+// A byte of V converts to two dims of one key, where an A operand wants two
+// keys of one dim side by side.  Up to 8 heads the products are arranged
+// around that instead of permuting: the contraction runs over (key, parity of
+// the dim) with P^T holding, for each head, one column with zeros at odd dims
+// and one with zeros at even ones.  That doubles the columns: with up to 4
+// heads they fill the 8 there are, with up to 8 it costs 8 more MMAs per 16
+// keys and saves 32 permutes; past 8 heads the MMAs would bound, and the
+// halves are permuted.
+//
 // code * scale is exact in fp16, so nothing is lost before the fp32
 // accumulators; P is rounded to fp16 (relative 2^-12) and q, scaled by a
 // power of two per head, is exact but for elements 2^14 below its largest.
 //
-// Each warp streams its own pages (every fourth of the item's) through its
-// own ring of whole-slab bulk copies and keeps its own running maximum, sum
-// and output, so warps meet only at the end of an item, where the four
-// results are merged through the warps' free page buffers.  Splits of one
-// sequence are merged by the last CTA to finish one (pa_decode) or by
-// combine_kernel.  Every wait is bounded.
+// A producer warp streams page pairs (whole-slab bulk copies, with the query
+// rows in front of an item's first pair) through a ring; four warps take 32
+// keys of a pair each, with a running maximum, sum and output of their own,
+// and meet only at the end of an item, where the four results are merged
+// through a buffer outside the ring while the next item's pages already land.
+// Splits of one sequence are merged by a second, small kernel.  Every wait is
+// bounded.
 #include <cstdint>
 
 #include "fp4.cuh"
@@ -43,21 +51,27 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 4;                    // that compute; one more fills the ring
+constexpr int kCompute = kWarps * 32;
+constexpr int kThreads = kCompute + 32;
 constexpr int kItems = 64;  // items of a CTA decoded once, in the prologue
 constexpr float kLn2 = 0.69314718055994531f;
 // The running maximum is only raised when a logit (in bits) exceeds it by more
 // than this: P then reaches 2^8 in fp16, and most steps rescale nothing.
 constexpr float kSlack = 8.f;
+constexpr float kNone = -3e38f;  // the running maximum before any key: finite, so that its differences are
 
-template <int D>
+// D: head dim; NH: query heads of a KV group it has room for (4, 8 or 16)
+template <int D, int NH>
 struct Layout {
     static constexpr int kSlab = fp4_slab_bytes(D);
-    static constexpr int kStage = 2 * kSlab;  // K slab, V slab
-    static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr int kBytes = kWarps * kStages * kStage;
-    static_assert(16 * D * 4 <= kStage, "a warp's output (16 heads) must fit a page buffer");
+    static constexpr int kQ = 4 * kSlab;  // a stage: K, V of two pages, then query rows
+    static constexpr int kStage = kQ + NH * D * 2;
+    static constexpr int kCtas = NH == 16 ? 2 : kFp4CtasPerSm;
+    static constexpr int kStages = (NH == 16 ? 4 : 3) * (D == 128 ? 1 : 2);
+    static constexpr int kMergeHeads = NH * D <= 512 ? NH : 512 / D;  // heads merged at a time
+    static constexpr int kMerge = kStages * kStage;
+    static constexpr int kBytes = kMerge + kWarps * kMergeHeads * D * 4;
 };
 
 struct Item {
@@ -104,6 +118,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same with C = 0
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -142,194 +166,231 @@ __device__ __forceinline__ uint16_t to_bf16(float x) { return __bfloat16_as_usho
 // 128-byte line of shared memory.
 __device__ __forceinline__ int key_row(int k) { return k ^ ((k >> 1) & 1); }
 
-// D: head dim; NT: 8-head tiles of the group
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 3) decode_fp4_kernel(const __grid_constant__ DecodeArgs a) {
-    using L = Layout<D>;
+// Barrier `id` over `nthreads` threads that also ORs a flag across them.
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred), "r"(id), "r"(nthreads)
+        : "memory");
+    return r != 0;
+}
+
+// The ring's consumer and producer sides step through the stages alike.
+template <int S>
+struct Cursor {
+    uint32_t st = 0, phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++st == S) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <int D, int NH>
+__global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas)
+    decode_fp4_kernel(const __grid_constant__ DecodeArgs a) {
+    using L = Layout<D, NH>;
     constexpr int S = L::kStages;
-    constexpr int KK = D / 16;             // MMA steps over the dims of QK; dim tiles of PV
-    constexpr int KB = NT == 1 ? 4 : 2;    // 16-key blocks per softmax step
-    constexpr int kWords = D / 32;         // 32-bit code words of a lane's share of a K row
+    constexpr int KK = D / 16;                          // MMA steps over the dims of QK
+    constexpr int NQ = NH == 16 ? 2 : 1;                // column tiles of S^T
+    constexpr int NP = NH == 4 ? 1 : 2;                 // column tiles of O^T
+    constexpr int MT = NH == 16 ? D / 16 : D / 32;      // row tiles of O^T
+    constexpr int HL = NH / 4;                          // heads whose logits a lane holds
+    constexpr int M4 = D / 32;                          // groups of 4 dims of a lane's output
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[kWarps][S];
+    __shared__ __align__(8) uint64_t full[S], empty[S];
     __shared__ Item items_sh[kItems];
-    __shared__ float red_m[kWarps][NT * 8], red_l[kWarps][NT * 8];
-    __shared__ int abort_store, merge_now;
-    __shared__ int scratch_at[kWarps];  // the page buffer that holds each warp's output
+    __shared__ float red_m[kWarps][NH], red_l[kWarps][NH];
+    __shared__ int live_sh[S][2];  // live keys of the two pages (64: all; 0: no such page, or its id is out of range)
+    __shared__ int abort_store;
     volatile int* abort_sh = &abort_store;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint8_t* ring = smem + warp * (S * L::kStage);
-    uint64_t* bar = full[warp];
-    if (lane < S) mbar_init(&bar[lane], 1);
-    if (threadIdx.x == 0) {
-        abort_store = 0;
-        merge_now = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < S) {
+        mbar_init(&full[threadIdx.x], 1);
+        mbar_init(&empty[threadIdx.x], kWarps);
     }
+    if (threadIdx.x == 0) abort_store = 0;
     fence_barrier_init();
     grid_dependency_wait();  // shared memory only up to here
+    // The merge kernel may become resident as this one's CTAs leave.  Nothing
+    // else may: a later decode let in early is dealt to the SMs in the order
+    // they empty, which undoes the schedule's balance (64 sequences, no
+    // splits: 53 us a call against 43).
+    if (a.counters) allow_dependents_launch();
 
-    const int items_off = kMetaHeader + 2 * a.batch + 1 + __ldg(&a.meta[5]) + 1;
-    int it_lo = 0, it_hi = 0;
-    if ((int)blockIdx.x < __ldg(&a.meta[5])) {
-        it_lo = __ldg(&a.meta[kMetaHeader + 2 * a.batch + 1 + blockIdx.x]);
-        it_hi = __ldg(&a.meta[kMetaHeader + 2 * a.batch + 1 + blockIdx.x + 1]);
-    }
+    const int32_t* indptr = a.meta + kMetaHeader + 2 * a.batch + 1;
+    const int grid = __ldg(&a.meta[5]);  // at most gridDim.x
+    int it_lo = __ldg(&indptr[blockIdx.x]), it_hi = __ldg(&indptr[blockIdx.x + 1]);
+    if ((int)blockIdx.x >= grid) it_lo = it_hi = 0;
+    const int items_off = kMetaHeader + 2 * a.batch + 1 + grid + 1;
     for (int i = threadIdx.x; i < min(it_hi - it_lo, kItems); i += kThreads) items_sh[i] = load_item(a, it_lo + i, items_off);
     __syncthreads();
     auto get_item = [&](int j) { return j - it_lo < kItems ? items_sh[j - it_lo] : load_item(a, j, items_off); };
+    Cursor<S> at;
 
-    // ---- producer side of this warp's ring
-    int pj = it_lo, pp = 0, pend = 0, pkvh = 0, id_base = 0, ids = 0;
-    long long bt_row = 0;
-    bool pdone = false;
-    uint32_t issued = 0, consumed = 0;  // pages handed to / taken from the ring
-    uint32_t dead = 0;                  // stages whose page id was out of range
-    auto load_ids = [&]() {  // the ids of this warp's next 32 pages
-        id_base = pp;
-        const int i = pp + kWarps * lane;
-        ids = i < pend ? __ldg(&a.block_table[bt_row + i]) : 0;
-    };
-    auto open_item = [&]() {
-        while (pp >= pend) {
-            if (pj >= it_hi) {
-                pdone = true;
-                return;
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ producer
+        bool ok = true;
+        uint32_t issued = 0;
+        for (int j = it_lo; j < it_hi && ok; ++j) {
+            const Item it = get_item(j);
+            const long long bt_row = (long long)it.b * a.max_pages;
+            const int key_end = min(it.seq_len, it.p1 * kPage);
+            int ids = 0;
+            for (int p = it.p0; p < it.p1; p += 2) {
+                const int k = (p - it.p0) & 31;
+                if (k == 0) ids = p + lane < it.p1 ? __ldg(&a.block_table[bt_row + p + lane]) : 0;
+                const int id0 = __shfl_sync(0xffffffffu, ids, k), id1 = __shfl_sync(0xffffffffu, ids, k + 1);
+                if (lane == 0) {
+                    ok = mbar_wait(&empty[at.st], at.phase ^ 1, abort_sh, a.wait_ns);
+                    if (ok) {
+                        const bool two = p + 1 < it.p1;
+                        const bool good0 = (unsigned)id0 < (unsigned)a.num_pool_pages;
+                        const bool good1 = two && (unsigned)id1 < (unsigned)a.num_pool_pages;
+                        const uint32_t qbytes = p == it.p0 ? (uint32_t)a.group * D * 2u : 0u;
+                        if (!good0 || (two && !good1)) record(a.status, PA_ERR_DEVICE_BOUNDS);
+                        live_sh[at.st][0] = good0 ? min(key_end - p * kPage, kPage) : 0;
+                        live_sh[at.st][1] = good1 ? min(key_end - (p + 1) * kPage, kPage) : 0;
+                        uint64_t* bar = &full[at.st];
+                        uint8_t* dst = smem + at.st * L::kStage;
+                        mbar_arrive_expect_tx(bar, ((good0 ? 2u : 0u) + (good1 ? 2u : 0u)) * L::kSlab + qbytes);
+                        if (qbytes)
+                            bulk_load(dst + L::kQ, a.q + ((long long)it.b * a.num_q_heads + it.kvh * a.group) * D, qbytes, bar);
+                        if (good0) {
+                            const long long off = ((long long)id0 * a.num_kv_heads + it.kvh) * L::kSlab;
+                            bulk_load(dst, a.k_pool + off, L::kSlab, bar);
+                            bulk_load(dst + L::kSlab, a.v_pool + off, L::kSlab, bar);
+                        }
+                        if (good1) {
+                            const long long off = ((long long)id1 * a.num_kv_heads + it.kvh) * L::kSlab;
+                            bulk_load(dst + 2 * L::kSlab, a.k_pool + off, L::kSlab, bar);
+                            bulk_load(dst + 3 * L::kSlab, a.v_pool + off, L::kSlab, bar);
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                if (!ok) break;
+                ++issued;
+                at.step();
             }
-            const Item it = get_item(pj++);
-            pp = it.p0 + warp;
-            pend = it.p1;
-            pkvh = it.kvh;
-            bt_row = (long long)it.b * a.max_pages;
-            if (pp < pend) load_ids();
         }
-    };
-    auto issue = [&]() {  // the warp's next page into the next stage, which is free
-        if (!pdone) open_item();
-        if (pdone) return;
-        if (pp - id_base >= 32 * kWarps) load_ids();
-        const int id = __shfl_sync(0xffffffffu, ids, (pp - id_base) / kWarps);
-        const uint32_t st = issued % S;
-        const bool ok = (unsigned)id < (unsigned)a.num_pool_pages;
-        dead = ok ? dead & ~(1u << st) : dead | (1u << st);
         if (lane == 0) {
-            if (ok) {
-                const long long off = ((long long)id * a.num_kv_heads + pkvh) * L::kSlab;
-                mbar_arrive_expect_tx(&bar[st], 2 * L::kSlab);
-                bulk_load(ring + st * L::kStage, a.k_pool + off, L::kSlab, &bar[st]);
-                bulk_load(ring + st * L::kStage + L::kSlab, a.v_pool + off, L::kSlab, &bar[st]);
-            } else {
-                record(a.status, PA_ERR_DEVICE_BOUNDS);
-                mbar_arrive(&bar[st]);
+            if (!ok) {
+                *abort_sh = 1;
+                record(a.status, PA_ERR_TIMEOUT);
             }
+            // every copy must land before the CTA may exit; the consumers have seen to it unless they gave up
+            const uint32_t last = issued < (uint32_t)S ? issued : (uint32_t)S;
+            for (uint32_t i = issued - last; i < issued; ++i) mbar_wait(&full[i % S], (i / S) & 1, nullptr, a.wait_ns);
         }
-        ++issued;
-        pp += kWarps;
-    };
-#pragma unroll 1
-    for (int i = 0; i < S; ++i) issue();
+        return;
+    }
 
-    const int G = a.group;
+    // ---------------------------------------------------------------- consumers
+    const int g = lane >> 2, t = lane & 3, G = a.group;
+    float* merge = reinterpret_cast<float*>(smem + L::kMerge);
+    // this lane's places in a slab, for the first 16-key block of the warp: K row, V keys
+    const int row0 = (warp & 1) * 32;
+    const int krow = row0 + key_row(g), vkey0 = row0 + key_row(2 * t), vkey1 = row0 + key_row(2 * t + 1);
+    const uint8_t* kbase = smem + (warp >> 1) * (2 * L::kSlab) + krow * (D / 2) + t * (D / 8);
+    const uint8_t* kscale = smem + (warp >> 1) * (2 * L::kSlab) + kPage * (D / 2) + krow * (D / 16) + (D == 128 ? 2 * t : t);
+    const uint8_t* vslab = smem + (warp >> 1) * (2 * L::kSlab) + L::kSlab;
+    // halves of a P pair (keys 2t, 2t + 1) with a zero beside them
+    const uint32_t sel0 = NH == 4 && (g & 1) ? 0x1044u : 0x4410u, sel1 = NH == 4 && (g & 1) ? 0x3244u : 0x4432u;
+
     bool bad = false;
     for (int j = it_lo; j < it_hi; ++j) {
         const Item it = get_item(j);
-        const int key_end = min(it.seq_len, it.p1 * kPage);
-
-        // ---- the group's queries as B fragments: head g (and 8 + g), dims [t D/4, (t + 1) D/4)
-        uint32_t q[NT][2 * KK];
-        float sl2[NT][2];
-        const float base_scale = a.scale_log2 * __ldg(&a.k_scale[it.kvh]);
+        const float k_scale = __ldg(&a.k_scale[it.kvh]), vs = __ldg(&a.v_scale[it.kvh]);
+        // logits in bits are products times |bits|: its sign goes into q, so that maxima can be taken of the products
+        const float bits = fabsf(a.scale_log2 * k_scale);
+        const uint32_t sign = __float_as_uint(a.scale_log2 * k_scale) & 0x80000000u;
+        uint32_t q[NQ][2 * KK];
+        float sl2[HL], o[NP][MT][4], m[HL], l[HL];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            uint4 raw[D / 32];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-            if (n * 8 + g < G) {
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    a.q + ((long long)it.b * a.num_q_heads + it.kvh * G + n * 8 + g) * D + t * (D / 4));
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) raw[i] = __ldg(src + i);
-            }
-            float amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // 2^e <= amax < 2^(e+1), kept where both 2^e and 2^-e are ordinary floats
-            const int e = amax > 0.f && amax < INFINITY ? min(max((int)(__float_as_uint(amax) >> 23) - 127, -96), 96) : 0;
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    q[n][4 * i + k] =
-                        pack_half2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
-            }
-            // head 2t + i of the tile: its power of two sits in lane 4 (2t + i)
-            sl2[n][0] = base_scale * __shfl_sync(0xffffffffu, up, 8 * t);
-            sl2[n][1] = base_scale * __shfl_sync(0xffffffffu, up, 8 * t + 4);
+        for (int i = 0; i < HL; ++i) {
+            m[i] = kNone;
+            l[i] = 0.f;
         }
-
-        float o[NT][KK][4], m[NT][2], l[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.f;
+        for (int n = 0; n < NP; ++n)
 #pragma unroll
-            for (int i = 0; i < KK; ++i)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[n][i][k] = 0.f;
+
+        if (it.p0 < it.p1) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[at.st], at.phase, abort_sh, a.wait_ns))) bad = true;
+            const uint32_t so = at.st * L::kStage;
+            // ---- the group's queries as B fragments: dims [t D/4, (t + 1) D/4) of the head of column g
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                const int h = NH == 4 ? g >> 1 : n * 8 + g;
+                const uint4* src = reinterpret_cast<const uint4*>(smem + so + L::kQ + h * (D * 2) + t * (D / 2));
+                uint32_t raw[D / 8];
+                float amax = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 v = h < G ? src[i] : make_uint4(0, 0, 0, 0);
+                    raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[i] << 16)), fabsf(__uint_as_float(raw[i] & 0xFFFF0000u))));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // 2^e <= amax < 2^(e+1), kept where both 2^e and 2^-e are ordinary floats
+                const int e = amax > 0.f && amax < INFINITY ? min(max((int)(__float_as_uint(amax) >> 23) - 127, -96), 96) : 0;
+                const float down = __uint_as_float(((uint32_t)(127 - e) << 23) | sign), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    q[n][i] = pack_half2(__uint_as_float(raw[i] << 16) * down, __uint_as_float(raw[i] & 0xFFFF0000u) * down);
+                // the power of two of each head whose logits this lane holds
+                if constexpr (NH == 4) {
+                    sl2[0] = bits * __shfl_sync(0xffffffffu, up, 8 * t);
+                } else {
+                    sl2[2 * n] = bits * __shfl_sync(0xffffffffu, up, 8 * t);
+                    sl2[2 * n + 1] = bits * __shfl_sync(0xffffffffu, up, 8 * t + 4);
+                }
+            }
         }
 
-        bool owed = false;  // the last page's stage is refilled after the merge
-        uint8_t* scratch = ring;
-        for (int p = it.p0 + warp; p < it.p1 && !bad; p += kWarps) {
-            const uint32_t st = consumed % S;
-            const bool landed = mbar_wait(&bar[st], (consumed / S) & 1, abort_sh, a.wait_ns);
-            if (!__all_sync(0xffffffffu, landed)) {
+        for (int p = it.p0; p < it.p1 && !bad; p += 2) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[at.st], at.phase, abort_sh, a.wait_ns))) {
                 bad = true;
                 break;
             }
-            ++consumed;
-            const uint8_t* kc = ring + st * L::kStage;
-            const uint8_t* vc = kc + L::kSlab;
-            const int live = (dead >> st) & 1u ? 0 : min(key_end - p * kPage, kPage);  // keys of this page
-#pragma unroll
-            for (int step = 0; step < 4 / KB; ++step) {
-                const int r0 = step * KB * 16;
-                if (r0 >= live) break;
+            const uint32_t so = at.st * L::kStage;
+            const int live = live_sh[at.st][warp >> 1] - row0;  // live keys among this warp's 32 (32 or more: all)
+            if (live > 0) {
                 // ---- S^T = K q^T
-                float s[NT][KB][4];
+                float c[NQ][2][4];
 #pragma unroll
-                for (int blk = 0; blk < KB; ++blk) {
-                    const int row = r0 + blk * 16 + key_row(g);
-                    uint32_t w[2][kWords], sc[2][kWords / 2];
+                for (int blk = 0; blk < 2; ++blk) {
+                    uint32_t w[2][D / 32], sc[2][D / 64];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint8_t* src = kc + (row + 8 * i) * (D / 2) + t * (D / 8);
-                        const uint8_t* scl = kc + kPage * (D / 2) + (row + 8 * i) * (D / 16);
+                        const uint8_t* src = kbase + so + (blk * 16 + 8 * i) * (D / 2);
+                        const uint8_t* scl = kscale + so + (blk * 16 + 8 * i) * (D / 16);
                         if constexpr (D == 128) {
                             const uint4 v = *reinterpret_cast<const uint4*>(src);
                             w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-                            const uint32_t h = e4m3x2_to_half2(reinterpret_cast<const uint16_t*>(scl)[t]);
+                            const uint32_t h = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(scl));
                             sc[i][0] = __byte_perm(h, 0, 0x1010);
                             sc[i][1] = __byte_perm(h, 0, 0x3232);
                         } else {
                             const uint2 v = *reinterpret_cast<const uint2*>(src);
                             w[i][0] = v.x; w[i][1] = v.y;
-                            sc[i][0] = __byte_perm(e4m3x2_to_half2(scl[t]), 0, 0x1010);
+                            sc[i][0] = __byte_perm(e4m3x2_to_half2(*scl), 0, 0x1010);
                         }
                     }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) s[n][blk][k] = 0.f;
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk) {
                         const int wi = kk / 2, byte = (kk & 1) * 2;
@@ -338,221 +399,295 @@ __global__ void __launch_bounds__(kThreads, 3) decode_fp4_kernel(const __grid_co
                         const uint32_t a2 = mul2(code_pair(w[0][wi], byte + 1), sc[0][wi / 2]);
                         const uint32_t a3 = mul2(code_pair(w[1][wi], byte + 1), sc[1][wi / 2]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(s[n][blk], a0, a1, a2, a3, q[n][2 * kk], q[n][2 * kk + 1]);
+                        for (int n = 0; n < NQ; ++n) {
+                            if (kk == 0) mma16816_first(c[n][blk], a0, a1, a2, a3, q[n][0], q[n][1]);
+                            else mma16816(c[n][blk], a0, a1, a2, a3, q[n][2 * kk], q[n][2 * kk + 1]);
+                        }
                     }
                 }
-                // ---- running softmax, in bits
-                const bool tail = live < r0 + KB * 16;
+                // products x[i][2 blk + r] of head slot i, row 16 blk + 8 r + g
+                float x[HL][4];
+#pragma unroll
+                for (int i = 0; i < HL; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[i][k] = c[NH == 16 ? i >> 1 : 0][k >> 1][2 * (k & 1) + (NH == 4 ? 0 : i & 1)];
+                if (live < 32) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (8 * k + key_row(g) >= live) {
+#pragma unroll
+                            for (int i = 0; i < HL; ++i) x[i][k] = -INFINITY;
+                        }
+                }
+                // ---- running softmax: lanes share a maximum only when one of them finds it too low
                 bool raise = false;
-                float mx[NT][2];
+                float top[HL];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int i = 0; i < HL; ++i) {
+                    top[i] = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])) * sl2[i];
+                    raise |= top[i] > m[i] + kSlack;
+                }
+                if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float v = -INFINITY;
-#pragma unroll
-                        for (int blk = 0; blk < KB; ++blk)
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                float& x = s[n][blk][2 * r + i];
-                                x *= sl2[n][i];
-                                if (tail && r0 + blk * 16 + 8 * r + key_row(g) >= live) x = -INFINITY;
-                                v = fmaxf(v, x);
-                            }
+                    for (int i = 0; i < HL; ++i) {
+                        float v = top[i];
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        mx[n][i] = v;
-                        raise |= v > m[n][i] + kSlack || (m[n][i] == -INFINITY && v > -INFINITY);
+                        const float mn = fmaxf(m[i], v);
+                        const float alpha = ex2(m[i] - mn);
+                        m[i] = mn;
+                        l[i] *= alpha;
+#pragma unroll
+                        for (int n = 0; n < NP; ++n)
+#pragma unroll
+                            for (int k = 0; k < MT; ++k)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (NH == 4 || (NH == 8 && (e & 1) == i) || (NH == 16 && n == i >> 1 && (e & 1) == (i & 1)))
+                                        o[n][k][e] *= alpha;
                     }
-                if (__any_sync(0xffffffffu, raise)) {
+                }
+                float pr[HL][4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                for (int i = 0; i < HL; ++i) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float mn = fmaxf(m[n][i], mx[n][i]);
-                            const float alpha = mn == -INFINITY ? 1.f : ex2(m[n][i] - mn);
-                            m[n][i] = mn;
-                            l[n][i] *= alpha;
+                    for (int k = 0; k < 4; ++k) pr[i][k] = ex2(fmaf(x[i][k], sl2[i], -m[i]));
+                }
+                if (live < 32) {  // whatever -inf times a scale of 0 came to
 #pragma unroll
-                            for (int k = 0; k < KK; ++k) {
-                                o[n][k][i] *= alpha;
-                                o[n][k][2 + i] *= alpha;
-                            }
+                    for (int k = 0; k < 4; ++k)
+                        if (8 * k + key_row(g) >= live) {
+#pragma unroll
+                            for (int i = 0; i < HL; ++i) pr[i][k] = 0.f;
                         }
                 }
-                uint32_t pb[NT][KB][2];  // P as B fragments: head g, keys (2t, 2t + 1) and (2t + 8, 2t + 9)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-#pragma unroll
-                    for (int blk = 0; blk < KB; ++blk)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float p0 = ex2(s[n][blk][2 * r] - m0), p1 = ex2(s[n][blk][2 * r + 1] - m1);
-                            l[n][0] += p0;
-                            l[n][1] += p1;
-                            pb[n][blk][r] = transpose8x8(pack_half2(p0, p1));
-                        }
-                }
+                for (int i = 0; i < HL; ++i) l[i] += (pr[i][0] + pr[i][1]) + (pr[i][2] + pr[i][3]);
                 // ---- O^T += V^T P^T
 #pragma unroll
-                for (int blk = 0; blk < KB; ++blk) {
-                    const int k0 = r0 + blk * 16 + key_row(2 * t), k1 = r0 + blk * 16 + key_row(2 * t + 1);
-                    const int keys[4] = {k0, k1, k0 + 8, k1 + 8};
-                    uint32_t w[4][D / 64], b[4];
+                for (int blk = 0; blk < 2; ++blk) {
+                    uint32_t w[4][D / 64], b[4];  // keys vkey0, vkey1, vkey0 + 8, vkey1 + 8 of the block
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        const int key = (i & 1 ? vkey1 : vkey0) + 8 * (i >> 1) + 16 * blk;
                         if constexpr (D == 128) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(vc + keys[i] * 64 + g * 8);
+                            const uint2 v = *reinterpret_cast<const uint2*>(vslab + so + key * 64 + g * 8);
                             w[i][0] = v.x;
                             w[i][1] = v.y;
-                            b[i] = vc[kPage * 64 + keys[i] * 8 + g];
+                            b[i] = vslab[so + kPage * 64 + key * 8 + g];
                         } else {
-                            w[i][0] = *reinterpret_cast<const uint32_t*>(vc + keys[i] * 32 + g * 4);
-                            b[i] = vc[kPage * 32 + keys[i] * 4 + (g >> 1)];
+                            w[i][0] = *reinterpret_cast<const uint32_t*>(vslab + so + key * 32 + g * 4);
+                            b[i] = vslab[so + kPage * 32 + key * 4 + (g >> 1)];
                         }
-                        // a dead key's scale may be a NaN, which a zero P would not cancel
-                        if (tail && keys[i] >= live) b[i] = 0;
+                    }
+                    if (live < 32) {  // a dead key's scale may be a NaN, which a zero P would not cancel
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((i & 1 ? vkey1 : vkey0) + 8 * (i >> 1) + 16 * blk >= live + row0) b[i] = 0;
                     }
                     const uint32_t s01 = e4m3x2_to_half2(b[0] | (b[1] << 8)), s23 = e4m3x2_to_half2(b[2] | (b[3] << 8));
+                    if constexpr (NH < 16) {
+                        // 8 keys at a time: A = (key, parity), B = P at one parity
 #pragma unroll
-                    for (int mt = 0; mt < KK; ++mt) {
-                        const uint32_t h0 = code_pair(w[0][mt / 4], mt & 3), h1 = code_pair(w[1][mt / 4], mt & 3);
-                        const uint32_t h2 = code_pair(w[2][mt / 4], mt & 3), h3 = code_pair(w[3][mt / 4], mt & 3);
-                        const uint32_t a0 = mul2(__byte_perm(h0, h1, 0x5410), s01);
-                        const uint32_t a1 = mul2(__byte_perm(h0, h1, 0x7632), s01);
-                        const uint32_t a2 = mul2(__byte_perm(h2, h3, 0x5410), s23);
-                        const uint32_t a3 = mul2(__byte_perm(h2, h3, 0x7632), s23);
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int k = 2 * blk + hf;
+                            const uint32_t y = transpose8x8(NH == 4 ? pack_half2(pr[0][k], pr[0][k])
+                                                                    : pack_half2(pr[0][k], pr[HL - 1][k]));
+                            const uint32_t even0 = __byte_perm(y, 0, sel0), even1 = __byte_perm(y, 0, sel1);
+                            const uint32_t odd0 = __byte_perm(y, 0, 0x1044), odd1 = __byte_perm(y, 0, 0x3244);
+                            const uint32_t sh = hf ? s23 : s01;
+                            const uint32_t sa = __byte_perm(sh, 0, 0x1010), sb = __byte_perm(sh, 0, 0x3232);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(o[n][mt], a0, a1, a2, a3, pb[n][blk][0], pb[n][blk][1]);
+                            for (int mt = 0; mt < MT; ++mt) {
+                                const uint32_t wa = w[2 * hf][mt / 2], wb = w[2 * hf + 1][mt / 2];
+                                const int byte = (mt & 1) * 2;
+                                const uint32_t a0 = mul2(code_pair(wa, byte), sa), a1 = mul2(code_pair(wa, byte + 1), sa);
+                                const uint32_t a2 = mul2(code_pair(wb, byte), sb), a3 = mul2(code_pair(wb, byte + 1), sb);
+                                mma16816(o[0][mt], a0, a1, a2, a3, even0, even1);
+                                if constexpr (NH == 8) mma16816(o[NP - 1][mt], a0, a1, a2, a3, odd0, odd1);
+                            }
+                        }
+                    } else {
+                        uint32_t pb[2][2];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                pb[n][r] = transpose8x8(pack_half2(pr[2 * n % HL][2 * blk + r], pr[(2 * n + 1) % HL][2 * blk + r]));
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            const uint32_t h0 = code_pair(w[0][mt / 4], mt & 3), h1 = code_pair(w[1][mt / 4], mt & 3);
+                            const uint32_t h2 = code_pair(w[2][mt / 4], mt & 3), h3 = code_pair(w[3][mt / 4], mt & 3);
+                            const uint32_t a0 = mul2(__byte_perm(h0, h1, 0x5410), s01);
+                            const uint32_t a1 = mul2(__byte_perm(h0, h1, 0x7632), s01);
+                            const uint32_t a2 = mul2(__byte_perm(h2, h3, 0x5410), s23);
+                            const uint32_t a3 = mul2(__byte_perm(h2, h3, 0x7632), s23);
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) mma16816(o[n % NP][mt], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                        }
                     }
                 }
             }
             __syncwarp();  // every lane is done with the stage
-            if (p + kWarps < it.p1) issue();
-            else {
-                owed = true;
-                scratch = ring + st * L::kStage;
-            }
+            if (lane == 0) mbar_arrive(&empty[at.st]);
+            at.step();
         }
 
-        // ---- merge the four warps: maxima and sums, then the outputs through the free page buffers
+        // ---- merge the four warps
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < HL; ++i) {
+            const int h = NH == 4 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int off = 4; off <= 16; off <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], off);
-                if (g == 0) {
-                    red_m[warp][n * 8 + 2 * t + i] = m[n][i];
-                    red_l[warp][n * 8 + 2 * t + i] = l[n][i];
-                }
+            for (int off = 4; off <= 16; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+            if (g == 0) {
+                red_m[warp][h] = m[i];
+                red_l[warp][h] = l[i];
             }
-        if (owed) {
-            float* so = reinterpret_cast<float*>(scratch);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int mt = 0; mt < KK; ++mt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (n * 8 + 2 * t + i < G)
-                            *reinterpret_cast<float2*>(so + (n * 8 + 2 * t + i) * D + g * (D / 8) + 2 * mt) =
-                                make_float2(o[n][mt][i], o[n][mt][2 + i]);
-        }
-        if (lane == 0) scratch_at[warp] = (int)(scratch - smem);
-        if (__syncthreads_or(bad || *abort_sh != 0)) {
-            bad = true;
-            break;
         }
         const bool partial = it.nsplit > 1;
         const long long head0 = (long long)it.kvh * G;
         const long long orow = partial ? (long long)(it.split_base + it.s) * a.num_q_heads + head0
                                        : (long long)it.b * a.num_q_heads + head0;
-        const float vs = __ldg(&a.v_scale[it.kvh]);
-        for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
-            const int h = idx / D, d = idx % D;
-            float mm = -INFINITY, ll = 0.f, val = 0.f;
+        constexpr int HC = L::kMergeHeads;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, red_m[w][h]);
+        for (int ch = 0; ch < NH / HC; ++ch) {  // heads ch HC .. ch HC + HC - 1
+            if (ch * HC >= G) break;
+            // [warp][head][dim], a lane's groups of 4 dims rotated by its t: no two lanes of a store meet in a bank
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float mw = red_m[w][h], lw = red_l[w][h];
-                if (mw == -INFINITY && lw == 0.f) continue;  // no live key: nothing was written
-                const float f = ex2(mw - mm);                // a NaN logit leaves a NaN sum, and so a NaN output
-                ll = fmaf(f, lw, ll);
-                val = fmaf(f, reinterpret_cast<const float*>(smem + scratch_at[w])[h * D + d], val);
-            }
-            val = ll == 0.f ? 0.f : val * (vs / ll);
-            if (partial) a.o_part[(orow + h) * D + d] = val;
-            else a.out[(orow + h) * D + d] = to_bf16(val);
-            if (d == 0) {
-                const float lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-                if (partial) a.lse_part[orow + h] = lse;
-                else if (a.lse) a.lse[orow + h] = lse;
-            }
-        }
-        fence_proxy_async_smem();  // the buffers go back to the async copies
-        if (partial && a.counters) __threadfence();
-        __syncthreads();
-        if (owed) issue();
-        if (partial && a.counters) {
-            // the last split of the sequence to arrive merges them all, in split order:
-            // lse = m + ln sum_s exp(lse_s - m), out = sum_s exp(lse_s - lse) o_s
-            int* ctr = a.counters + (long long)it.b * a.num_kv_heads + it.kvh;
-            if (threadIdx.x == 0) {
-                int prev;
-                asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(prev) : "l"(ctr) : "memory");
-                merge_now = prev == it.nsplit - 1;
-            }
-            __syncthreads();
-            if (merge_now) {
-                __threadfence();
-                const long long base = (long long)it.split_base * a.num_q_heads + head0;
-                const long long row = (long long)it.b * a.num_q_heads + head0;
-                for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
-                    const int h = idx / D, d = idx % D;
-                    float mm = -INFINITY, sum = 0.f, acc = 0.f;
-                    for (int s = 0; s < it.nsplit; ++s) mm = fmaxf(mm, __ldcg(&a.lse_part[base + (long long)s * a.num_q_heads + h]));
-                    for (int s = 0; s < it.nsplit; ++s) {
-                        const long long pr = base + (long long)s * a.num_q_heads + h;
-                        const float ls = __ldcg(&a.lse_part[pr]);
-                        if (ls == -INFINITY) continue;
-                        const float w = __expf(ls - mm);
-                        sum += w;
-                        acc = fmaf(w, __ldcg(&a.o_part[pr * D + d]), acc);
+            for (int i = 0; i < HL; ++i) {
+                const int h = (NH == 4 ? t : 8 * (i >> 1) + 2 * t + (i & 1)) - ch * HC;
+                if (h >= 0 && h < HC) {
+#pragma unroll
+                    for (int k = 0; k < M4; ++k) {
+                        float4 v;
+                        if constexpr (NH == 4) v = make_float4(o[0][k][0], o[0][k][1], o[0][k][2], o[0][k][3]);
+                        else if constexpr (NH == 8)
+                            v = make_float4(o[0][k][i], o[NP - 1][k][i], o[0][k][2 + i], o[NP - 1][k][2 + i]);
+                        else
+                            v = make_float4(o[(i >> 1) % NP][2 * k % MT][i & 1], o[(i >> 1) % NP][2 * k % MT][2 + (i & 1)],
+                                            o[(i >> 1) % NP][(2 * k + 1) % MT][i & 1], o[(i >> 1) % NP][(2 * k + 1) % MT][2 + (i & 1)]);
+                        *reinterpret_cast<float4*>(merge + (warp * HC + h) * D + g * (D / 8) + 4 * ((k + t) & (M4 - 1))) = v;
                     }
-                    a.out[(row + h) * D + d] = to_bf16(sum == 0.f ? 0.f : acc / sum);
-                    if (d == 0 && a.lse) a.lse[row + h] = sum == 0.f ? -INFINITY : mm + __logf(sum);
                 }
-                if (threadIdx.x == 0) *ctr = 0;
             }
+            if (named_bar_or(1, kCompute, bad || *abort_sh != 0)) {
+                bad = true;
+                break;
+            }
+            for (int idx = threadIdx.x; idx < min(HC, G - ch * HC) * D; idx += kCompute) {
+                const int hh = idx / D, d = idx % D, h = ch * HC + hh;
+                const int ht = NH == 4 ? h : (h >> 1) & 3;  // the t of the lanes that held head h
+                const int slot = d / (D / 8) * (D / 8) + 4 * ((d % (D / 8) / 4 + ht) & (M4 - 1)) + (d & 3);
+                float mm = kNone, ll = 0.f, val = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, red_m[w][h]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float mw = red_m[w][h], lw = red_l[w][h];
+                    if (lw == 0.f) continue;       // no live key
+                    const float f = ex2(mw - mm);  // a NaN logit leaves a NaN sum, and so a NaN output
+                    ll = fmaf(f, lw, ll);
+                    val = fmaf(f, merge[(w * HC + hh) * D + slot], val);
+                }
+                val = ll == 0.f ? 0.f : val * (vs / ll);
+                if (partial) a.o_part[(orow + h) * D + d] = val;
+                else a.out[(orow + h) * D + d] = to_bf16(val);
+                if (d == 0) {
+                    const float lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+                    if (partial) a.lse_part[orow + h] = lse;
+                    else if (a.lse) a.lse[orow + h] = lse;
+                }
+            }
+            named_bar_sync(1, kCompute);
         }
+        if (bad) break;
     }
-    if (bad) {
-        if (lane == 0) {
-            *abort_sh = 1;
-            record(a.status, PA_ERR_TIMEOUT);
-            // every issued copy must land before the CTA may exit
-            for (; consumed < issued; ++consumed) mbar_wait(&bar[consumed % S], (consumed / S) & 1, nullptr, a.wait_ns);
-        }
+    if (bad && lane == 0) {
+        *abort_sh = 1;  // the producer stops too
+        record(a.status, PA_ERR_TIMEOUT);
     }
 }
 
-template <int D, int NT>
+// Merges the splits of every sequence that has more than one, in split order:
+//   lse = m + ln sum_s exp(lse_s - m),  out = sum_s exp(lse_s - lse) o_s
+// One warp per (sequence, query head); its loads of all splits are in flight
+// together.  A kernel of its own: merged by the last CTA to finish a split
+// instead, the wait for the partials and two rounds of dependent loads fell
+// into that CTA's stream of pages (64 sequences of up to 4096 keys: 70 us a
+// call, XX this way).
+template <int D>
+__global__ void __launch_bounds__(128) combine_fp4_kernel(const __grid_constant__ DecodeArgs a) {
+    const int w = (int)(blockIdx.x * 4 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const bool any = w < a.batch * a.num_q_heads;
+    const int b = any ? w / a.num_q_heads : 0, h = any ? w % a.num_q_heads : 0;
+    const int n = any ? __ldg(&a.meta[kMetaHeader + b]) : 0;
+    const long long base = (long long)__ldg(&a.meta[kMetaHeader + a.batch + b]) * a.num_q_heads + h;
+    // The metadata was complete before the attention kernel let this one in;
+    // its partials are now.  Every warp waits, also one with nothing to do:
+    // this kernel must not be complete before that one.
+    grid_dependency_wait();
+    if (n <= 1) return;
+    // lanes hold the splits' log-sum-exps (at most PA_MAX_SPLITS = 64)
+    const float l0 = lane < n ? a.lse_part[base + (long long)lane * a.num_q_heads] : -INFINITY;
+    const float l1 = lane + 32 < n ? a.lse_part[base + (long long)(lane + 32) * a.num_q_heads] : -INFINITY;
+    float mm = fmaxf(l0, l1);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    // a split without keys weighs nothing; a NaN stays one
+    const float w0 = l0 == -INFINITY ? 0.f : __expf(l0 - mm), w1 = l1 == -INFINITY ? 0.f : __expf(l1 - mm);
+    float sum = 0.f, acc[D / 32] = {};
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
+        const float* o = a.o_part + (base + (long long)s * a.num_q_heads) * D + lane * (D / 32);
+        sum += ws;
+        if constexpr (D == 128) {
+            const float4 v = *reinterpret_cast<const float4*>(o);
+            acc[0] = fmaf(ws, v.x, acc[0]);
+            acc[1] = fmaf(ws, v.y, acc[1]);
+            acc[2] = fmaf(ws, v.z, acc[2]);
+            acc[3] = fmaf(ws, v.w, acc[3]);
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(o);
+            acc[0] = fmaf(ws, v.x, acc[0]);
+            acc[1] = fmaf(ws, v.y, acc[1]);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long row = (long long)b * a.num_q_heads + h;
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * D + lane * (D / 32));
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+        out[i] = (uint32_t)to_bf16(acc[2 * i] * inv) | ((uint32_t)to_bf16(acc[2 * i + 1] * inv) << 16);
+    if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : mm + __logf(sum);
+}
+
+template <int D, int NH>
 cudaError_t launch_d(const DecodeArgs& a, int grid, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = ensure_dynamic_smem(decode_fp4_kernel<D, NT>, Layout<D>::kBytes, done);
+    constexpr int bytes = Layout<D, NH>::kBytes;
+    cudaError_t e = ensure_dynamic_smem(decode_fp4_kernel<D, NH>, bytes, done);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(decode_fp4_kernel<D, NT>, dim3((unsigned)grid), dim3(kThreads), Layout<D>::kBytes, stream, a);
+    return launch_overlapped(decode_fp4_kernel<D, NH>, dim3((unsigned)grid), dim3(kThreads), bytes, stream, a);
+}
+
+template <int D>
+cudaError_t launch_heads(const DecodeArgs& a, int grid, cudaStream_t stream) {
+    return a.group <= 4 ? launch_d<D, 4>(a, grid, stream) : a.group <= 8 ? launch_d<D, 8>(a, grid, stream)
+                                                                         : launch_d<D, 16>(a, grid, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_fp4(int head_dim, const DecodeArgs& a, int grid, cudaStream_t stream) {
-    if (head_dim == 128) return a.group <= 8 ? launch_d<128, 1>(a, grid, stream) : launch_d<128, 2>(a, grid, stream);
-    return a.group <= 8 ? launch_d<64, 1>(a, grid, stream) : launch_d<64, 2>(a, grid, stream);
+    return head_dim == 128 ? launch_heads<128>(a, grid, stream) : launch_heads<64>(a, grid, stream);
+}
+
+cudaError_t launch_combine_fp4(int head_dim, const DecodeArgs& a, cudaStream_t stream) {
+    const dim3 grid((unsigned)(((int64_t)a.batch * a.num_q_heads + 3) / 4));
+    return head_dim == 128 ? launch_overlapped(combine_fp4_kernel<128>, grid, dim3(128), 0, stream, a)
+                           : launch_overlapped(combine_fp4_kernel<64>, grid, dim3(128), 0, stream, a);
 }
 
 }  // namespace pa

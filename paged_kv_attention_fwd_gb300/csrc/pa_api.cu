@@ -166,7 +166,8 @@ struct SchedItem {
 // persistent decode CTAs per SM: the caller's count, or what the page type's kernel is built for
 int resolve_ctas_per_sm(const pa_decode_shapes* sh) {
     if (sh->ctas_per_sm != 0) return sh->ctas_per_sm;
-    return sh->kv_dtype == PA_KV_FP4_E2M1 ? pa::kFp4CtasPerSm : 1;
+    if (sh->kv_dtype != PA_KV_FP4_E2M1) return 1;
+    return sh->num_q_heads > 8 * sh->num_kv_heads ? 2 : pa::kFp4CtasPerSm;
 }
 
 }  // namespace
@@ -463,8 +464,9 @@ pa_status decode_launch(bool fused, const pa_decode_shapes* sh, const pa_decode_
     }
     cudaError_t e = fp4 ? pa::launch_decode_fp4(D, a, plan->grid, stream)
                         : pa::launch_decode(D, fp8, a, &mk, &mv, &mq, plan->grid, stream);
+    if (e == cudaSuccess && fp4 && fused && plan->total_splits > B) e = pa::launch_combine_fp4(D, a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
-    if (fused && plan->total_splits > B && !a.counters) {
+    if (!fp4 && fused && plan->total_splits > B && !a.counters) {
         // no room for the arrival counters: merge in a second kernel
         return pa_decode_combine(sh, plan, meta_dev, out, lse, workspace, workspace_bytes, stream);
     }

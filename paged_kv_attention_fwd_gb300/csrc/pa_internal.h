@@ -58,6 +58,8 @@ cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
 // 4-bit pages (decode_fp4.cu); kFp4CtasPerSm of its CTAs fit on one SM
 constexpr int kFp4CtasPerSm = 3;
 cudaError_t launch_decode_fp4(int head_dim, const DecodeArgs& a, int grid, cudaStream_t stream);
+// merges the splits that launch_decode_fp4 left in a.o_part and a.lse_part
+cudaError_t launch_combine_fp4(int head_dim, const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_wait_timeout_probe(int* status, uint64_t limit_ns, cudaStream_t stream);
 
 // Prefill (prefill.cu)
