@@ -34,13 +34,11 @@
 // accumulators; P is rounded to fp16 (relative 2^-12) and q, scaled by a
 // power of two per head, is exact but for elements 2^14 below its largest.
 //
-// A producer warp streams page pairs (whole-slab bulk copies, with the query
-// rows in front of an item's first pair) through a ring; four warps take 32
-// keys of a pair each, with a running maximum, sum and output of their own,
-// and meet only at the end of an item, where the four results are merged
-// through a buffer outside the ring while the next item's pages already land.
-// Splits of one sequence are merged by a second, small kernel.  Every wait is
-// bounded.
+// Each warp streams its own pages (every fourth of the item's) through its
+// own ring of whole-slab bulk copies and keeps its own running maximum, sum
+// and output, so warps meet only at the end of an item, where the four
+// results are merged through the warps' last page buffers.  Splits of one
+// sequence are merged by a second, small kernel.  Every wait is bounded.
 #include <cstdint>
 
 #include "fp4.cuh"
@@ -51,9 +49,8 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;                    // that compute; one more fills the ring
-constexpr int kCompute = kWarps * 32;
-constexpr int kThreads = kCompute + 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 constexpr int kItems = 64;  // items of a CTA decoded once, in the prologue
 constexpr float kLn2 = 0.69314718055994531f;
 // The running maximum is only raised when a logit (in bits) exceeds it by more
@@ -61,17 +58,15 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kSlack = 8.f;
 constexpr float kNone = -3e38f;  // the running maximum before any key: finite, so that its differences are
 
-// D: head dim; NH: query heads of a KV group it has room for (4, 8 or 16)
-template <int D, int NH>
+// D: head dim
+template <int D>
 struct Layout {
     static constexpr int kSlab = fp4_slab_bytes(D);
-    static constexpr int kQ = 4 * kSlab;  // a stage: K, V of two pages, then query rows
-    static constexpr int kStage = kQ + NH * D * 2;
-    static constexpr int kCtas = NH == 16 ? 2 : kFp4CtasPerSm;
-    static constexpr int kStages = (NH == 16 ? 4 : 3) * (D == 128 ? 1 : 2);
-    static constexpr int kMergeHeads = NH * D <= 512 ? NH : 512 / D;  // heads merged at a time
-    static constexpr int kMerge = kStages * kStage;
-    static constexpr int kBytes = kMerge + kWarps * kMergeHeads * D * 4;
+    static constexpr int kStage = 2 * kSlab;  // K slab, V slab
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kRing = kStages * kStage;  // of one warp
+    static constexpr int kBytes = kWarps * kRing;
+    static_assert(16 * D * 4 <= kStage, "a warp's output (16 heads) must fit a page buffer");
 };
 
 struct Item {
@@ -166,56 +161,29 @@ __device__ __forceinline__ uint16_t to_bf16(float x) { return __bfloat16_as_usho
 // 128-byte line of shared memory.
 __device__ __forceinline__ int key_row(int k) { return k ^ ((k >> 1) & 1); }
 
-// Barrier `id` over `nthreads` threads that also ORs a flag across them.
-__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)pred), "r"(id), "r"(nthreads)
-        : "memory");
-    return r != 0;
-}
-
-// The ring's consumer and producer sides step through the stages alike.
-template <int S>
-struct Cursor {
-    uint32_t st = 0, phase = 0;
-    __device__ __forceinline__ void step() {
-        if (++st == S) {
-            st = 0;
-            phase ^= 1;
-        }
-    }
-};
-
+// D: head dim; NH: query heads of a KV group it has room for (4, 8 or 16)
 template <int D, int NH>
-__global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas)
-    decode_fp4_kernel(const __grid_constant__ DecodeArgs a) {
-    using L = Layout<D, NH>;
+__global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(const __grid_constant__ DecodeArgs a) {
+    using L = Layout<D>;
     constexpr int S = L::kStages;
-    constexpr int KK = D / 16;                          // MMA steps over the dims of QK
-    constexpr int NQ = NH == 16 ? 2 : 1;                // column tiles of S^T
-    constexpr int NP = NH == 4 ? 1 : 2;                 // column tiles of O^T
-    constexpr int MT = NH == 16 ? D / 16 : D / 32;      // row tiles of O^T
-    constexpr int HL = NH / 4;                          // heads whose logits a lane holds
-    constexpr int M4 = D / 32;                          // groups of 4 dims of a lane's output
+    constexpr int KB = NH == 16 ? 2 : 4;             // 16-key blocks of a softmax step
+    constexpr int KK = D / 16;                       // MMA steps over the dims of QK
+    constexpr int NQ = NH == 16 ? 2 : 1;             // column tiles of S^T and O^T
+    constexpr int MT = NH == 4 ? D / 32 : D / 16;    // row tiles of O^T
+    constexpr int HL = NH / 4;                       // heads whose logits a lane holds
+    constexpr int M4 = D / 32;                       // groups of 4 dims of a lane's output
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[S], empty[S];
+    __shared__ __align__(8) uint64_t full[kWarps][S];
     __shared__ Item items_sh[kItems];
     __shared__ float red_m[kWarps][NH], red_l[kWarps][NH];
-    __shared__ int live_sh[S][2];  // live keys of the two pages (64: all; 0: no such page, or its id is out of range)
+    __shared__ int scratch_at[kWarps];  // the page buffer that holds each warp's output
     __shared__ int abort_store;
     volatile int* abort_sh = &abort_store;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < S) {
-        mbar_init(&full[threadIdx.x], 1);
-        mbar_init(&empty[threadIdx.x], kWarps);
-    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.group;
+    uint8_t* ring = smem + warp * L::kRing;
+    uint64_t* bar = full[warp];
+    if (lane < S) mbar_init(&bar[lane], 1);
     if (threadIdx.x == 0) abort_store = 0;
     fence_barrier_init();
     grid_dependency_wait();  // shared memory only up to here
@@ -233,152 +201,152 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas)
     for (int i = threadIdx.x; i < min(it_hi - it_lo, kItems); i += kThreads) items_sh[i] = load_item(a, it_lo + i, items_off);
     __syncthreads();
     auto get_item = [&](int j) { return j - it_lo < kItems ? items_sh[j - it_lo] : load_item(a, j, items_off); };
-    Cursor<S> at;
 
-    if (warp == kWarps) {
-        // ------------------------------------------------------------ producer
-        bool ok = true;
-        uint32_t issued = 0;
-        for (int j = it_lo; j < it_hi && ok; ++j) {
-            const Item it = get_item(j);
-            const long long bt_row = (long long)it.b * a.max_pages;
-            const int key_end = min(it.seq_len, it.p1 * kPage);
-            int ids = 0;
-            for (int p = it.p0; p < it.p1; p += 2) {
-                const int k = (p - it.p0) & 31;
-                if (k == 0) ids = p + lane < it.p1 ? __ldg(&a.block_table[bt_row + p + lane]) : 0;
-                const int id0 = __shfl_sync(0xffffffffu, ids, k), id1 = __shfl_sync(0xffffffffu, ids, k + 1);
-                if (lane == 0) {
-                    ok = mbar_wait(&empty[at.st], at.phase ^ 1, abort_sh, a.wait_ns);
-                    if (ok) {
-                        const bool two = p + 1 < it.p1;
-                        const bool good0 = (unsigned)id0 < (unsigned)a.num_pool_pages;
-                        const bool good1 = two && (unsigned)id1 < (unsigned)a.num_pool_pages;
-                        const uint32_t qbytes = p == it.p0 ? (uint32_t)a.group * D * 2u : 0u;
-                        if (!good0 || (two && !good1)) record(a.status, PA_ERR_DEVICE_BOUNDS);
-                        live_sh[at.st][0] = good0 ? min(key_end - p * kPage, kPage) : 0;
-                        live_sh[at.st][1] = good1 ? min(key_end - (p + 1) * kPage, kPage) : 0;
-                        uint64_t* bar = &full[at.st];
-                        uint8_t* dst = smem + at.st * L::kStage;
-                        mbar_arrive_expect_tx(bar, ((good0 ? 2u : 0u) + (good1 ? 2u : 0u)) * L::kSlab + qbytes);
-                        if (qbytes)
-                            bulk_load(dst + L::kQ, a.q + ((long long)it.b * a.num_q_heads + it.kvh * a.group) * D, qbytes, bar);
-                        if (good0) {
-                            const long long off = ((long long)id0 * a.num_kv_heads + it.kvh) * L::kSlab;
-                            bulk_load(dst, a.k_pool + off, L::kSlab, bar);
-                            bulk_load(dst + L::kSlab, a.v_pool + off, L::kSlab, bar);
-                        }
-                        if (good1) {
-                            const long long off = ((long long)id1 * a.num_kv_heads + it.kvh) * L::kSlab;
-                            bulk_load(dst + 2 * L::kSlab, a.k_pool + off, L::kSlab, bar);
-                            bulk_load(dst + 3 * L::kSlab, a.v_pool + off, L::kSlab, bar);
-                        }
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-                if (!ok) break;
-                ++issued;
-                at.step();
-            }
+    // ---- filling the ring: a cursor over this warp's pages of all items
+    int pj = it_lo - 1, pp = 0, pend = 0, pkvh = 0;
+    int ids = 0, id_base = 0;     // ids of the warp's next 32 pages of item pj, one per lane
+    int next_ids = 0;             // and of its first 32 of item pj + 1, on their way
+    uint32_t fill_st = 0, dead = 0;  // next stage to fill; stages whose page id was out of range
+    int in_ring = 0;
+    auto first_ids = [&](int j) {
+        if (j >= it_hi) return 0;
+        const Item it = get_item(j);
+        const int i = it.p0 + warp + kWarps * lane;
+        return i < it.p1 ? __ldg(&a.block_table[(long long)it.b * a.max_pages + i]) : 0;
+    };
+    next_ids = first_ids(it_lo);
+    auto fill = [&]() {  // the warp's next page into stage fill_st, which is free
+        while (pp >= pend) {
+            if (pj + 1 >= it_hi) return;
+            const Item it = get_item(++pj);
+            pp = id_base = it.p0 + warp;
+            pend = it.p1;
+            pkvh = it.kvh;
+            ids = next_ids;
+            next_ids = first_ids(pj + 1);
         }
+        if (pp - id_base >= 32 * kWarps) {
+            const Item it = get_item(pj);
+            id_base = pp;
+            const int i = pp + kWarps * lane;
+            ids = i < pend ? __ldg(&a.block_table[(long long)it.b * a.max_pages + i]) : 0;
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, (pp - id_base) / kWarps);
+        const bool ok = (unsigned)id < (unsigned)a.num_pool_pages;
+        dead = ok ? dead & ~(1u << fill_st) : dead | (1u << fill_st);
         if (lane == 0) {
-            if (!ok) {
-                *abort_sh = 1;
-                record(a.status, PA_ERR_TIMEOUT);
+            uint8_t* dst = ring + fill_st * L::kStage;
+            if (ok) {
+                const long long off = ((long long)id * a.num_kv_heads + pkvh) * L::kSlab;
+                mbar_arrive_expect_tx(&bar[fill_st], 2 * L::kSlab);
+                bulk_load(dst, a.k_pool + off, L::kSlab, &bar[fill_st]);
+                bulk_load(dst + L::kSlab, a.v_pool + off, L::kSlab, &bar[fill_st]);
+            } else {
+                record(a.status, PA_ERR_DEVICE_BOUNDS);
+                mbar_arrive(&bar[fill_st]);
             }
-            // every copy must land before the CTA may exit; the consumers have seen to it unless they gave up
-            const uint32_t last = issued < (uint32_t)S ? issued : (uint32_t)S;
-            for (uint32_t i = issued - last; i < issued; ++i) mbar_wait(&full[i % S], (i / S) & 1, nullptr, a.wait_ns);
         }
-        return;
-    }
+        if (++fill_st == S) fill_st = 0;
+        ++in_ring;
+        pp += kWarps;
+    };
+#pragma unroll 1
+    for (int i = 0; i < S; ++i) fill();
 
-    // ---------------------------------------------------------------- consumers
-    const int g = lane >> 2, t = lane & 3, G = a.group;
-    float* merge = reinterpret_cast<float*>(smem + L::kMerge);
-    // this lane's places in a slab, for the first 16-key block of the warp: K row, V keys
-    const int row0 = (warp & 1) * 32;
-    const int krow = row0 + key_row(g), vkey0 = row0 + key_row(2 * t), vkey1 = row0 + key_row(2 * t + 1);
-    const uint8_t* kbase = smem + (warp >> 1) * (2 * L::kSlab) + krow * (D / 2) + t * (D / 8);
-    const uint8_t* kscale = smem + (warp >> 1) * (2 * L::kSlab) + kPage * (D / 2) + krow * (D / 16) + (D == 128 ? 2 * t : t);
-    const uint8_t* vslab = smem + (warp >> 1) * (2 * L::kSlab) + L::kSlab;
+    uint32_t raw[NQ][D / 8];  // the next item's queries, as they lie in memory: the head of column g, dims of t
+    auto load_q = [&](int j) {
+        const Item it = get_item(j);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            const int h = NH == 4 ? g >> 1 : n * 8 + g;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                a.q + ((long long)it.b * a.num_q_heads + it.kvh * G + h) * D + t * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 v = h < G ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                raw[n][4 * i] = v.x; raw[n][4 * i + 1] = v.y; raw[n][4 * i + 2] = v.z; raw[n][4 * i + 3] = v.w;
+            }
+        }
+    };
+    if (it_lo < it_hi) load_q(it_lo);
+
+    // this lane's places in a slab, for the first 16-key block: K row, V keys
+    const int krow = key_row(g), vkey0 = key_row(2 * t), vkey1 = key_row(2 * t + 1);
+    const uint8_t* kbase = ring + krow * (D / 2) + t * (D / 8);
+    const uint8_t* kscale = ring + kPage * (D / 2) + krow * (D / 16) + (D == 128 ? 2 * t : t);
+    const uint8_t* vslab = ring + L::kSlab;
     // halves of a P pair (keys 2t, 2t + 1) with a zero beside them
-    const uint32_t sel0 = NH == 4 && (g & 1) ? 0x1044u : 0x4410u, sel1 = NH == 4 && (g & 1) ? 0x3244u : 0x4432u;
+    const uint32_t sel0 = g & 1 ? 0x1044u : 0x4410u, sel1 = g & 1 ? 0x3244u : 0x4432u;
 
+    uint32_t st = 0, phase = 0;  // next stage to take
     bool bad = false;
     for (int j = it_lo; j < it_hi; ++j) {
         const Item it = get_item(j);
+        const int key_end = min(it.seq_len, it.p1 * kPage);
         const float k_scale = __ldg(&a.k_scale[it.kvh]), vs = __ldg(&a.v_scale[it.kvh]);
         // logits in bits are products times |bits|: its sign goes into q, so that maxima can be taken of the products
         const float bits = fabsf(a.scale_log2 * k_scale);
         const uint32_t sign = __float_as_uint(a.scale_log2 * k_scale) & 0x80000000u;
-        uint32_t q[NQ][2 * KK];
-        float sl2[HL], o[NP][MT][4], m[HL], l[HL];
+        uint32_t q[NQ][2 * KK];  // B fragments
+        float sl2[HL], o[NQ][MT][4], m[HL], l[HL];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[n][i] << 16)), fabsf(__uint_as_float(raw[n][i] & 0xFFFF0000u))));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^e <= amax < 2^(e+1), kept where both 2^e and 2^-e are ordinary floats
+            const int e = amax > 0.f && amax < INFINITY ? min(max((int)(__float_as_uint(amax) >> 23) - 127, -96), 96) : 0;
+            const float down = __uint_as_float(((uint32_t)(127 - e) << 23) | sign), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                q[n][i] = pack_half2(__uint_as_float(raw[n][i] << 16) * down, __uint_as_float(raw[n][i] & 0xFFFF0000u) * down);
+            // the power of two of each head whose logits this lane holds
+            if constexpr (NH == 4) {
+                sl2[0] = bits * __shfl_sync(0xffffffffu, up, 8 * t);
+            } else {
+                sl2[2 * n] = bits * __shfl_sync(0xffffffffu, up, 8 * t);
+                sl2[2 * n + 1] = bits * __shfl_sync(0xffffffffu, up, 8 * t + 4);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
             m[i] = kNone;
             l[i] = 0.f;
         }
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[n][i][k] = 0.f;
 
-        if (it.p0 < it.p1) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[at.st], at.phase, abort_sh, a.wait_ns))) bad = true;
-            const uint32_t so = at.st * L::kStage;
-            // ---- the group's queries as B fragments: dims [t D/4, (t + 1) D/4) of the head of column g
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                const int h = NH == 4 ? g >> 1 : n * 8 + g;
-                const uint4* src = reinterpret_cast<const uint4*>(smem + so + L::kQ + h * (D * 2) + t * (D / 2));
-                uint32_t raw[D / 8];
-                float amax = 0.f;
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const uint4 v = h < G ? src[i] : make_uint4(0, 0, 0, 0);
-                    raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
-                }
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[i] << 16)), fabsf(__uint_as_float(raw[i] & 0xFFFF0000u))));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // 2^e <= amax < 2^(e+1), kept where both 2^e and 2^-e are ordinary floats
-                const int e = amax > 0.f && amax < INFINITY ? min(max((int)(__float_as_uint(amax) >> 23) - 127, -96), 96) : 0;
-                const float down = __uint_as_float(((uint32_t)(127 - e) << 23) | sign), up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    q[n][i] = pack_half2(__uint_as_float(raw[i] << 16) * down, __uint_as_float(raw[i] & 0xFFFF0000u) * down);
-                // the power of two of each head whose logits this lane holds
-                if constexpr (NH == 4) {
-                    sl2[0] = bits * __shfl_sync(0xffffffffu, up, 8 * t);
-                } else {
-                    sl2[2 * n] = bits * __shfl_sync(0xffffffffu, up, 8 * t);
-                    sl2[2 * n + 1] = bits * __shfl_sync(0xffffffffu, up, 8 * t + 4);
-                }
-            }
-        }
-
-        for (int p = it.p0; p < it.p1 && !bad; p += 2) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[at.st], at.phase, abort_sh, a.wait_ns))) {
+        bool owed = false;  // the last page's buffer is refilled after the merge
+        uint32_t last = 0;
+        for (int p = it.p0 + warp; p < it.p1; p += kWarps) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar[st], phase, abort_sh, a.wait_ns))) {
                 bad = true;
                 break;
             }
-            const uint32_t so = at.st * L::kStage;
-            const int live = live_sh[at.st][warp >> 1] - row0;  // live keys among this warp's 32 (32 or more: all)
-            if (live > 0) {
+            --in_ring;
+            const uint32_t so = st * L::kStage;
+            const int page_live = (dead >> st) & 1u ? 0 : key_end - p * kPage;  // live keys (64 or more: all)
+#pragma unroll 1
+            for (int r0 = 0; r0 < kPage; r0 += KB * 16) {
+                const int live = page_live - r0;
+                if (live <= 0) break;
+                const uint32_t ko = so + r0 * (D / 2);
                 // ---- S^T = K q^T
-                float c[NQ][2][4];
+                float c[NQ][KB][4];
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
+                for (int blk = 0; blk < KB; ++blk) {
                     uint32_t w[2][D / 32], sc[2][D / 64];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint8_t* src = kbase + so + (blk * 16 + 8 * i) * (D / 2);
-                        const uint8_t* scl = kscale + so + (blk * 16 + 8 * i) * (D / 16);
+                        const uint8_t* src = kbase + ko + (blk * 16 + 8 * i) * (D / 2);
+                        const uint8_t* scl = kscale + so + (r0 + blk * 16 + 8 * i) * (D / 16);
                         if constexpr (D == 128) {
                             const uint4 v = *reinterpret_cast<const uint4*>(src);
                             w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
@@ -406,15 +374,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas)
                     }
                 }
                 // products x[i][2 blk + r] of head slot i, row 16 blk + 8 r + g
-                float x[HL][4];
+                float x[HL][2 * KB];
 #pragma unroll
                 for (int i = 0; i < HL; ++i)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x[i][k] = c[NH == 16 ? i >> 1 : 0][k >> 1][2 * (k & 1) + (NH == 4 ? 0 : i & 1)];
-                if (live < 32) {
+                    for (int k = 0; k < 2 * KB; ++k) x[i][k] = c[i >> 1][k >> 1][2 * (k & 1) + (NH == 4 ? 0 : i & 1)];
+                const bool tail = live < KB * 16;
+                if (tail) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (8 * k + key_row(g) >= live) {
+                    for (int k = 0; k < 2 * KB; ++k)
+                        if (8 * k + krow >= live) {
 #pragma unroll
                             for (int i = 0; i < HL; ++i) x[i][k] = -INFINITY;
                         }
@@ -424,7 +393,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas)
                 float top[HL];
 #pragma unroll
                 for (int i = 0; i < HL; ++i) {
-                    top[i] = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])) * sl2[i];
+                    top[i] = x[i][0];
+#pragma unroll
+                    for (int k = 1; k < 2 * KB; ++k) top[i] = fmaxf(top[i], x[i][k]);
+                    top[i] *= sl2[i];
                     raise |= top[i] > m[i] + kSlack;
                 }
                 if (__any_sync(0xffffffffu, raise)) {
@@ -439,63 +411,58 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas)
                         m[i] = mn;
                         l[i] *= alpha;
 #pragma unroll
-                        for (int n = 0; n < NP; ++n)
+                        for (int n = 0; n < NQ; ++n)
 #pragma unroll
                             for (int k = 0; k < MT; ++k)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    if (NH == 4 || (NH == 8 && (e & 1) == i) || (NH == 16 && n == i >> 1 && (e & 1) == (i & 1)))
-                                        o[n][k][e] *= alpha;
+                                    if (NH == 4 || (n == i >> 1 && (e & 1) == (i & 1))) o[n][k][e] *= alpha;
                     }
                 }
-                float pr[HL][4];
 #pragma unroll
-                for (int i = 0; i < HL; ++i) {
+                for (int i = 0; i < HL; ++i)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) pr[i][k] = ex2(fmaf(x[i][k], sl2[i], -m[i]));
-                }
-                if (live < 32) {  // whatever -inf times a scale of 0 came to
+                    for (int k = 0; k < 2 * KB; ++k) x[i][k] = ex2(fmaf(x[i][k], sl2[i], -m[i]));
+                if (tail) {  // whatever -inf times a scale of 0 came to
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (8 * k + key_row(g) >= live) {
+                    for (int k = 0; k < 2 * KB; ++k)
+                        if (8 * k + krow >= live) {
 #pragma unroll
-                            for (int i = 0; i < HL; ++i) pr[i][k] = 0.f;
+                            for (int i = 0; i < HL; ++i) x[i][k] = 0.f;
                         }
                 }
-#pragma unroll
-                for (int i = 0; i < HL; ++i) l[i] += (pr[i][0] + pr[i][1]) + (pr[i][2] + pr[i][3]);
                 // ---- O^T += V^T P^T
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
+                for (int blk = 0; blk < KB; ++blk) {
+#pragma unroll
+                    for (int i = 0; i < HL; ++i) l[i] += x[i][2 * blk] + x[i][2 * blk + 1];
                     uint32_t w[4][D / 64], b[4];  // keys vkey0, vkey1, vkey0 + 8, vkey1 + 8 of the block
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = (i & 1 ? vkey1 : vkey0) + 8 * (i >> 1) + 16 * blk;
                         if constexpr (D == 128) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(vslab + so + key * 64 + g * 8);
+                            const uint2 v = *reinterpret_cast<const uint2*>(vslab + ko + key * 64 + g * 8);
                             w[i][0] = v.x;
                             w[i][1] = v.y;
-                            b[i] = vslab[so + kPage * 64 + key * 8 + g];
+                            b[i] = vslab[so + kPage * 64 + (r0 + key) * 8 + g];
                         } else {
-                            w[i][0] = *reinterpret_cast<const uint32_t*>(vslab + so + key * 32 + g * 4);
-                            b[i] = vslab[so + kPage * 32 + key * 4 + (g >> 1)];
+                            w[i][0] = *reinterpret_cast<const uint32_t*>(vslab + ko + key * 32 + g * 4);
+                            b[i] = vslab[so + kPage * 32 + (r0 + key) * 4 + (g >> 1)];
                         }
                     }
-                    if (live < 32) {  // a dead key's scale may be a NaN, which a zero P would not cancel
+                    if (tail) {  // a dead key's scale may be a NaN, which a zero P would not cancel
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if ((i & 1 ? vkey1 : vkey0) + 8 * (i >> 1) + 16 * blk >= live + row0) b[i] = 0;
+                            if ((i & 1 ? vkey1 : vkey0) + 8 * (i >> 1) + 16 * blk >= live) b[i] = 0;
                     }
                     const uint32_t s01 = e4m3x2_to_half2(b[0] | (b[1] << 8)), s23 = e4m3x2_to_half2(b[2] | (b[3] << 8));
-                    if constexpr (NH < 16) {
-                        // 8 keys at a time: A = (key, parity), B = P at one parity
+                    if constexpr (NH == 4) {
+                        // 8 keys at a time: A = (key, parity of the dim), B = P at one parity
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             const int k = 2 * blk + hf;
-                            const uint32_t y = transpose8x8(NH == 4 ? pack_half2(pr[0][k], pr[0][k])
-                                                                    : pack_half2(pr[0][k], pr[HL - 1][k]));
-                            const uint32_t even0 = __byte_perm(y, 0, sel0), even1 = __byte_perm(y, 0, sel1);
-                            const uint32_t odd0 = __byte_perm(y, 0, 0x1044), odd1 = __byte_perm(y, 0, 0x3244);
+                            const uint32_t y = transpose8x8(pack_half2(x[0][k], x[0][k]));
+                            const uint32_t p0 = __byte_perm(y, 0, sel0), p1 = __byte_perm(y, 0, sel1);
                             const uint32_t sh = hf ? s23 : s01;
                             const uint32_t sa = __byte_perm(sh, 0, 0x1010), sb = __byte_perm(sh, 0, 0x3232);
 #pragma unroll
@@ -504,17 +471,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas)
                                 const int byte = (mt & 1) * 2;
                                 const uint32_t a0 = mul2(code_pair(wa, byte), sa), a1 = mul2(code_pair(wa, byte + 1), sa);
                                 const uint32_t a2 = mul2(code_pair(wb, byte), sb), a3 = mul2(code_pair(wb, byte + 1), sb);
-                                mma16816(o[0][mt], a0, a1, a2, a3, even0, even1);
-                                if constexpr (NH == 8) mma16816(o[NP - 1][mt], a0, a1, a2, a3, odd0, odd1);
+                                mma16816(o[0][mt], a0, a1, a2, a3, p0, p1);
                             }
                         }
                     } else {
-                        uint32_t pb[2][2];
+                        uint32_t pb[NQ][2];
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                        for (int n = 0; n < NQ; ++n)
 #pragma unroll
                             for (int r = 0; r < 2; ++r)
-                                pb[n][r] = transpose8x8(pack_half2(pr[2 * n % HL][2 * blk + r], pr[(2 * n + 1) % HL][2 * blk + r]));
+                                pb[n][r] = transpose8x8(pack_half2(x[2 * n][2 * blk + r], x[(2 * n + 1) % HL][2 * blk + r]));
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
                             const uint32_t h0 = code_pair(w[0][mt / 4], mt & 3), h1 = code_pair(w[1][mt / 4], mt & 3);
@@ -524,17 +490,26 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas)
                             const uint32_t a2 = mul2(__byte_perm(h2, h3, 0x5410), s23);
                             const uint32_t a3 = mul2(__byte_perm(h2, h3, 0x7632), s23);
 #pragma unroll
-                            for (int n = 0; n < 2; ++n) mma16816(o[n % NP][mt], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                            for (int n = 0; n < NQ; ++n) mma16816(o[n][mt], a0, a1, a2, a3, pb[n][0], pb[n][1]);
                         }
                     }
                 }
             }
             __syncwarp();  // every lane is done with the stage
-            if (lane == 0) mbar_arrive(&empty[at.st]);
-            at.step();
+            if (p + kWarps < it.p1) fill();
+            else {
+                owed = true;
+                last = so;
+            }
+            if (++st == S) {
+                st = 0;
+                phase ^= 1;
+            }
         }
+        if (j + 1 < it_hi) load_q(j + 1);  // lands while the warps merge
 
-        // ---- merge the four warps
+        // ---- merge the four warps: [head][dim] in each one's last page buffer, a lane's groups of 4 dims rotated by
+        // its t, so that no two lanes of a store meet in a bank
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
             const int h = NH == 4 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
@@ -544,68 +519,66 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas)
                 red_m[warp][h] = m[i];
                 red_l[warp][h] = l[i];
             }
+            if (owed && h < G) {
+#pragma unroll
+                for (int k = 0; k < M4; ++k) {
+                    float4 v;
+                    if constexpr (NH == 4) v = make_float4(o[0][k][0], o[0][k][1], o[0][k][2], o[0][k][3]);
+                    else
+                        v = make_float4(o[i >> 1][2 * k % MT][i & 1], o[i >> 1][2 * k % MT][2 + (i & 1)],
+                                        o[i >> 1][(2 * k + 1) % MT][i & 1], o[i >> 1][(2 * k + 1) % MT][2 + (i & 1)]);
+                    *reinterpret_cast<float4*>(ring + last + (h * D + g * (D / 8) + 4 * ((k + t) & (M4 - 1))) * 4) = v;
+                }
+            }
+        }
+        if (lane == 0) scratch_at[warp] = (int)(ring - smem) + (int)last;
+        if (__syncthreads_or(bad || *abort_sh != 0)) {
+            bad = true;
+            break;
         }
         const bool partial = it.nsplit > 1;
         const long long head0 = (long long)it.kvh * G;
         const long long orow = partial ? (long long)(it.split_base + it.s) * a.num_q_heads + head0
                                        : (long long)it.b * a.num_q_heads + head0;
-        constexpr int HC = L::kMergeHeads;
+        for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
+            const int h = idx / D, d = idx % D;
+            const int ht = NH == 4 ? h : (h >> 1) & 3;  // the t of the lanes that held head h
+            const int slot = h * D + d / (D / 8) * (D / 8) + 4 * ((d % (D / 8) / 4 + ht) & (M4 - 1)) + (d & 3);
+            float mm = kNone, ll = 0.f, val = 0.f;
 #pragma unroll
-        for (int ch = 0; ch < NH / HC; ++ch) {  // heads ch HC .. ch HC + HC - 1
-            if (ch * HC >= G) break;
-            // [warp][head][dim], a lane's groups of 4 dims rotated by its t: no two lanes of a store meet in a bank
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, red_m[w][h]);
 #pragma unroll
-            for (int i = 0; i < HL; ++i) {
-                const int h = (NH == 4 ? t : 8 * (i >> 1) + 2 * t + (i & 1)) - ch * HC;
-                if (h >= 0 && h < HC) {
-#pragma unroll
-                    for (int k = 0; k < M4; ++k) {
-                        float4 v;
-                        if constexpr (NH == 4) v = make_float4(o[0][k][0], o[0][k][1], o[0][k][2], o[0][k][3]);
-                        else if constexpr (NH == 8)
-                            v = make_float4(o[0][k][i], o[NP - 1][k][i], o[0][k][2 + i], o[NP - 1][k][2 + i]);
-                        else
-                            v = make_float4(o[(i >> 1) % NP][2 * k % MT][i & 1], o[(i >> 1) % NP][2 * k % MT][2 + (i & 1)],
-                                            o[(i >> 1) % NP][(2 * k + 1) % MT][i & 1], o[(i >> 1) % NP][(2 * k + 1) % MT][2 + (i & 1)]);
-                        *reinterpret_cast<float4*>(merge + (warp * HC + h) * D + g * (D / 8) + 4 * ((k + t) & (M4 - 1))) = v;
-                    }
-                }
+            for (int w = 0; w < kWarps; ++w) {
+                const float lw = red_l[w][h];
+                if (lw == 0.f) continue;                // no live key: nothing was written
+                const float f = ex2(red_m[w][h] - mm);  // a NaN logit leaves a NaN sum, and so a NaN output
+                ll = fmaf(f, lw, ll);
+                val = fmaf(f, reinterpret_cast<const float*>(smem + scratch_at[w])[slot], val);
             }
-            if (named_bar_or(1, kCompute, bad || *abort_sh != 0)) {
-                bad = true;
-                break;
+            val = ll == 0.f ? 0.f : val * (vs / ll);
+            if (partial) a.o_part[(orow + h) * D + d] = val;
+            else a.out[(orow + h) * D + d] = to_bf16(val);
+            if (d == 0) {
+                const float lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+                if (partial) a.lse_part[orow + h] = lse;
+                else if (a.lse) a.lse[orow + h] = lse;
             }
-            for (int idx = threadIdx.x; idx < min(HC, G - ch * HC) * D; idx += kCompute) {
-                const int hh = idx / D, d = idx % D, h = ch * HC + hh;
-                const int ht = NH == 4 ? h : (h >> 1) & 3;  // the t of the lanes that held head h
-                const int slot = d / (D / 8) * (D / 8) + 4 * ((d % (D / 8) / 4 + ht) & (M4 - 1)) + (d & 3);
-                float mm = kNone, ll = 0.f, val = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, red_m[w][h]);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float mw = red_m[w][h], lw = red_l[w][h];
-                    if (lw == 0.f) continue;       // no live key
-                    const float f = ex2(mw - mm);  // a NaN logit leaves a NaN sum, and so a NaN output
-                    ll = fmaf(f, lw, ll);
-                    val = fmaf(f, merge[(w * HC + hh) * D + slot], val);
-                }
-                val = ll == 0.f ? 0.f : val * (vs / ll);
-                if (partial) a.o_part[(orow + h) * D + d] = val;
-                else a.out[(orow + h) * D + d] = to_bf16(val);
-                if (d == 0) {
-                    const float lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-                    if (partial) a.lse_part[orow + h] = lse;
-                    else if (a.lse) a.lse[orow + h] = lse;
-                }
-            }
-            named_bar_sync(1, kCompute);
         }
-        if (bad) break;
+        fence_proxy_async_smem();  // the buffers go back to the async copies
+        __syncthreads();
+        if (owed) fill();
     }
     if (bad && lane == 0) {
-        *abort_sh = 1;  // the producer stops too
+        *abort_sh = 1;
         record(a.status, PA_ERR_TIMEOUT);
+        // every copy must land before the CTA may exit
+        for (; in_ring > 0; --in_ring) {
+            mbar_wait(&bar[st], phase, nullptr, a.wait_ns);
+            if (++st == S) {
+                st = 0;
+                phase ^= 1;
+            }
+        }
     }
 }
 
@@ -666,10 +639,9 @@ __global__ void __launch_bounds__(128) combine_fp4_kernel(const __grid_constant_
 template <int D, int NH>
 cudaError_t launch_d(const DecodeArgs& a, int grid, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    constexpr int bytes = Layout<D, NH>::kBytes;
-    cudaError_t e = ensure_dynamic_smem(decode_fp4_kernel<D, NH>, bytes, done);
+    cudaError_t e = ensure_dynamic_smem(decode_fp4_kernel<D, NH>, Layout<D>::kBytes, done);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(decode_fp4_kernel<D, NH>, dim3((unsigned)grid), dim3(kThreads), bytes, stream, a);
+    return launch_overlapped(decode_fp4_kernel<D, NH>, dim3((unsigned)grid), dim3(kThreads), Layout<D>::kBytes, stream, a);
 }
 
 template <int D>

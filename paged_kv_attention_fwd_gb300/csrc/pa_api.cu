@@ -167,7 +167,7 @@ struct SchedItem {
 int resolve_ctas_per_sm(const pa_decode_shapes* sh) {
     if (sh->ctas_per_sm != 0) return sh->ctas_per_sm;
     if (sh->kv_dtype != PA_KV_FP4_E2M1) return 1;
-    return sh->num_q_heads > 8 * sh->num_kv_heads ? 2 : pa::kFp4CtasPerSm;
+    return pa::kFp4CtasPerSm;
 }
 
 }  // namespace
