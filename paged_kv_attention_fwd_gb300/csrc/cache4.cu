@@ -3,9 +3,13 @@
 //
 // Both are copies with a conversion, so HBM-bound: 2 bytes of a 16-bit row
 // against 0.5625 (4-bit), 1 (e4m3) or 2 bytes of a page row per element.  A
-// thread owns one 16-element piece -- the block of the 4-bit type, so neither
-// its largest magnitude nor its scale crosses threads -- of the key row and
-// of the value row of one head, and issues all its loads before any store.
+// thread owns one 16-element piece of a row -- the block of the 4-bit type, so
+// neither its largest magnitude nor its scale crosses threads.  A warp takes
+// 32 / (D / 16) consecutive tokens, whose rows are neighbours in a page, of up
+// to kHeads heads: what it touches of a slab is contiguous (at D = 128, 256
+// bytes of codes and one 32-byte sector of scales), and the search for the
+// tokens' sequence and page is paid once for all heads.  All loads of a batch
+// of heads are issued before any store.
 #include "cache4.cuh"
 #include "pa_launch.h"
 #include "token_place.cuh"
@@ -13,33 +17,59 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kHeads = 4;  // heads of a warp
 
-// grid: x = tokens / kWarps (one warp each), y = groups of 32 / (D / 16) KV heads
+// This thread's token and the first of its warp's heads.
+// grid: x = groups of tokens, kWarps to a CTA; y = groups of kHeads heads
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const AppendArgs a) {
+struct Share {
+    static constexpr int kLanes = D / 16, kTokens = 32 / kLanes;
+    int tok, piece, h0;
+    __device__ __forceinline__ Share()
+        : tok((int)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * kTokens + (int)(threadIdx.x & 31) / kLanes),
+          piece((int)(threadIdx.x & 31) % kLanes),
+          h0((int)blockIdx.y * kHeads) {}
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_constant__ AppendArgs a) {
+    grid_dependency_wait();
     allow_dependents_launch();
-    constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
-    const int tok = (int)(blockIdx.x * kWarps + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    if (tok >= a.total_new) return;
+    const Share<D> my;
+    if (my.tok >= a.total_new) return;
+    const int nh = min(kHeads, a.num_kv_heads - my.h0);
+    // rows first: they do not depend on the token's place
+    uint4 w[kHeads][2][2];
+    const long long src = ((long long)my.tok * a.num_kv_heads + my.h0) * D + my.piece * 16;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+        if (i < nh) {
+            const uint4* k = reinterpret_cast<const uint4*>(a.k_new + src + i * D);
+            const uint4* v = reinterpret_cast<const uint4*>(a.v_new + src + i * D);
+            w[i][0][0] = __ldg(k);
+            w[i][0][1] = __ldg(k + 1);
+            w[i][1][0] = __ldg(v);
+            w[i][1][1] = __ldg(v + 1);
+        }
     int page, row;
     long long pos;
-    const Place at = token_place(tok, a.cu_new, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages,
+    const Place at = token_place(my.tok, a.cu_new, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages,
                                  page, row, pos);
     if (at != Place::kOk) {
-        if (lane == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
+        if (my.piece == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         return;
     }
-    const int h = (int)blockIdx.y * kHeads + lane / kLanes, piece = lane % kLanes;
-    if (h >= a.num_kv_heads) return;
-    const long long src = ((long long)tok * a.num_kv_heads + h) * D + piece * 16;
-    const uint4* k = reinterpret_cast<const uint4*>(a.k_new + src);
-    const uint4* v = reinterpret_cast<const uint4*>(a.v_new + src);
-    const uint4 k0 = __ldg(k), k1 = __ldg(k + 1), v0 = __ldg(v), v1 = __ldg(v + 1);
-    const float ks = __ldg(&a.k_scale[h]), vs = __ldg(&a.v_scale[h]);
-    const long long slab = ((long long)page * a.num_kv_heads + h) * fp4_slab_bytes(D);
-    fp4_store_block<D>(static_cast<uint8_t*>(a.k_pool) + slab, row, piece, k0, k1, ks);
-    fp4_store_block<D>(static_cast<uint8_t*>(a.v_pool) + slab, row, piece, v0, v1, vs);
+    const long long slab = ((long long)page * a.num_kv_heads + my.h0) * fp4_slab_bytes(D);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+        if (i < nh) {
+            const long long at_head = slab + (long long)i * fp4_slab_bytes(D);
+            fp4_store_block<D>(static_cast<uint8_t*>(a.k_pool) + at_head, row, my.piece, w[i][0][0], w[i][0][1],
+                               __ldg(&a.k_scale[my.h0 + i]));
+            fp4_store_block<D>(static_cast<uint8_t*>(a.v_pool) + at_head, row, my.piece, w[i][1][0], w[i][1][1],
+                               __ldg(&a.v_scale[my.h0 + i]));
+        }
 }
 
 // 16 elements as they lie in a page, before conversion
@@ -100,59 +130,65 @@ __device__ __forceinline__ void store_piece(uint16_t* dst, const Piece<kType>& p
 
 // grid as for append_fp4_kernel
 template <int D, int kType>
-__global__ void __launch_bounds__(kWarps * 32) gather_kernel(const GatherArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_constant__ GatherArgs a) {
+    grid_dependency_wait();
     allow_dependents_launch();
-    constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
-    const int tok = (int)(blockIdx.x * kWarps + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    if (tok >= a.total) return;
+    const Share<D> my;
+    if (my.tok >= a.total) return;
     int page, row;
     long long pos;
     const Place at =
-        token_place(tok, a.cu, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages, page, row, pos);
+        token_place(my.tok, a.cu, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages, page, row, pos);
     if (at != Place::kOk) {
-        if (lane == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
+        if (my.piece == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         return;
     }
-    const int h = (int)blockIdx.y * kHeads + lane / kLanes, piece = lane % kLanes;
-    if (h >= a.num_kv_heads) return;
-    const long long slab = (long long)page * a.num_kv_heads + h;
-    const Piece<kType> k = load_piece<D, kType>(a.k_pool, slab, row, piece);
-    const Piece<kType> v = load_piece<D, kType>(a.v_pool, slab, row, piece);
-    float ks = 1.f, vs = 1.f;
-    if constexpr (kType == PA_KV_FP4_E2M1 || kType == PA_KV_FP8_E4M3) {
-        ks = __ldg(&a.k_scale[h]);
-        vs = __ldg(&a.v_scale[h]);
-    }
-    const long long dst = ((long long)tok * a.num_kv_heads + h) * D + piece * 16;
-    store_piece<kType>(a.k_out + dst, k, ks);
-    store_piece<kType>(a.v_out + dst, v, vs);
+    const int nh = min(kHeads, a.num_kv_heads - my.h0);
+    const long long slab = (long long)page * a.num_kv_heads + my.h0;
+    Piece<kType> k[kHeads], v[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+        if (i < nh) {
+            k[i] = load_piece<D, kType>(a.k_pool, slab + i, row, my.piece);
+            v[i] = load_piece<D, kType>(a.v_pool, slab + i, row, my.piece);
+        }
+    const long long dst = ((long long)my.tok * a.num_kv_heads + my.h0) * D + my.piece * 16;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+        if (i < nh) {
+            float ks = 1.f, vs = 1.f;
+            if constexpr (kType == PA_KV_FP4_E2M1 || kType == PA_KV_FP8_E4M3) {
+                ks = __ldg(&a.k_scale[my.h0 + i]);
+                vs = __ldg(&a.v_scale[my.h0 + i]);
+            }
+            store_piece<kType>(a.k_out + dst + i * D, k[i], ks);
+            store_piece<kType>(a.v_out + dst + i * D, v[i], vs);
+        }
 }
 
 template <int D>
 dim3 token_grid(int tokens, int heads) {
-    constexpr int kHeads = 32 / (D / 16);
-    return dim3((unsigned)((tokens + kWarps - 1) / kWarps), (unsigned)((heads + kHeads - 1) / kHeads));
+    constexpr int per_cta = kWarps * Share<D>::kTokens;
+    return dim3((unsigned)((tokens + per_cta - 1) / per_cta), (unsigned)((heads + kHeads - 1) / kHeads));
 }
 
 template <int D>
 cudaError_t launch_gather_d(const GatherArgs& a, int kv_dtype, cudaStream_t stream) {
-    const dim3 grid = token_grid<D>(a.total, a.num_kv_heads);
+    const dim3 grid = token_grid<D>(a.total, a.num_kv_heads), block(kWarps * 32);
     switch (kv_dtype) {
-        case PA_KV_FP4_E2M1: gather_kernel<D, PA_KV_FP4_E2M1><<<grid, kWarps * 32, 0, stream>>>(a); break;
-        case PA_KV_FP8_E4M3: gather_kernel<D, PA_KV_FP8_E4M3><<<grid, kWarps * 32, 0, stream>>>(a); break;
-        default: gather_kernel<D, PA_KV_BF16><<<grid, kWarps * 32, 0, stream>>>(a); break;  // either 16-bit type: a copy
+        case PA_KV_FP4_E2M1: return launch_overlapped(gather_kernel<D, PA_KV_FP4_E2M1>, grid, block, 0, stream, a);
+        case PA_KV_FP8_E4M3: return launch_overlapped(gather_kernel<D, PA_KV_FP8_E4M3>, grid, block, 0, stream, a);
+        default: return launch_overlapped(gather_kernel<D, PA_KV_BF16>, grid, block, 0, stream, a);  // either 16-bit type
     }
-    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_append_fp4(const AppendArgs& a, cudaStream_t stream) {
-    if (a.head_dim == 128)
-        append_fp4_kernel<128><<<token_grid<128>(a.total_new, a.num_kv_heads), kWarps * 32, 0, stream>>>(a);
-    else
-        append_fp4_kernel<64><<<token_grid<64>(a.total_new, a.num_kv_heads), kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    const dim3 block(kWarps * 32);
+    return a.head_dim == 128
+               ? launch_overlapped(append_fp4_kernel<128>, token_grid<128>(a.total_new, a.num_kv_heads), block, 0, stream, a)
+               : launch_overlapped(append_fp4_kernel<64>, token_grid<64>(a.total_new, a.num_kv_heads), block, 0, stream, a);
 }
 
 cudaError_t launch_gather(const GatherArgs& a, int head_dim, int kv_dtype, cudaStream_t stream) {

@@ -7,11 +7,13 @@
 //   (a, b) -> (a cos - b sin, b cos + a sin)          (first rope_dim elements)
 //
 // with one rounding to 16 bits at the end.  HBM-bound: 2 bytes in, 2 out per
-// element and a table row per token.  A head row is held by D / 8 lanes, 8
-// elements each: two groups of 4 whose elements pair up with one another, so
-// the rotation needs no shuffle in either pairing.  A warp takes
-// kPasses * (32 / (D / 8)) rows of one token -- queries, keys, values in that
-// order -- and loads all of them, and its angles once, before it computes.
+// element and a table row per token; what it must not be is issue-bound.  So
+// a head row is held by D / 8 lanes, 8 elements each, in two groups of 4 that
+// pair up with one another (the rotation needs no shuffle in either pairing);
+// a warp takes rows of one token and one kind (queries, keys or values), with
+// the weights multiplied into its cosines and sines once,
+//   a' = inv (a (w_a cos) - b (w_b sin)),  b' = inv (b (w_b cos) + a (w_a sin)),
+// and the arithmetic runs on pairs of fp32 (f32x2).
 #include "cache4.cuh"
 #include "pa_launch.h"
 #include "token_place.cuh"
@@ -19,19 +21,49 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4, kPasses = 4;
+constexpr int kWarps = 4;
+constexpr int kPasses = 4;  // rows of a lane whose loads are in flight together
+
+struct F2 {  // two fp32 values in one 64-bit register pair
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 swapped(F2 a) {
+    const float2 s = split(a);
+    return f2(s.y, s.x);
+}
 
 __device__ __forceinline__ float2 unpack16(uint32_t w, bool f16) {
     if (f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) {
+__device__ __forceinline__ uint32_t pack16(F2 a, bool f16) {
+    const float2 v = split(a);
     if (f16) {
-        const __half2 h = __floats2half2_rn(a, b);
+        const __half2 h = __floats2half2_rn(v.x, v.y);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
@@ -70,45 +102,52 @@ __device__ __forceinline__ void load_angles(const NormRopeArgs& a, const int (&p
 }
 
 // kCache: -1 keys to k_out, else the page type they (and the values) go to
-template <int D, bool kInterleaved, int kCache>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopeArgs a) {
+template <int D, bool kInterleaved, int kCache, bool kF16>
+__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+    grid_dependency_wait();
     allow_dependents_launch();
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     constexpr bool kAppend = kCache >= 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kLanes;
-    const int rows = a.num_q_heads + (kAppend ? 2 : 1) * a.num_kv_heads;
-    const int chunks = (rows + kPasses * kRows - 1) / (kPasses * kRows);
+    // this warp's token, kind of rows and first row
+    const int per_warp = a.batches * kPasses * kRows;
+    const int qchunks = (a.num_q_heads + per_warp - 1) / per_warp, kchunks = (a.num_kv_heads + per_warp - 1) / per_warp;
+    const int chunks = qchunks + (kAppend ? 2 : 1) * kchunks;
     const long long id = (long long)blockIdx.x * kWarps + warp;
-    const int tok = (int)(id / chunks), chunk = (int)(id % chunks);
+    const int tok = (int)(id / chunks);
+    int chunk = (int)(id % chunks);
     if (tok >= a.total_tokens) return;
-    const bool f16 = a.f16;
+    const int kind = chunk < qchunks ? 0 : chunk < qchunks + kchunks ? 1 : 2;  // queries, keys, values
+    chunk -= kind == 0 ? 0 : kind == 1 ? qchunks : qchunks + kchunks;
+    const int heads = kind == 0 ? a.num_q_heads : a.num_kv_heads;
+    const int row_end = min(heads, (chunk + 1) * per_warp);
+    const uint16_t* src = kind == 0 ? a.q + tok * a.q_stride : kind == 1 ? a.k + tok * a.k_stride : a.v + tok * a.v_stride;
 
     // where this lane's two groups of 4 elements lie in a row, and whether they turn
     const int half = a.rope_dim / 2;
-    const bool turns = kInterleaved ? 8 * l < a.rope_dim : 4 * l < half;
-    const int off0 = kInterleaved ? 8 * l : turns ? 4 * l : a.rope_dim + 8 * (l - half / 4);
-    const int off1 = kInterleaved || !turns ? off0 + 4 : half + 4 * l;
+    const bool turns = kind != 2 && (kInterleaved ? 8 * l < a.rope_dim : 4 * l < half);
+    const int off0 = kInterleaved ? 8 * l : 4 * l < half ? 4 * l : a.rope_dim + 8 * (l - half / 4);
+    const int off1 = kInterleaved || 4 * l >= half ? off0 + 4 : half + 4 * l;
 
-    // rows of this warp: all loads first
     uint2 x[kPasses][2];
+    auto load_rows = [&](int r0) {
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-        const int r = (chunk * kPasses + p) * kRows + lane / kLanes;
-        if (r < rows) {
-            const uint16_t* src =
-                r < a.num_q_heads ? a.q + tok * a.q_stride + (long long)r * D
-                : r < a.num_q_heads + a.num_kv_heads ? a.k + tok * a.k_stride + (long long)(r - a.num_q_heads) * D
-                                                     : a.v + tok * a.v_stride + (long long)(r - a.num_q_heads - a.num_kv_heads) * D;
-            if constexpr (kInterleaved) {
-                const uint4 w = *reinterpret_cast<const uint4*>(src + off0);
-                x[p][0] = make_uint2(w.x, w.y);
-                x[p][1] = make_uint2(w.z, w.w);
-            } else {
-                x[p][0] = *reinterpret_cast<const uint2*>(src + off0);
-                x[p][1] = *reinterpret_cast<const uint2*>(src + off1);
+        for (int p = 0; p < kPasses; ++p) {
+            const int r = r0 + p * kRows + lane / kLanes;
+            if (r < row_end) {
+                const uint16_t* row = src + r * D;
+                if constexpr (kInterleaved) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(row + off0);
+                    x[p][0] = make_uint2(w.x, w.y);
+                    x[p][1] = make_uint2(w.z, w.w);
+                } else {
+                    x[p][0] = *reinterpret_cast<const uint2*>(row + off0);
+                    x[p][1] = *reinterpret_cast<const uint2*>(row + off1);
+                }
             }
         }
-    }
+    };
+    load_rows(chunk * per_warp);
 
     // place in the cache, positions, angles
     int page = 0, prow = 0;
@@ -121,9 +160,9 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopeAr
             return;
         }
     }
-    int pos[3] = {0, 0, 0};
     float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
     if (a.rope_dim > 0) {
+        int pos[3] = {0, 0, 0};
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < 3; ++i)
@@ -140,117 +179,140 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopeAr
         if (turns) load_angles(a, pos, 4 * l, c, s);
     }
 
+    // y = inv (x c1 + partner c2): elements 01, 23, 45, 67 of the lane
+    F2 c1[4], c2[4];
+    {
+        float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+        const uint16_t* wp = kind == 0 ? a.q_weight : a.k_weight;
+        if (a.norm && wp != nullptr && kind != 2) {
+            const uint2 w0 = __ldg(reinterpret_cast<const uint2*>(wp + off0)), w1 = __ldg(reinterpret_cast<const uint2*>(wp + off1));
+            const float2 p0 = unpack16(w0.x, kF16), p1 = unpack16(w0.y, kF16), p2 = unpack16(w1.x, kF16), p3 = unpack16(w1.y, kF16);
+            w[0] = p0.x; w[1] = p0.y; w[2] = p1.x; w[3] = p1.y;
+            w[4] = p2.x; w[5] = p2.y; w[6] = p3.x; w[7] = p3.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kInterleaved) {
+                c1[i] = f2(w[2 * i] * c[i], w[2 * i + 1] * c[i]);
+                c2[i] = f2(-w[2 * i + 1] * s[i], w[2 * i] * s[i]);
+            } else {
+                const int e = 2 * (i & 1), n = 2 * i, m = (n + 4) & 7;  // pairs e, e + 1; elements n, n + 1; partners m, m + 1
+                const float sg = i < 2 ? -1.f : 1.f;
+                c1[i] = f2(w[n] * c[e], w[n + 1] * c[e + 1]);
+                c2[i] = f2(sg * w[m] * s[e], sg * w[m + 1] * s[e + 1]);
+            }
+        }
+    }
+
     __shared__ __align__(16) uint16_t stage[kCache == PA_KV_FP4_E2M1 ? kWarps : 1][kCache == PA_KV_FP4_E2M1 ? kRows * D : 8];
 
+    for (int rb = chunk * per_warp; rb < row_end; rb += kPasses * kRows) {
+        if (rb > chunk * per_warp) load_rows(rb);
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-        const int r0 = (chunk * kPasses + p) * kRows;  // first row of the pass (warp-uniform)
-        if (r0 >= rows) break;
-        const int r = r0 + lane / kLanes;
-        const bool is_q = r < a.num_q_heads, is_v = r >= a.num_q_heads + a.num_kv_heads;
-        uint2 y0 = make_uint2(0, 0), y1 = make_uint2(0, 0);
-        if (r < rows) {
-            y0 = x[p][0];
-            y1 = x[p][1];
-        }
-        float f[8];
-        const float2 f01 = unpack16(y0.x, f16), f23 = unpack16(y0.y, f16), f45 = unpack16(y1.x, f16),
-                     f67 = unpack16(y1.y, f16);
-        f[0] = f01.x; f[1] = f01.y; f[2] = f23.x; f[3] = f23.y;
-        f[4] = f45.x; f[5] = f45.y; f[6] = f67.x; f[7] = f67.y;
-        if (a.norm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-#pragma unroll
-            for (int o = kLanes / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float inv = rsqrtf(ss * (1.f / D) + a.eps);
-            const uint16_t* wp = is_q ? a.q_weight : a.k_weight;
-            float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-            if (wp != nullptr && !is_v) {
-                const uint2 w0 = __ldg(reinterpret_cast<const uint2*>(wp + off0)),
-                            w1 = __ldg(reinterpret_cast<const uint2*>(wp + off1));
-                const float2 a01 = unpack16(w0.x, f16), a23 = unpack16(w0.y, f16), a45 = unpack16(w1.x, f16),
-                             a67 = unpack16(w1.y, f16);
-                w[0] = a01.x; w[1] = a01.y; w[2] = a23.x; w[3] = a23.y;
-                w[4] = a45.x; w[5] = a45.y; w[6] = a67.x; w[7] = a67.y;
+        for (int p = 0; p < kPasses; ++p) {
+            const int r0 = rb + p * kRows;  // first row of the pass (warp-uniform)
+            if (r0 >= row_end) break;
+            const int r = r0 + lane / kLanes;
+            const bool mine = r < row_end;
+            uint2 y0 = make_uint2(0, 0), y1 = make_uint2(0, 0);
+            if (mine) {
+                y0 = x[p][0];
+                y1 = x[p][1];
             }
+            if (kind != 2) {  // values pass through bit for bit
+                const uint32_t u[4] = {y0.x, y0.y, y1.x, y1.y};
+                F2 f[4], y[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * w[i];
-        }
-        if (turns) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int ia = kInterleaved ? 2 * i : i, ib = kInterleaved ? 2 * i + 1 : 4 + i;
-                const float u = f[ia], v = f[ib];
-                f[ia] = u * c[i] - v * s[i];
-                f[ib] = v * c[i] + u * s[i];
-            }
-        }
-        if (!is_v) {  // values pass through bit for bit
-            y0 = make_uint2(pack16(f[0], f[1], f16), pack16(f[2], f[3], f16));
-            y1 = make_uint2(pack16(f[4], f[5], f16), pack16(f[6], f[7], f16));
-        }
-        uint16_t* dst = nullptr;  // a 16-bit destination row
-        if (r < rows) {
-            if (is_q) dst = a.q_out + tok * a.q_out_stride + (long long)r * D;
-            else if constexpr (!kAppend) dst = a.k_out + tok * a.k_out_stride + (long long)(r - a.num_q_heads) * D;
-        }
-        if constexpr (kAppend) {
-            const int h = is_v ? r - a.num_q_heads - a.num_kv_heads : r - a.num_q_heads;
-            const long long slab = (long long)page * a.num_kv_heads + h;
-            uint8_t* pool = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool);
-            const float* scales = is_v ? a.v_scale : a.k_scale;
-            if constexpr (kCache == PA_KV_BF16) {  // either 16-bit type
-                if (r < rows && !is_q) dst = reinterpret_cast<uint16_t*>(pool) + (slab * kPage + prow) * D;
-            } else if constexpr (kCache == PA_KV_FP8_E4M3) {
-                if (r < rows && !is_q) {
-                    uint8_t* out = pool + (slab * kPage + prow) * D;
-                    const float scale = __ldg(&scales[h]);
-                    *reinterpret_cast<uint32_t*>(out + off0) = e4m3x4(y0, scale);
-                    *reinterpret_cast<uint32_t*>(out + off1) = e4m3x4(y1, scale);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = unpack16(u[i], kF16);
+                    f[i] = f2(v.x, v.y);
                 }
-            } else if (r0 + kRows > a.num_q_heads) {  // the pass holds a cache row: through shared memory, so
-                uint16_t* st = stage[warp];           // that one lane sees the 16 elements of a block
-                *reinterpret_cast<uint2*>(st + (lane / kLanes) * D + off0) = y0;
-                *reinterpret_cast<uint2*>(st + (lane / kLanes) * D + off1) = y1;
-                __syncwarp();
-                constexpr int kBlocks = D / 16;
-                const int br = r0 + lane / kBlocks, piece = lane % kBlocks;
-                if (lane < kRows * kBlocks && br >= a.num_q_heads && br < rows) {
-                    const bool bv = br >= a.num_q_heads + a.num_kv_heads;
-                    const int bh = br - a.num_q_heads - (bv ? a.num_kv_heads : 0);
-                    const uint4* w = reinterpret_cast<const uint4*>(st + (lane / kBlocks) * D + piece * 16);
-                    fp4_store_block<D>(static_cast<uint8_t*>(bv ? a.v_pool : a.k_pool) +
-                                           ((long long)page * a.num_kv_heads + bh) * fp4_slab_bytes(D),
-                                       prow, piece, w[0], w[1], __ldg(&(bv ? a.v_scale : a.k_scale)[bh]));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = f[i] * c1[i];
+                if (turns) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = fma2(kInterleaved ? swapped(f[i]) : f[(i + 2) & 3], c2[i], y[i]);
                 }
-                __syncwarp();
+                if (a.norm) {
+                    const float2 sq = split(fma2(f[3], f[3], fma2(f[2], f[2], fma2(f[1], f[1], f[0] * f[0]))));
+                    float ss = sq.x + sq.y;
+#pragma unroll
+                    for (int o = kLanes / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+                    const F2 inv2 = f2(inv, inv);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = y[i] * inv2;
+                }
+                y0 = make_uint2(pack16(y[0], kF16), pack16(y[1], kF16));
+                y1 = make_uint2(pack16(y[2], kF16), pack16(y[3], kF16));
             }
-        }
-        if (dst != nullptr) {
-            if constexpr (kInterleaved) {
-                *reinterpret_cast<uint4*>(dst + off0) = make_uint4(y0.x, y0.y, y1.x, y1.y);
-            } else {
-                *reinterpret_cast<uint2*>(dst + off0) = y0;
-                *reinterpret_cast<uint2*>(dst + off1) = y1;
+            uint16_t* dst = nullptr;  // a 16-bit destination row
+            if (kind == 0) dst = a.q_out + tok * a.q_out_stride + (long long)r * D;
+            else if constexpr (!kAppend) dst = a.k_out + tok * a.k_out_stride + (long long)r * D;
+            if constexpr (kAppend) {
+                if (kind != 0) {
+                    const long long slab = (long long)page * a.num_kv_heads + r;
+                    uint8_t* pool = static_cast<uint8_t*>(kind == 2 ? a.v_pool : a.k_pool);
+                    const float* scales = kind == 2 ? a.v_scale : a.k_scale;
+                    if constexpr (kCache == PA_KV_BF16) {  // either 16-bit type
+                        dst = reinterpret_cast<uint16_t*>(pool) + (slab * kPage + prow) * D;
+                    } else if constexpr (kCache == PA_KV_FP8_E4M3) {
+                        if (mine) {
+                            uint8_t* out = pool + (slab * kPage + prow) * D;
+                            const float scale = __ldg(&scales[r]);
+                            *reinterpret_cast<uint32_t*>(out + off0) = e4m3x4(y0, scale);
+                            *reinterpret_cast<uint32_t*>(out + off1) = e4m3x4(y1, scale);
+                        }
+                    } else {  // through shared memory, so that one lane sees the 16 elements of a block
+                        uint16_t* st = stage[warp];
+                        *reinterpret_cast<uint2*>(st + (lane / kLanes) * D + off0) = y0;
+                        *reinterpret_cast<uint2*>(st + (lane / kLanes) * D + off1) = y1;
+                        __syncwarp();
+                        constexpr int kBlocks = D / 16;
+                        const int br = r0 + lane / kBlocks, piece = lane % kBlocks;
+                        if (lane < kRows * kBlocks && br < row_end) {
+                            const uint4* w = reinterpret_cast<const uint4*>(st + (lane / kBlocks) * D + piece * 16);
+                            fp4_store_block<D>(pool + ((long long)page * a.num_kv_heads + br) * fp4_slab_bytes(D), prow,
+                                               piece, w[0], w[1], __ldg(&scales[br]));
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (dst != nullptr && mine) {
+                if constexpr (kInterleaved) {
+                    *reinterpret_cast<uint4*>(dst + off0) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+                } else {
+                    *reinterpret_cast<uint2*>(dst + off0) = y0;
+                    *reinterpret_cast<uint2*>(dst + off1) = y1;
+                }
             }
         }
     }
 }
 
-template <int D, bool kInterleaved, int kCache>
-cudaError_t launch(const NormRopeArgs& a, cudaStream_t stream) {
+template <int D, bool kInterleaved, int kCache, bool kF16>
+cudaError_t launch(NormRopeArgs a, cudaStream_t stream) {
     constexpr int kRows = 32 / (D / 8) * kPasses;
-    const int rows = a.num_q_heads + (kCache >= 0 ? 2 : 1) * a.num_kv_heads;
-    const long long warps = (long long)a.total_tokens * ((rows + kRows - 1) / kRows);
-    norm_rope_kernel<D, kInterleaved, kCache><<<(unsigned)((warps + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    auto warps = [&] {
+        const int per_warp = a.batches * kRows;
+        return (long long)a.total_tokens * ((a.num_q_heads + per_warp - 1) / per_warp +
+                                            (kCache >= 0 ? 2 : 1) * ((a.num_kv_heads + per_warp - 1) / per_warp));
+    };
+    // Rows of a warp share its token's angles and weights, so the more the
+    // better once every SM has its warps anyway.
+    a.batches = 1;
+    if (warps() >= 32768) a.batches = 4;
+    return launch_overlapped(norm_rope_kernel<D, kInterleaved, kCache, kF16>, dim3((unsigned)((warps() + kWarps - 1) / kWarps)),
+                             dim3(kWarps * 32), 0, stream, a);
 }
 
 template <int D, int kCache>
 cudaError_t launch_pairing(const NormRopeArgs& a, cudaStream_t stream) {
-    return a.interleaved ? launch<D, true, kCache>(a, stream) : launch<D, false, kCache>(a, stream);
+    if constexpr (kCache <= PA_KV_BF16) {  // the other page types take bf16 tokens only
+        if (a.f16) return a.interleaved ? launch<D, true, kCache, true>(a, stream) : launch<D, false, kCache, true>(a, stream);
+    }
+    return a.interleaved ? launch<D, true, kCache, false>(a, stream) : launch<D, false, kCache, false>(a, stream);
 }
 
 template <int D>
