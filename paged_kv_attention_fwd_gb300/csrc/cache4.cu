@@ -25,11 +25,19 @@ constexpr int kHeads = 4;  // heads of a warp
 template <int D>
 struct Share {
     static constexpr int kLanes = D / 16, kTokens = 32 / kLanes;
-    int tok, piece, h0;
+    int tok0, tok, piece, h0;  // tok0: the warp's first token
     __device__ __forceinline__ Share()
-        : tok((int)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * kTokens + (int)(threadIdx.x & 31) / kLanes),
+        : tok0((int)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * kTokens),
+          tok(tok0 + (int)(threadIdx.x & 31) / kLanes),
           piece((int)(threadIdx.x & 31) % kLanes),
           h0((int)blockIdx.y * kHeads) {}
+    // the sequence that holds this thread's token; the whole warp calls it
+    __device__ __forceinline__ int sequence(const int32_t* __restrict__ cu, int batch) const {
+        int b = max(warp_sequence(tok0, cu, batch), 0);
+        if (tok < __ldg(&cu[b])) return -1;
+        while (b < batch && __ldg(&cu[b + 1]) <= tok) ++b;
+        return b;
+    }
 };
 
 template <int D>
@@ -37,6 +45,8 @@ __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_co
     grid_dependency_wait();
     allow_dependents_launch();
     const Share<D> my;
+    if (my.tok0 >= a.total_new) return;
+    const int b = my.sequence(a.cu_new, a.batch);
     if (my.tok >= a.total_new) return;
     const int nh = min(kHeads, a.num_kv_heads - my.h0);
     // rows first: they do not depend on the token's place
@@ -54,7 +64,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_co
         }
     int page, row;
     long long pos;
-    const Place at = token_place(my.tok, a.cu_new, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages,
+    const Place at = token_place(my.tok, b, a.cu_new, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages,
                                  page, row, pos);
     if (at != Place::kOk) {
         if (my.piece == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
@@ -134,11 +144,13 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
     grid_dependency_wait();
     allow_dependents_launch();
     const Share<D> my;
+    if (my.tok0 >= a.total) return;
+    const int b = my.sequence(a.cu, a.batch);
     if (my.tok >= a.total) return;
     int page, row;
     long long pos;
     const Place at =
-        token_place(my.tok, a.cu, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages, page, row, pos);
+        token_place(my.tok, b, a.cu, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages, page, row, pos);
     if (at != Place::kOk) {
         if (my.piece == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         return;

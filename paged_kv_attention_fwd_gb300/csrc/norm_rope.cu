@@ -10,10 +10,11 @@
 // element and a table row per token; what it must not be is issue-bound.  So
 // a head row is held by D / 8 lanes, 8 elements each, in two groups of 4 that
 // pair up with one another (the rotation needs no shuffle in either pairing);
-// a warp takes rows of one token and one kind (queries, keys or values), with
-// the weights multiplied into its cosines and sines once,
+// a warp takes up to kPasses rows per lane of one kind (queries, keys or
+// values), with the weights multiplied into the cosines and sines,
 //   a' = inv (a (w_a cos) - b (w_b sin)),  b' = inv (b (w_b cos) + a (w_a sin)),
-// and the arithmetic runs on pairs of fp32 (f32x2).
+// the arithmetic runs on pairs of fp32 (f32x2), and a warp goes on to the same
+// rows of the next tokens with their elements and angles already on the way.
 #include "cache4.cuh"
 #include "pa_launch.h"
 #include "token_place.cuh"
@@ -22,6 +23,7 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kCtas = 4;    // CTAs of an SM
 constexpr int kPasses = 4;  // rows of a lane whose loads are in flight together
 
 struct F2 {  // two fp32 values in one 64-bit register pair
@@ -80,48 +82,51 @@ __device__ __forceinline__ uint32_t e4m3x4(uint2 w, float scale) {
 
 // The four cos and sin a lane needs: pairs pair0 .. pair0 + 3, whose positions
 // may belong to different axes.
-__device__ __forceinline__ void load_angles(const NormRopeArgs& a, const int (&pos)[3], int pair0, float (&c)[4],
-                                            float (&s)[4]) {
+struct Angles {
+    float c[4], s[4];
+};
+__device__ __forceinline__ void load_angles(const NormRopeArgs& a, const int (&pos)[3], int pair0, Angles& to) {
     const int half = a.rope_dim / 2;
     const int e0 = a.sections[0], e1 = e0 + a.sections[1];
     auto axis = [&](int p) { return p < e0 ? pos[0] : p < e1 ? pos[1] : pos[2]; };
-    const int first = axis(pair0), last = axis(pair0 + 3);
-    if (first == last && axis(pair0 + 1) == first && axis(pair0 + 2) == first) {
+    const int first = axis(pair0);
+    if (a.num_axes == 1 || (axis(pair0 + 1) == first && axis(pair0 + 2) == first && axis(pair0 + 3) == first)) {
         const float* t = a.cos_sin + (long long)first * a.rope_dim + pair0;
         const float4 c4 = __ldg(reinterpret_cast<const float4*>(t)), s4 = __ldg(reinterpret_cast<const float4*>(t + half));
-        c[0] = c4.x; c[1] = c4.y; c[2] = c4.z; c[3] = c4.w;
-        s[0] = s4.x; s[1] = s4.y; s[2] = s4.z; s[3] = s4.w;
+        to.c[0] = c4.x; to.c[1] = c4.y; to.c[2] = c4.z; to.c[3] = c4.w;
+        to.s[0] = s4.x; to.s[1] = s4.y; to.s[2] = s4.z; to.s[3] = s4.w;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float* t = a.cos_sin + (long long)axis(pair0 + i) * a.rope_dim + pair0 + i;
-            c[i] = __ldg(t);
-            s[i] = __ldg(t + half);
+            to.c[i] = __ldg(t);
+            to.s[i] = __ldg(t + half);
         }
     }
 }
 
 // kCache: -1 keys to k_out, else the page type they (and the values) go to
 template <int D, bool kInterleaved, int kCache, bool kF16>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     grid_dependency_wait();
     allow_dependents_launch();
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     constexpr bool kAppend = kCache >= 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kLanes;
-    // this warp's token, kind of rows and first row
-    const int per_warp = a.batches * kPasses * kRows;
-    const int qchunks = (a.num_q_heads + per_warp - 1) / per_warp, kchunks = (a.num_kv_heads + per_warp - 1) / per_warp;
+    // this warp's kind of rows, its rows of a token, and its tokens
+    constexpr int kPer = kPasses * kRows;
+    const int qchunks = (a.num_q_heads + kPer - 1) / kPer, kchunks = (a.num_kv_heads + kPer - 1) / kPer;
     const int chunks = qchunks + (kAppend ? 2 : 1) * kchunks;
     const long long id = (long long)blockIdx.x * kWarps + warp;
-    const int tok = (int)(id / chunks);
     int chunk = (int)(id % chunks);
-    if (tok >= a.total_tokens) return;
+    const int tok0 = (int)min(id / chunks * a.tokens_per_warp, (long long)a.total_tokens);
+    const int tok_end = min(a.total_tokens, tok0 + a.tokens_per_warp);
+    if (tok0 >= tok_end) return;
     const int kind = chunk < qchunks ? 0 : chunk < qchunks + kchunks ? 1 : 2;  // queries, keys, values
     chunk -= kind == 0 ? 0 : kind == 1 ? qchunks : qchunks + kchunks;
-    const int heads = kind == 0 ? a.num_q_heads : a.num_kv_heads;
-    const int row_end = min(heads, (chunk + 1) * per_warp);
-    const uint16_t* src = kind == 0 ? a.q + tok * a.q_stride : kind == 1 ? a.k + tok * a.k_stride : a.v + tok * a.v_stride;
+    const int first_row = chunk * kPer, row_end = min(kind == 0 ? a.num_q_heads : a.num_kv_heads, first_row + kPer);
+    const uint16_t* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    const long long src_stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
 
     // where this lane's two groups of 4 elements lie in a row, and whether they turn
     const int half = a.rope_dim / 2;
@@ -129,123 +134,164 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const __grid_con
     const int off0 = kInterleaved ? 8 * l : 4 * l < half ? 4 * l : a.rope_dim + 8 * (l - half / 4);
     const int off1 = kInterleaved || 4 * l >= half ? off0 + 4 : half + 4 * l;
 
-    uint2 x[kPasses][2];
-    auto load_rows = [&](int r0) {
+    struct Rows {
+        uint2 x[kPasses][2];
+    };
+    auto load_rows = [&](Rows& to, int tok) {
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-            const int r = r0 + p * kRows + lane / kLanes;
-            if (r < row_end) {
-                const uint16_t* row = src + r * D;
+            const int r = min(first_row + p * kRows + lane / kLanes, row_end - 1);  // past the last row: that row again
+            {
+                const uint16_t* row = src + tok * src_stride + r * D;
                 if constexpr (kInterleaved) {
                     const uint4 w = *reinterpret_cast<const uint4*>(row + off0);
-                    x[p][0] = make_uint2(w.x, w.y);
-                    x[p][1] = make_uint2(w.z, w.w);
+                    to.x[p][0] = make_uint2(w.x, w.y);
+                    to.x[p][1] = make_uint2(w.z, w.w);
                 } else {
-                    x[p][0] = *reinterpret_cast<const uint2*>(row + off0);
-                    x[p][1] = *reinterpret_cast<const uint2*>(row + off1);
+                    to.x[p][0] = *reinterpret_cast<const uint2*>(row + off0);
+                    to.x[p][1] = *reinterpret_cast<const uint2*>(row + off1);
                 }
             }
         }
     };
-    load_rows(chunk * per_warp);
-
-    // place in the cache, positions, angles
-    int page = 0, prow = 0;
-    long long cpos = 0;
-    if constexpr (kAppend) {
-        const Place at = token_place(tok, a.cu_new, a.start_pos, a.block_table, a.batch, a.max_pages,
-                                     a.num_pool_pages, page, prow, cpos);
-        if (at != Place::kOk) {
-            if (lane == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
-            return;
-        }
-    }
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.rope_dim > 0) {
-        int pos[3] = {0, 0, 0};
-        bool bad = false;
+    struct Pos {
+        int at[3];
+    };
+    const bool by_place = kAppend && a.positions == nullptr;  // positions are those in the cache
+    auto load_pos = [&](Pos& to, int tok) {
+        if (a.rope_dim == 0 || by_place) return;
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-            if (i < a.num_axes) {
-                if (kAppend && a.positions == nullptr) pos[i] = (int)min(cpos, (long long)a.max_position);
-                else pos[i] = __ldg(&a.positions[(long long)i * a.total_tokens + tok]);
-                bad |= pos[i] < 0 || pos[i] >= a.max_position;
-            }
-        if (pos[0] < 0) return;  // a padding row
-        if (bad) {
-            if (lane == 0) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
-            return;
+            if (i < a.num_axes) to.at[i] = __ldg(&a.positions[(long long)i * a.total_tokens + tok]);
+    };
+    struct Where {  // a token's place in the cache
+        int page, row;
+        Place place;
+    };
+    auto find_place = [&](Where& to, Pos& pos, int tok) {
+        long long cpos = 0;
+        to.place = token_place(tok, warp_sequence(tok, a.cu_new, a.batch), a.cu_new, a.start_pos, a.block_table,
+                               a.batch, a.max_pages, a.num_pool_pages, to.page, to.row, cpos);
+        if (by_place) {
+            const int p = to.place == Place::kOk ? (int)min(cpos, (long long)a.max_position) : 0;
+            pos.at[0] = pos.at[1] = pos.at[2] = p;
         }
-        if (turns) load_angles(a, pos, 4 * l, c, s);
-    }
-
-    // y = inv (x c1 + partner c2): elements 01, 23, 45, 67 of the lane
-    F2 c1[4], c2[4];
-    {
-        float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-        const uint16_t* wp = kind == 0 ? a.q_weight : a.k_weight;
-        if (a.norm && wp != nullptr && kind != 2) {
-            const uint2 w0 = __ldg(reinterpret_cast<const uint2*>(wp + off0)), w1 = __ldg(reinterpret_cast<const uint2*>(wp + off1));
-            const float2 p0 = unpack16(w0.x, kF16), p1 = unpack16(w0.y, kF16), p2 = unpack16(w1.x, kF16), p3 = unpack16(w1.y, kF16);
-            w[0] = p0.x; w[1] = p0.y; w[2] = p1.x; w[3] = p1.y;
-            w[4] = p2.x; w[5] = p2.y; w[6] = p3.x; w[7] = p3.y;
-        }
+    };
+    // angles of a token whose positions are known; false where one is outside the table
+    auto start_angles = [&](Angles& to, const Pos& pos) {
+        if (a.rope_dim == 0) return true;
+        bool ok = true;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (kInterleaved) {
-                c1[i] = f2(w[2 * i] * c[i], w[2 * i + 1] * c[i]);
-                c2[i] = f2(-w[2 * i + 1] * s[i], w[2 * i] * s[i]);
-            } else {
-                const int e = 2 * (i & 1), n = 2 * i, m = (n + 4) & 7;  // pairs e, e + 1; elements n, n + 1; partners m, m + 1
-                const float sg = i < 2 ? -1.f : 1.f;
-                c1[i] = f2(w[n] * c[e], w[n + 1] * c[e + 1]);
-                c2[i] = f2(sg * w[m] * s[e], sg * w[m + 1] * s[e + 1]);
-            }
-        }
+        for (int i = 0; i < 3; ++i)
+            if (i < a.num_axes) ok &= (unsigned)pos.at[i] < (unsigned)a.max_position;
+        if (ok && turns) load_angles(a, pos.at, 4 * l, to);
+        return ok;
+    };
+
+    Rows rows;
+    Pos pos{{0, 0, 0}}, pos1{{0, 0, 0}};
+    Angles ang{{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
+    Where where{0, 0, Place::kOk};
+    load_rows(rows, tok0);
+    load_pos(pos, tok0);
+    if (tok0 + 1 < tok_end) load_pos(pos1, tok0 + 1);
+    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    const uint16_t* wp = kind == 0 ? a.q_weight : a.k_weight;
+    if (a.norm && wp != nullptr && kind != 2) {
+        const uint2 w0 = __ldg(reinterpret_cast<const uint2*>(wp + off0)), w1 = __ldg(reinterpret_cast<const uint2*>(wp + off1));
+        const float2 p0 = unpack16(w0.x, kF16), p1 = unpack16(w0.y, kF16), p2 = unpack16(w1.x, kF16), p3 = unpack16(w1.y, kF16);
+        w[0] = p0.x; w[1] = p0.y; w[2] = p1.x; w[3] = p1.y;
+        w[4] = p2.x; w[5] = p2.y; w[6] = p3.x; w[7] = p3.y;
+    }
+    if constexpr (kAppend) {
+        if (by_place) find_place(where, pos, tok0);
+    }
+    bool in_table = start_angles(ang, pos);
+    if constexpr (kAppend) {
+        if (!by_place) find_place(where, pos, tok0);
     }
 
     __shared__ __align__(16) uint16_t stage[kCache == PA_KV_FP4_E2M1 ? kWarps : 1][kCache == PA_KV_FP4_E2M1 ? kRows * D : 8];
 
-    for (int rb = chunk * per_warp; rb < row_end; rb += kPasses * kRows) {
-        if (rb > chunk * per_warp) load_rows(rb);
+#pragma unroll 1
+    for (int tok = tok0; tok < tok_end; ++tok) {
+        // y = inv (x c1 + partner c2): elements 01, 23, 45, 67 of the lane
+        F2 c1[4], c2[4];
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            const int r0 = rb + p * kRows;  // first row of the pass (warp-uniform)
-            if (r0 >= row_end) break;
-            const int r = r0 + lane / kLanes;
-            const bool mine = r < row_end;
-            uint2 y0 = make_uint2(0, 0), y1 = make_uint2(0, 0);
-            if (mine) {
-                y0 = x[p][0];
-                y1 = x[p][1];
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kInterleaved) {
+                c1[i] = f2(w[2 * i] * ang.c[i], w[2 * i + 1] * ang.c[i]);
+                c2[i] = f2(-w[2 * i + 1] * ang.s[i], w[2 * i] * ang.s[i]);
+            } else {
+                const int e = 2 * (i & 1), n = 2 * i, m = (n + 4) & 7;  // pairs e, e + 1; elements n, n + 1; partners m, m + 1
+                const float sg = i < 2 ? -1.f : 1.f;
+                c1[i] = f2(w[n] * ang.c[e], w[n + 1] * ang.c[e + 1]);
+                c2[i] = f2(sg * w[m] * ang.s[e], sg * w[m + 1] * ang.s[e + 1]);
             }
-            if (kind != 2) {  // values pass through bit for bit
-                const uint32_t u[4] = {y0.x, y0.y, y1.x, y1.y};
-                F2 f[4], y[4];
+        }
+        // a padding token, or one that is out of range: nothing is written
+        const bool padding = where.place == Place::kPadding || (where.place == Place::kOk && a.rope_dim > 0 && pos.at[0] < 0);
+        const bool skip = padding || where.place != Place::kOk || !in_table;
+        if (skip && !padding && lane == 0) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
+        const int page = where.page, prow = where.row;
+        const Rows now = rows;
+        if (tok + 1 < tok_end) {  // the next token's loads
+            load_rows(rows, tok + 1);
+            pos = pos1;
+            if constexpr (kAppend) find_place(where, pos, tok + 1);
+            in_table = start_angles(ang, pos);
+            if (tok + 2 < tok_end) load_pos(pos1, tok + 2);
+        }
+        if (skip) continue;
+
+        // all passes of a stage side by side: their chains of dependent steps overlap
+        Rows out = now;
+        if (kind != 2) {  // values pass through bit for bit
+            F2 y[kPasses][4];
+            float inv[kPasses];
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) {
+                const uint32_t u[4] = {now.x[p][0].x, now.x[p][0].y, now.x[p][1].x, now.x[p][1].y};
+                F2 f[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 v = unpack16(u[i], kF16);
                     f[i] = f2(v.x, v.y);
                 }
+                const float2 sq = split(fma2(f[3], f[3], fma2(f[2], f[2], fma2(f[1], f[1], f[0] * f[0]))));
+                inv[p] = sq.x + sq.y;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = f[i] * c1[i];
+                for (int i = 0; i < 4; ++i) y[p][i] = f[i] * c1[i];
                 if (turns) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = fma2(kInterleaved ? swapped(f[i]) : f[(i + 2) & 3], c2[i], y[i]);
+                    for (int i = 0; i < 4; ++i) y[p][i] = fma2(kInterleaved ? swapped(f[i]) : f[(i + 2) & 3], c2[i], y[p][i]);
                 }
-                if (a.norm) {
-                    const float2 sq = split(fma2(f[3], f[3], fma2(f[2], f[2], fma2(f[1], f[1], f[0] * f[0]))));
-                    float ss = sq.x + sq.y;
-#pragma unroll
-                    for (int o = kLanes / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const float inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-                    const F2 inv2 = f2(inv, inv);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = y[i] * inv2;
-                }
-                y0 = make_uint2(pack16(y[0], kF16), pack16(y[1], kF16));
-                y1 = make_uint2(pack16(y[2], kF16), pack16(y[3], kF16));
             }
+            if (a.norm) {
+#pragma unroll
+                for (int o = kLanes / 2; o >= 1; o >>= 1)
+#pragma unroll
+                    for (int p = 0; p < kPasses; ++p) inv[p] += __shfl_xor_sync(0xffffffffu, inv[p], o);
+#pragma unroll
+                for (int p = 0; p < kPasses; ++p) {
+                    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv[p]) : "f"(fmaf(inv[p], 1.f / D, a.eps)));
+                    const F2 inv2 = f2(inv[p], inv[p]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[p][i] = y[p][i] * inv2;
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) {
+                out.x[p][0] = make_uint2(pack16(y[p][0], kF16), pack16(y[p][1], kF16));
+                out.x[p][1] = make_uint2(pack16(y[p][2], kF16), pack16(y[p][3], kF16));
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const int r0 = first_row + p * kRows;  // first row of the pass (warp-uniform)
+            const int r = r0 + lane / kLanes;
+            const bool mine = r < row_end;
+            const uint2 y0 = out.x[p][0], y1 = out.x[p][1];
             uint16_t* dst = nullptr;  // a 16-bit destination row
             if (kind == 0) dst = a.q_out + tok * a.q_out_stride + (long long)r * D;
             else if constexpr (!kAppend) dst = a.k_out + tok * a.k_out_stride + (long long)r * D;
@@ -263,7 +309,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const __grid_con
                             *reinterpret_cast<uint32_t*>(out + off0) = e4m3x4(y0, scale);
                             *reinterpret_cast<uint32_t*>(out + off1) = e4m3x4(y1, scale);
                         }
-                    } else {  // through shared memory, so that one lane sees the 16 elements of a block
+                    } else if (r0 < row_end) {  // through shared memory, so that one lane sees the 16 elements of a block
                         uint16_t* st = stage[warp];
                         *reinterpret_cast<uint2*>(st + (lane / kLanes) * D + off0) = y0;
                         *reinterpret_cast<uint2*>(st + (lane / kLanes) * D + off1) = y1;
@@ -293,17 +339,17 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const __grid_con
 
 template <int D, bool kInterleaved, int kCache, bool kF16>
 cudaError_t launch(NormRopeArgs a, cudaStream_t stream) {
-    constexpr int kRows = 32 / (D / 8) * kPasses;
-    auto warps = [&] {
-        const int per_warp = a.batches * kRows;
-        return (long long)a.total_tokens * ((a.num_q_heads + per_warp - 1) / per_warp +
-                                            (kCache >= 0 ? 2 : 1) * ((a.num_kv_heads + per_warp - 1) / per_warp));
-    };
-    // Rows of a warp share its token's angles and weights, so the more the
-    // better once every SM has its warps anyway.
-    a.batches = 1;
-    if (warps() >= 32768) a.batches = 4;
-    return launch_overlapped(norm_rope_kernel<D, kInterleaved, kCache, kF16>, dim3((unsigned)((warps() + kWarps - 1) / kWarps)),
+    constexpr int kPer = 32 / (D / 8) * kPasses;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long long chunks = (a.num_q_heads + kPer - 1) / kPer + (kCache >= 0 ? 2 : 1) * ((a.num_kv_heads + kPer - 1) / kPer);
+    // As many warps as stay on the SMs; each walks over its share of the tokens.
+    const long long resident = (long long)sms * kCtas * kWarps;
+    a.tokens_per_warp = (int)((a.total_tokens * chunks + resident - 1) / resident);
+    const long long warps = (a.total_tokens + a.tokens_per_warp - 1) / a.tokens_per_warp * chunks;
+    return launch_overlapped(norm_rope_kernel<D, kInterleaved, kCache, kF16>, dim3((unsigned)((warps + kWarps - 1) / kWarps)),
                              dim3(kWarps * 32), 0, stream, a);
 }
 
