@@ -40,6 +40,8 @@ struct Share {
     }
 };
 
+__device__ __forceinline__ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_constant__ AppendArgs a) {
     grid_dependency_wait();
@@ -50,17 +52,14 @@ __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_co
     if (my.tok >= a.total_new) return;
     const int nh = min(kHeads, a.num_kv_heads - my.h0);
     // rows first: they do not depend on the token's place
-    uint4 w[kHeads][2][2];
+    const bool wide = aligned32(a.k_new) && aligned32(a.v_new);
+    Sector w[kHeads][2];
     const long long src = ((long long)my.tok * a.num_kv_heads + my.h0) * D + my.piece * 16;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
         if (i < nh) {
-            const uint4* k = reinterpret_cast<const uint4*>(a.k_new + src + i * D);
-            const uint4* v = reinterpret_cast<const uint4*>(a.v_new + src + i * D);
-            w[i][0][0] = __ldg(k);
-            w[i][0][1] = __ldg(k + 1);
-            w[i][1][0] = __ldg(v);
-            w[i][1][1] = __ldg(v + 1);
+            w[i][0] = load_sector(a.k_new + src + i * D, wide);
+            w[i][1] = load_sector(a.v_new + src + i * D, wide);
         }
     int page, row;
     long long pos;
@@ -75,9 +74,9 @@ __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_co
     for (int i = 0; i < kHeads; ++i)
         if (i < nh) {
             const long long at_head = slab + (long long)i * fp4_slab_bytes(D);
-            fp4_store_block<D>(static_cast<uint8_t*>(a.k_pool) + at_head, row, my.piece, w[i][0][0], w[i][0][1],
+            fp4_store_block<D>(static_cast<uint8_t*>(a.k_pool) + at_head, row, my.piece, w[i][0].lo, w[i][0].hi,
                                __ldg(&a.k_scale[my.h0 + i]));
-            fp4_store_block<D>(static_cast<uint8_t*>(a.v_pool) + at_head, row, my.piece, w[i][1][0], w[i][1][1],
+            fp4_store_block<D>(static_cast<uint8_t*>(a.v_pool) + at_head, row, my.piece, w[i][1].lo, w[i][1].hi,
                                __ldg(&a.v_scale[my.h0 + i]));
         }
 }
@@ -89,7 +88,7 @@ struct Piece {
 };
 
 template <int D, int kType>
-__device__ __forceinline__ Piece<kType> load_piece(const uint8_t* pool, long long slab_index, int row, int piece) {
+__device__ __forceinline__ Piece<kType> load_piece(const uint8_t* pool, long long slab_index, int row, int piece, bool wide) {
     Piece<kType> p;
     if constexpr (kType == PA_KV_FP4_E2M1) {
         const uint8_t* slab = pool + slab_index * fp4_slab_bytes(D);
@@ -98,9 +97,9 @@ __device__ __forceinline__ Piece<kType> load_piece(const uint8_t* pool, long lon
     } else if constexpr (kType == PA_KV_FP8_E4M3) {
         p.raw[0] = __ldg(reinterpret_cast<const uint4*>(pool + (slab_index * kPage + row) * D) + piece);
     } else {
-        const uint4* src = reinterpret_cast<const uint4*>(pool + (slab_index * kPage + row) * (2 * D)) + 2 * piece;
-        p.raw[0] = __ldg(src);
-        p.raw[1] = __ldg(src + 1);
+        const Sector s = load_sector(pool + (slab_index * kPage + row) * (2 * D) + 32 * piece, wide);
+        p.raw[0] = s.lo;
+        p.raw[1] = s.hi;
     }
     return p;
 }
@@ -113,8 +112,8 @@ __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float scale) {
 }
 
 template <int kType>
-__device__ __forceinline__ void store_piece(uint16_t* dst, const Piece<kType>& p, float head) {
-    uint4* out = reinterpret_cast<uint4*>(dst);
+__device__ __forceinline__ void store_piece(uint16_t* dst, const Piece<kType>& p, float head, bool wide) {
+    uint4 out[2];
     if constexpr (kType == PA_KV_FP4_E2M1) {
         // block scale * head scale in fp32: a code has 2 significant bits, so
         // the product with it is within one fp32 rounding of the exact value
@@ -136,6 +135,7 @@ __device__ __forceinline__ void store_piece(uint16_t* dst, const Piece<kType>& p
         out[0] = p.raw[0];
         out[1] = p.raw[1];
     }
+    store_sector(dst, Sector{out[0], out[1]}, wide);
 }
 
 // grid as for append_fp4_kernel
@@ -157,12 +157,13 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
     }
     const int nh = min(kHeads, a.num_kv_heads - my.h0);
     const long long slab = (long long)page * a.num_kv_heads + my.h0;
+    const bool wide_in = aligned32(a.k_pool) && aligned32(a.v_pool), wide_out = aligned32(a.k_out) && aligned32(a.v_out);
     Piece<kType> k[kHeads], v[kHeads];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
         if (i < nh) {
-            k[i] = load_piece<D, kType>(a.k_pool, slab + i, row, my.piece);
-            v[i] = load_piece<D, kType>(a.v_pool, slab + i, row, my.piece);
+            k[i] = load_piece<D, kType>(a.k_pool, slab + i, row, my.piece, wide_in);
+            v[i] = load_piece<D, kType>(a.v_pool, slab + i, row, my.piece, wide_in);
         }
     const long long dst = ((long long)my.tok * a.num_kv_heads + my.h0) * D + my.piece * 16;
 #pragma unroll
@@ -173,8 +174,8 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
                 ks = __ldg(&a.k_scale[my.h0 + i]);
                 vs = __ldg(&a.v_scale[my.h0 + i]);
             }
-            store_piece<kType>(a.k_out + dst + i * D, k[i], ks);
-            store_piece<kType>(a.v_out + dst + i * D, v[i], vs);
+            store_piece<kType>(a.k_out + dst + i * D, k[i], ks, wide_out);
+            store_piece<kType>(a.v_out + dst + i * D, v[i], vs, wide_out);
         }
 }
 

@@ -197,6 +197,33 @@ def test_gather_fp4_bit_exact(d, hk):
         assert np.array_equal(np.where(zero, 0, want), np.where((bits & 0x7FFF) == 0, 0, bits))
 
 
+@pytest.mark.parametrize("kv", ["fp4", "bf16", "e4m3"])
+def test_buffers_of_16_byte_alignment(kv):
+    """Every buffer 16 bytes off a 32-byte boundary gives the bits of aligned ones."""
+    d, hk, n = 64, 3, 150
+    sc = (None, None) if kv == "bf16" else (torch.full((hk,), 0.02, device=DEV), torch.full((hk,), 0.03, device=DEV))
+
+    def off(x):
+        raw = torch.empty(x.numel() * x.element_size() + 16, dtype=torch.uint8, device=DEV)
+        y = raw[16:].view(x.dtype).view(x.shape)
+        assert y.data_ptr() % 32 == 16
+        return y.copy_(x)
+
+    new = [ops.as_bf16(W.bf16_normal(74, s, (n, hk, d)), DEV) for s in (1, 2)]
+    pools = [ops.kv_pool(3, hk, d, kv, DEV) for _ in range(2)]
+    table, cu, start = dev(np.array([[2, 0, 1]], np.int32)), dev(np.array([0, n], np.int32)), dev(np.array([5], np.int32))
+    sh = ops.append_shapes(1, hk, d, 3, 3, n, kv)
+    got = []
+    for wrap in (lambda x: x.clone(), off):
+        kp, vp = wrap(pools[0]), wrap(pools[1])
+        ws = ops.append_kv(sh, wrap(new[0]), wrap(new[1]), cu, start, table, kp, vp, *sc)
+        ko, vo = wrap(torch.zeros_like(new[0])), wrap(torch.zeros_like(new[0]))
+        ops.gather_kv(sh, kp, vp, cu, start, table, *sc, ko, vo, ws)
+        assert B.pa_check_status(ws) == B.PA_OK
+        got.append((kp.view(torch.uint8), vp.view(torch.uint8), ko, vo))
+    assert all(torch.equal(x, y) for x, y in zip(*got)) and got[0][2].any()
+
+
 @pytest.mark.parametrize("kv", ["fp4", "bf16"])
 def test_bad_pages_are_reported_and_skipped(kv):
     d, hk, n = 128, 4, 200
