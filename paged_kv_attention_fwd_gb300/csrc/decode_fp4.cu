@@ -202,6 +202,25 @@ __global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(con
     __syncthreads();
     auto get_item = [&](int j) { return j - it_lo < kItems ? items_sh[j - it_lo] : load_item(a, j, items_off); };
 
+    // Queries are read once and so come from memory: the first item's are asked for before the pages, behind which they
+    // would wait (4 us of a call), the next one's while the warps merge.
+    uint32_t raw[NQ][D / 8];  // as they lie in memory: the head of column g, dims of t
+    auto load_q = [&](int j) {
+        const Item it = get_item(j);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            const int h = NH == 4 ? g >> 1 : n * 8 + g;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                a.q + ((long long)it.b * a.num_q_heads + it.kvh * G + h) * D + t * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 v = h < G ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                raw[n][4 * i] = v.x; raw[n][4 * i + 1] = v.y; raw[n][4 * i + 2] = v.z; raw[n][4 * i + 3] = v.w;
+            }
+        }
+    };
+    if (it_lo < it_hi) load_q(it_lo);
+
     // ---- filling the ring: a cursor over this warp's pages of all items
     int pj = it_lo - 1, pp = 0, pend = 0, pkvh = 0;
     int ids = 0, id_base = 0;     // ids of the warp's next 32 pages of item pj, one per lane
@@ -252,23 +271,6 @@ __global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(con
     };
 #pragma unroll 1
     for (int i = 0; i < S; ++i) fill();
-
-    uint32_t raw[NQ][D / 8];  // the next item's queries, as they lie in memory: the head of column g, dims of t
-    auto load_q = [&](int j) {
-        const Item it = get_item(j);
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            const int h = NH == 4 ? g >> 1 : n * 8 + g;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                a.q + ((long long)it.b * a.num_q_heads + it.kvh * G + h) * D + t * (D / 4));
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint4 v = h < G ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                raw[n][4 * i] = v.x; raw[n][4 * i + 1] = v.y; raw[n][4 * i + 2] = v.z; raw[n][4 * i + 3] = v.w;
-            }
-        }
-    };
-    if (it_lo < it_hi) load_q(it_lo);
 
     // this lane's places in a slab, for the first 16-key block: K row, V keys
     const int krow = key_row(g), vkey0 = key_row(2 * t), vkey1 = key_row(2 * t + 1);
@@ -540,11 +542,12 @@ __global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(con
         const long long head0 = (long long)it.kvh * G;
         const long long orow = partial ? (long long)(it.split_base + it.s) * a.num_q_heads + head0
                                        : (long long)it.b * a.num_q_heads + head0;
-        for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
-            const int h = idx / D, d = idx % D;
+        for (int idx = threadIdx.x; idx < G * (D / 4); idx += kThreads) {  // 4 dims of a head per thread
+            const int h = idx / (D / 4), d = idx % (D / 4) * 4;
             const int ht = NH == 4 ? h : (h >> 1) & 3;  // the t of the lanes that held head h
-            const int slot = h * D + d / (D / 8) * (D / 8) + 4 * ((d % (D / 8) / 4 + ht) & (M4 - 1)) + (d & 3);
-            float mm = kNone, ll = 0.f, val = 0.f;
+            const int slot = h * D + d / (D / 8) * (D / 8) + 4 * ((d % (D / 8) / 4 + ht) & (M4 - 1));
+            float mm = kNone, ll = 0.f;
+            float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, red_m[w][h]);
 #pragma unroll
@@ -553,11 +556,21 @@ __global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(con
                 if (lw == 0.f) continue;                // no live key: nothing was written
                 const float f = ex2(red_m[w][h] - mm);  // a NaN logit leaves a NaN sum, and so a NaN output
                 ll = fmaf(f, lw, ll);
-                val = fmaf(f, reinterpret_cast<const float*>(smem + scratch_at[w])[slot], val);
+                const float4 v = *reinterpret_cast<const float4*>(smem + scratch_at[w] + 4 * slot);
+                val.x = fmaf(f, v.x, val.x);
+                val.y = fmaf(f, v.y, val.y);
+                val.z = fmaf(f, v.z, val.z);
+                val.w = fmaf(f, v.w, val.w);
             }
-            val = ll == 0.f ? 0.f : val * (vs / ll);
-            if (partial) a.o_part[(orow + h) * D + d] = val;
-            else a.out[(orow + h) * D + d] = to_bf16(val);
+            const float r = ll == 0.f ? 0.f : __fdividef(vs, ll);
+            val = make_float4(val.x * r, val.y * r, val.z * r, val.w * r);
+            if (partial) {
+                *reinterpret_cast<float4*>(a.o_part + (orow + h) * D + d) = val;
+            } else {
+                *reinterpret_cast<uint2*>(a.out + (orow + h) * D + d) =
+                    make_uint2((uint32_t)to_bf16(val.x) | ((uint32_t)to_bf16(val.y) << 16),
+                               (uint32_t)to_bf16(val.z) | ((uint32_t)to_bf16(val.w) << 16));
+            }
             if (d == 0) {
                 const float lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
                 if (partial) a.lse_part[orow + h] = lse;
