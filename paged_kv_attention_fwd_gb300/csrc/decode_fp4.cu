@@ -542,25 +542,31 @@ __global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(con
         const long long head0 = (long long)it.kvh * G;
         const long long orow = partial ? (long long)(it.split_base + it.s) * a.num_q_heads + head0
                                        : (long long)it.b * a.num_q_heads + head0;
+        const float* from[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) from[w] = reinterpret_cast<const float*>(smem + scratch_at[w]);
         for (int idx = threadIdx.x; idx < G * (D / 4); idx += kThreads) {  // 4 dims of a head per thread
             const int h = idx / (D / 4), d = idx % (D / 4) * 4;
             const int ht = NH == 4 ? h : (h >> 1) & 3;  // the t of the lanes that held head h
             const int slot = h * D + d / (D / 8) * (D / 8) + 4 * ((d % (D / 8) / 4 + ht) & (M4 - 1));
-            float mm = kNone, ll = 0.f;
-            float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, red_m[w][h]);
+            float mw[kWarps], lw[kWarps], mm = kNone, ll = 0.f;
+            float4 v[kWarps], val = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float lw = red_l[w][h];
-                if (lw == 0.f) continue;                // no live key: nothing was written
-                const float f = ex2(red_m[w][h] - mm);  // a NaN logit leaves a NaN sum, and so a NaN output
-                ll = fmaf(f, lw, ll);
-                const float4 v = *reinterpret_cast<const float4*>(smem + scratch_at[w] + 4 * slot);
-                val.x = fmaf(f, v.x, val.x);
-                val.y = fmaf(f, v.y, val.y);
-                val.z = fmaf(f, v.z, val.z);
-                val.w = fmaf(f, v.w, val.w);
+                mw[w] = red_m[w][h];
+                lw[w] = red_l[w][h];
+                v[w] = *reinterpret_cast<const float4*>(from[w] + slot);
+                mm = fmaxf(mm, mw[w]);
+            }
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const bool any = lw[w] != 0.f;                // else no live key, and the buffer holds anything;
+                const float f = any ? ex2(mw[w] - mm) : 0.f;  // a NaN logit leaves a NaN sum, and so a NaN output
+                ll = fmaf(f, lw[w], ll);
+                val.x = fmaf(f, any ? v[w].x : 0.f, val.x);
+                val.y = fmaf(f, any ? v[w].y : 0.f, val.y);
+                val.z = fmaf(f, any ? v[w].z : 0.f, val.z);
+                val.w = fmaf(f, any ? v[w].w : 0.f, val.w);
             }
             const float r = ll == 0.f ? 0.f : __fdividef(vs, ll);
             val = make_float4(val.x * r, val.y * r, val.z * r, val.w * r);
