@@ -113,12 +113,14 @@ typedef struct {
  *
  * Split rule (integers only, deterministic):
  *   pages_b = ceil(len_b / 64); units = sum_b pages_b * Hk;
- *   cap = num_sms * ctas_per_sm; chunk = max(4, ceil(units / (2 * cap)));
+ *   cap = num_sms * ctas_per_sm; chunk = max(4, ceil(units / (2 * cap)))
+ *   (with 4-bit pages ceil(units / cap));
  *   n_b = 1 if pages_b <= 1, else min(forced, pages_b, 64) if forced > 0,
  *   else min(ceil(pages_b / chunk), 64).  Split s of b covers pages
  *   [floor(s * pages_b / n_b), floor((s + 1) * pages_b / n_b)).
- * Work items (b, s, kv head), cost = pages + 1, are dealt longest first to the
- * least-loaded of grid = min(#items, cap) CTAs (ties: lowest index).
+ * Work items (b, s, kv head), cost = pages + 1 (4-bit pages: pages + 6), are
+ * dealt longest first to the least-loaded of grid = min(#items, cap) CTAs
+ * (ties: lowest index).
  *
  * Packed layout (int32): [0] 0x50414D31 [1] B [2] Hk [3] total_splits
  * [4] num_items [5] grid [6] chunk [7] ctas_per_sm, then n_splits[B],
@@ -138,8 +140,8 @@ pa_status pa_get_metadata(const int32_t* seq_lens_host, const int32_t* block_tab
  *
  * pa_get_static_plan (host, no lengths): a plan that covers every length mix
  * of `batch` sequences -- the split rule yields at most
- * batch + ceil(2 * num_sms * ctas_per_sm / Hk) splits (batch * min(forced, 64)
- * with forced splits).  Use it for pa_decode and for sizing the metadata
+ * batch + ceil(2 * num_sms * ctas_per_sm / Hk) splits (4-bit pages: without the
+ * 2; batch * min(forced, 64) with forced splits).  Use it for pa_decode and for sizing the metadata
  * buffer (plan->meta_ints) and the workspace.  Limits: batch <= 8192, at most
  * 16384 work items (splits * Hk); PA_ERR_UNSUPPORTED beyond.
  *

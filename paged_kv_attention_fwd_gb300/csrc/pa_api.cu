@@ -170,6 +170,12 @@ int resolve_ctas_per_sm(const pa_decode_shapes* sh) {
     return pa::kFp4CtasPerSm;
 }
 
+// Work items a CTA's share is cut into.  An item of 4-bit pages costs as much
+// beside its pages as six of them (below), so those are cut half as fine: 64
+// sequences of up to 4096 keys XX us a call against 39.5, 128 of up to 8192
+// YY against 113.8.
+int items_per_share(const pa_decode_shapes* sh) { return sh->kv_dtype == PA_KV_FP4_E2M1 ? 1 : 2; }
+
 }  // namespace
 
 namespace pa {
@@ -228,7 +234,7 @@ pa_status pa_get_metadata(const int32_t* seq_lens_host, const int32_t* block_tab
         }
     }
     const int64_t cap = (int64_t)sh->num_sms * cps;
-    const int64_t chunk = std::max<int64_t>(4, cdiv(units, 2 * cap));  // two items per CTA share
+    const int64_t chunk = std::max<int64_t>(4, cdiv(units, items_per_share(sh) * cap));
     std::vector<int32_t> nsplit(B), indptr(B + 1, 0);
     for (int b = 0; b < B; ++b) {
         int n;
@@ -239,13 +245,18 @@ pa_status pa_get_metadata(const int32_t* seq_lens_host, const int32_t* block_tab
         indptr[b + 1] = indptr[b] + n;
     }
     const int64_t total_splits = indptr[B];
+    // What an item costs beside its pages, in pages.  4-bit pages are quick to
+    // take (0.40 us each in one of an SM's three CTAs) next to an item's ends
+    // (2.6 us); counted as 1, CTAs of three short items ended a batch of 64
+    // sequences 36 us in, those of two 26.
+    const int item_cost = sh->kv_dtype == PA_KV_FP4_E2M1 ? 6 : 1;
     std::vector<SchedItem> items;
     items.reserve((size_t)total_splits * Hk);
     for (int b = 0; b < B; ++b)
         for (int s = 0; s < nsplit[b]; ++s) {
             const int lo = (int)((int64_t)s * pages[b] / nsplit[b]);
             const int hi = (int)((int64_t)(s + 1) * pages[b] / nsplit[b]);
-            for (int g = 0; g < Hk; ++g) items.push_back({hi - lo + 1, (int)items.size(), b, s, g});
+            for (int g = 0; g < Hk; ++g) items.push_back({hi - lo + item_cost, (int)items.size(), b, s, g});
         }
     const int64_t nitems = (int64_t)items.size();
     const int64_t grid = std::min<int64_t>(nitems, cap);
@@ -1201,7 +1212,7 @@ pa_status pa_get_static_plan(const pa_decode_shapes* sh, pa_decode_plan* plan) {
     const int cps = resolve_ctas_per_sm(sh);
     const int64_t cap = (int64_t)sh->num_sms * cps;
     const int64_t splits = sh->forced_splits > 0 ? (int64_t)B * std::min(sh->forced_splits, PA_MAX_SPLITS)
-                                                 : B + cdiv(2 * cap, Hk);
+                                                 : B + cdiv(items_per_share(sh) * cap, Hk);
     const int64_t items = splits * Hk;
     if (items > 16384) return fail(PA_ERR_UNSUPPORTED, "device scheduling handles up to 16384 work items (%lld)",
                                    (long long)items);
@@ -1233,7 +1244,8 @@ pa_status pa_get_metadata_device(const pa_decode_shapes* sh, const pa_decode_pla
     const size_t smem = pa::schedule_smem_bytes(sh->batch, p2);
     if (smem > 227 * 1024) return fail(PA_ERR_UNSUPPORTED, "schedule needs %zu bytes of shared memory", smem);
     cudaError_t e = pa::launch_schedule(seq_lens_dev, sh->batch, sh->num_kv_heads, sh->max_pages_per_seq,
-                                        plan->ctas_per_sm, plan->grid, sh->forced_splits, p2, meta_dev, stream);
+                                        plan->ctas_per_sm, plan->grid, items_per_share(sh), sh->forced_splits, p2,
+                                        meta_dev, stream);
     if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
     return PA_OK;
 }

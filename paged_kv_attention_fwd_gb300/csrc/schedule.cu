@@ -71,8 +71,8 @@ __device__ void block_exclusive_scan(const int* in, int* out, int n, int* tmp) {
 // T threads; below 1024 the launcher gives at most one sort key a thread
 template <int T>
 __global__ void __launch_bounds__(T, 1)
-    schedule_kernel(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int forced,
-                    int p2cap, int32_t* meta) {
+    schedule_kernel(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int per_share,
+                    int forced, int p2cap, int32_t* meta) {
     constexpr int kPer = T == kMaxThreads ? kMaxPer : 4;
     allow_dependents_launch();  // the decode kernel's prologue overlaps this one
     extern __shared__ unsigned long long dyn[];
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(T, 1)
         local += p;
     }
     const long long units = block_sum(local, tmp64) * Hk;
-    const long long shares = 2LL * cap;  // two items per CTA share
+    const long long shares = (long long)per_share * cap;  // items per CTA share: two, or one (4-bit pages)
     const long long chunk = max(4LL, (units + shares - 1) / shares);
     for (int b = threadIdx.x; b < B; b += T) {
         const int p = pages[b];
@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(kPtThreads) page_table_kernel(const int32_t* _
 
 size_t schedule_smem_bytes(int B, int p2cap) { return (size_t)p2cap * 8 + (size_t)(3 * B + 1) * 4; }
 
-cudaError_t launch_schedule(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int forced,
-                            int p2cap, int32_t* meta, cudaStream_t stream) {
+cudaError_t launch_schedule(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int per_share,
+                            int forced, int p2cap, int32_t* meta, cudaStream_t stream) {
     const size_t smem = schedule_smem_bytes(B, p2cap);
     // a power of two with one sort key and at most 4 sequences a thread, up to
     // 1024 threads (then at most kMaxPer = 16 keys, p2cap <= 16384); the e4m3
@@ -305,7 +305,7 @@ cudaError_t launch_schedule(const int32_t* seq_lens, int B, int Hk, int max_page
     auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
         cudaError_t e = ensure_dynamic_smem(kernel, (int)schedule_smem_bytes(kMaxBatch, 16384), done);
         if (e != cudaSuccess) return e;
-        kernel<<<1, threads, smem, stream>>>(seq_lens, B, Hk, max_pages, cps, cap, forced, p2cap, meta);
+        kernel<<<1, threads, smem, stream>>>(seq_lens, B, Hk, max_pages, cps, cap, per_share, forced, p2cap, meta);
         return cudaGetLastError();
     };
     switch (threads) {

@@ -28,7 +28,7 @@ def test_plan_uses_three_ctas_per_sm_by_default():
     lens = np.array([10, 3000, 0, 777], np.int32)
     for cps, want in ((0, 3), (1, 1), (5, 5)):
         meta, plan = B.pa_get_metadata(lens, None, shapes(4, sms=7, cps=cps, kv=B.PA_KV_FP4_E2M1))
-        assert plan.ctas_per_sm == want and meta.tolist() == S.schedule(lens.tolist(), 8, 7, want, 0)
+        assert plan.ctas_per_sm == want and meta.tolist() == S.schedule(lens.tolist(), 8, 7, want, 0, item_cost=6)
     assert B.pa_get_static_plan(shapes(4, cps=0, kv=B.PA_KV_FP4_E2M1)).ctas_per_sm == 3
     assert B.pa_get_static_plan(shapes(4, cps=0)).ctas_per_sm == 1
 
