@@ -58,12 +58,16 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kSlack = 8.f;
 constexpr float kNone = -3e38f;  // the running maximum before any key: finite, so that its differences are
 
-// D: head dim
-template <int D>
+// D: head dim; NH: query heads of a KV group the kernel has room for (4, 8 or 16)
+template <int D, int NH>
 struct Layout {
     static constexpr int kSlab = fp4_slab_bytes(D);
     static constexpr int kStage = 2 * kSlab;  // K slab, V slab
-    static constexpr int kStages = D == 128 ? 2 : 4;
+    // CTAs of an SM.  Past 8 heads two with up to 255 registers a thread: three
+    // spill (64 sequences of up to 8192 keys, 16 heads a group: 114 us a call, 98
+    // with two).
+    static constexpr int kCtas = fp4_ctas_per_sm(NH);
+    static constexpr int kStages = (NH == 16 ? 3 : 2) * (D == 128 ? 1 : 2);
     static constexpr int kRing = kStages * kStage;  // of one warp
     static constexpr int kBytes = kWarps * kRing;
     static_assert(16 * D * 4 <= kStage, "a warp's output (16 heads) must fit a page buffer");
@@ -163,10 +167,10 @@ __device__ __forceinline__ int key_row(int k) { return k ^ ((k >> 1) & 1); }
 
 // D: head dim; NH: query heads of a KV group it has room for (4, 8 or 16)
 template <int D, int NH>
-__global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(const __grid_constant__ DecodeArgs a) {
-    using L = Layout<D>;
+__global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_kernel(const __grid_constant__ DecodeArgs a) {
+    using L = Layout<D, NH>;
     constexpr int S = L::kStages;
-    constexpr int KB = NH == 16 ? 2 : 4;             // 16-key blocks of a softmax step
+    constexpr int KB = kPage / 16;                   // 16-key blocks of a page
     constexpr int KK = D / 16;                       // MMA steps over the dims of QK
     constexpr int NQ = NH == 16 ? 2 : 1;             // column tiles of S^T and O^T
     constexpr int MT = NH == 4 ? D / 32 : D / 16;    // row tiles of O^T
@@ -334,12 +338,8 @@ __global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(con
             }
             --in_ring;
             const uint32_t so = st * L::kStage;
-            const int page_live = (dead >> st) & 1u ? 0 : key_end - p * kPage;  // live keys (64 or more: all)
-#pragma unroll 1
-            for (int r0 = 0; r0 < kPage; r0 += KB * 16) {
-                const int live = page_live - r0;
-                if (live <= 0) break;
-                const uint32_t ko = so + r0 * (D / 2);
+            const int live = (dead >> st) & 1u ? 0 : key_end - p * kPage;  // live keys (64 or more: all)
+            if (live > 0) {
                 // ---- S^T = K q^T
                 float c[NQ][KB][4];
 #pragma unroll
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(con
                     uint32_t w[2][D / 32], sc[2][D / 64];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint8_t* src = kbase + ko + (blk * 16 + 8 * i) * (D / 2);
-                        const uint8_t* scl = kscale + so + (r0 + blk * 16 + 8 * i) * (D / 16);
+                        const uint8_t* src = kbase + so + (blk * 16 + 8 * i) * (D / 2);
+                        const uint8_t* scl = kscale + so + (blk * 16 + 8 * i) * (D / 16);
                         if constexpr (D == 128) {
                             const uint4 v = *reinterpret_cast<const uint4*>(src);
                             w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(con
                 for (int i = 0; i < HL; ++i)
 #pragma unroll
                     for (int k = 0; k < 2 * KB; ++k) x[i][k] = c[i >> 1][k >> 1][2 * (k & 1) + (NH == 4 ? 0 : i & 1)];
-                const bool tail = live < KB * 16;
+                const bool tail = live < kPage;
                 if (tail) {
 #pragma unroll
                     for (int k = 0; k < 2 * KB; ++k)
@@ -443,13 +443,13 @@ __global__ void __launch_bounds__(kThreads, kFp4CtasPerSm) decode_fp4_kernel(con
                     for (int i = 0; i < 4; ++i) {
                         const int key = (i & 1 ? vkey1 : vkey0) + 8 * (i >> 1) + 16 * blk;
                         if constexpr (D == 128) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(vslab + ko + key * 64 + g * 8);
+                            const uint2 v = *reinterpret_cast<const uint2*>(vslab + so + key * 64 + g * 8);
                             w[i][0] = v.x;
                             w[i][1] = v.y;
-                            b[i] = vslab[so + kPage * 64 + (r0 + key) * 8 + g];
+                            b[i] = vslab[so + kPage * 64 + key * 8 + g];
                         } else {
-                            w[i][0] = *reinterpret_cast<const uint32_t*>(vslab + ko + key * 32 + g * 4);
-                            b[i] = vslab[so + kPage * 32 + (r0 + key) * 4 + (g >> 1)];
+                            w[i][0] = *reinterpret_cast<const uint32_t*>(vslab + so + key * 32 + g * 4);
+                            b[i] = vslab[so + kPage * 32 + key * 4 + (g >> 1)];
                         }
                     }
                     if (tail) {  // a dead key's scale may be a NaN, which a zero P would not cancel
@@ -658,9 +658,9 @@ __global__ void __launch_bounds__(128) combine_fp4_kernel(const __grid_constant_
 template <int D, int NH>
 cudaError_t launch_d(const DecodeArgs& a, int grid, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = ensure_dynamic_smem(decode_fp4_kernel<D, NH>, Layout<D>::kBytes, done);
+    cudaError_t e = ensure_dynamic_smem(decode_fp4_kernel<D, NH>, Layout<D, NH>::kBytes, done);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(decode_fp4_kernel<D, NH>, dim3((unsigned)grid), dim3(kThreads), Layout<D>::kBytes, stream, a);
+    return launch_overlapped(decode_fp4_kernel<D, NH>, dim3((unsigned)grid), dim3(kThreads), Layout<D, NH>::kBytes, stream, a);
 }
 
 template <int D>

@@ -55,8 +55,8 @@ struct CombineArgs {
 cudaError_t launch_decode(int head_dim, bool fp8, const DecodeArgs& a, const CUtensorMap* map_k,
                           const CUtensorMap* map_v, const CUtensorMap* map_q, int grid, cudaStream_t stream);
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
-// 4-bit pages (decode_fp4.cu); kFp4CtasPerSm of its CTAs fit on one SM
-constexpr int kFp4CtasPerSm = 3;
+// 4-bit pages (decode_fp4.cu): CTAs that fit on one SM, by query heads per KV head
+__host__ __device__ constexpr int fp4_ctas_per_sm(int group) { return group > 8 ? 2 : 3; }
 cudaError_t launch_decode_fp4(int head_dim, const DecodeArgs& a, int grid, cudaStream_t stream);
 // merges the splits that launch_decode_fp4 left in a.o_part and a.lse_part
 cudaError_t launch_combine_fp4(int head_dim, const DecodeArgs& a, cudaStream_t stream);

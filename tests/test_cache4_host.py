@@ -24,12 +24,36 @@ def test_slab_bytes():
     assert B.pa_page_slab_bytes(96, 3) == 0 and B.pa_page_slab_bytes(128, 4) == 0
 
 
-def test_plan_uses_three_ctas_per_sm_by_default():
-    lens = np.array([10, 3000, 0, 777], np.int32)
-    for cps, want in ((0, 3), (1, 1), (5, 5)):
-        meta, plan = B.pa_get_metadata(lens, None, shapes(4, sms=7, cps=cps, kv=B.PA_KV_FP4_E2M1))
-        assert plan.ctas_per_sm == want and meta.tolist() == S.schedule(lens.tolist(), 8, 7, want, 0, item_cost=6)
-    assert B.pa_get_static_plan(shapes(4, cps=0, kv=B.PA_KV_FP4_E2M1)).ctas_per_sm == 3
+def plain_plan(lens, hk, cap, forced):
+    """(splits per sequence, items of each CTA) of the 4-bit rule: one item per CTA share, an item counts pages + 6."""
+    pages = [-(-n // 64) for n in lens]
+    chunk = max(4, -(-sum(pages) * hk // cap))
+    n = [1 if p <= 1 else min(forced, p, 64) if forced else min(-(-p // chunk), 64) for p in pages]
+    items = [((s + 1) * p // k - s * p // k + 6, b, s, g) for b, (p, k) in enumerate(zip(pages, n)) for s in range(k)
+             for g in range(hk)]
+    ctas = [[] for _ in range(min(len(items), cap))]
+    loads = [[0, c] for c in range(len(ctas))]
+    for cost, b, s, g in sorted(items, key=lambda i: -i[0]):  # stable: ties keep their order
+        least = min(loads)
+        least[0] += cost
+        ctas[least[1]].append((b, s, g))
+    return n, ctas
+
+
+@pytest.mark.parametrize("lens,hq,forced", [([10, 3000, 0, 777], 32, 0), ([5000], 32, 0), ([4096] * 9, 128, 0),
+                                            (list(range(0, 4000, 130)), 32, 0), ([640, 1000], 64, 5)])
+def test_plan_of_4_bit_pages(lens, hq, forced):
+    for cps, want in ((0, 2 if hq > 64 else 3), (1, 1), (5, 5)):
+        sh = shapes(len(lens), hq=hq, max_pages=80, sms=7, cps=cps, forced=forced, kv=B.PA_KV_FP4_E2M1)
+        meta, plan = B.pa_get_metadata(np.array(lens, np.int32), None, sh)
+        u = S.unpack(meta.tolist())
+        n, ctas = plain_plan(lens, 8, 7 * want, forced)
+        assert plan.ctas_per_sm == u["ctas_per_sm"] == want and u["n_splits"] == n and u["grid"] == len(ctas)
+        ptr = u["cta_indptr"]
+        assert [u["items"][ptr[c]:ptr[c + 1]] for c in range(len(ctas))] == ctas
+        static = B.pa_get_static_plan(sh)
+        assert static.total_splits >= u["total_splits"] and static.grid >= u["grid"]
+        assert static.meta_ints >= plan.meta_ints and static.workspace_bytes >= plan.workspace_bytes
     assert B.pa_get_static_plan(shapes(4, cps=0)).ctas_per_sm == 1
 
 
