@@ -31,12 +31,10 @@ struct Share {
           tok(tok0 + (int)(threadIdx.x & 31) / kLanes),
           piece((int)(threadIdx.x & 31) % kLanes),
           h0((int)blockIdx.y * kHeads) {}
-    // the sequence that holds this thread's token; the whole warp calls it
-    __device__ __forceinline__ int sequence(const int32_t* __restrict__ cu, int batch) const {
-        int b = max(warp_sequence(tok0, cu, batch), 0);
-        if (tok < __ldg(&cu[b])) return -1;
-        while (b < batch && __ldg(&cu[b + 1]) <= tok) ++b;
-        return b;
+    // that of this thread's token; the whole warp calls it
+    __device__ __forceinline__ Sequence sequence(const int32_t* __restrict__ cu, const int32_t* __restrict__ start_pos,
+                                                 int batch) const {
+        return warp_sequences<kTokens>(tok0, tok - tok0, cu, start_pos, batch);
     }
 };
 
@@ -48,8 +46,6 @@ __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_co
     allow_dependents_launch();
     const Share<D> my;
     if (my.tok0 >= a.total_new) return;
-    const int b = my.sequence(a.cu_new, a.batch);
-    if (my.tok >= a.total_new) return;
     const int nh = min(kHeads, a.num_kv_heads - my.h0);
     // rows first: they do not depend on the token's place
     const bool wide = aligned32(a.k_new) && aligned32(a.v_new);
@@ -57,14 +53,15 @@ __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_co
     const long long src = ((long long)my.tok * a.num_kv_heads + my.h0) * D + my.piece * 16;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
-        if (i < nh) {
+        if (i < nh && my.tok < a.total_new) {
             w[i][0] = load_sector(a.k_new + src + i * D, wide);
             w[i][1] = load_sector(a.v_new + src + i * D, wide);
         }
+    const Sequence seq = my.sequence(a.cu_new, a.start_pos, a.batch);
+    if (my.tok >= a.total_new) return;
     int page, row;
     long long pos;
-    const Place at = token_place(my.tok, b, a.cu_new, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages,
-                                 page, row, pos);
+    const Place at = token_place(my.tok, seq, a.block_table, a.batch, a.max_pages, a.num_pool_pages, page, row, pos);
     if (at != Place::kOk) {
         if (my.piece == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         return;
@@ -145,12 +142,11 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
     allow_dependents_launch();
     const Share<D> my;
     if (my.tok0 >= a.total) return;
-    const int b = my.sequence(a.cu, a.batch);
+    const Sequence seq = my.sequence(a.cu, a.start_pos, a.batch);
     if (my.tok >= a.total) return;
     int page, row;
     long long pos;
-    const Place at =
-        token_place(my.tok, b, a.cu, a.start_pos, a.block_table, a.batch, a.max_pages, a.num_pool_pages, page, row, pos);
+    const Place at = token_place(my.tok, seq, a.block_table, a.batch, a.max_pages, a.num_pool_pages, page, row, pos);
     if (at != Place::kOk) {
         if (my.piece == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         return;

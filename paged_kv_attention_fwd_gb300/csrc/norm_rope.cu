@@ -168,10 +168,20 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
         int page, row;
         Place place;
     };
+    // Tokens come in order: the sequence is searched for where it changes, its block table read where the page does.
+    Sequence seq{-1, 0, 0};
+    int seq_end = tok0;  // the first token that is not seq's
     auto find_place = [&](Where& to, Pos& pos, int tok) {
-        long long cpos = 0;
-        to.place = token_place(tok, warp_sequence(tok, a.cu_new, a.batch), a.cu_new, a.start_pos, a.block_table,
-                               a.batch, a.max_pages, a.num_pool_pages, to.page, to.row, cpos);
+        if (tok >= seq_end) {
+            seq = warp_sequences<1>(tok, 0, a.cu_new, a.start_pos, a.batch);
+            seq_end = seq.b >= a.batch ? 0x7FFFFFFF : seq.b < 0 ? tok + 1 : __ldg(&a.cu_new[seq.b + 1]);
+            to.row = kPage - 1;
+        }
+        long long cpos = (long long)seq.start + (tok - seq.cu);
+        if (to.row == kPage - 1 || to.place != Place::kOk)
+            to.place = token_place(tok, seq, a.block_table, a.batch, a.max_pages, a.num_pool_pages, to.page, to.row, cpos);
+        else
+            ++to.row;
         if (by_place) {
             const int p = to.place == Place::kOk ? (int)min(cpos, (long long)a.max_position) : 0;
             pos.at[0] = pos.at[1] = pos.at[2] = p;
