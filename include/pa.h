@@ -118,9 +118,8 @@ typedef struct {
  *   n_b = 1 if pages_b <= 1, else min(forced, pages_b, 64) if forced > 0,
  *   else min(ceil(pages_b / chunk), 64).  Split s of b covers pages
  *   [floor(s * pages_b / n_b), floor((s + 1) * pages_b / n_b)).
- * Work items (b, s, kv head), cost = pages + 1 (4-bit pages: pages + 6), are
- * dealt longest first to the least-loaded of grid = min(#items, cap) CTAs
- * (ties: lowest index).
+ * Work items (b, s, kv head), cost = pages + 1, are dealt longest first to the
+ * least-loaded of grid = min(#items, cap) CTAs (ties: lowest index).
  *
  * Packed layout (int32): [0] 0x50414D31 [1] B [2] Hk [3] total_splits
  * [4] num_items [5] grid [6] chunk [7] ctas_per_sm, then n_splits[B],

@@ -545,7 +545,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
         const float* from[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) from[w] = reinterpret_cast<const float*>(smem + scratch_at[w]);
-        for (int idx = threadIdx.x; idx < G * (D / 4); idx += kThreads) {  // 4 dims of a head per thread
+#pragma unroll
+        for (int i = 0; i < (NH * D / 4 + kThreads - 1) / kThreads; ++i) {  // 4 dims of a head per thread
+            const int idx = threadIdx.x + i * kThreads;
+            if (idx >= G * (D / 4)) break;
             const int h = idx / (D / 4), d = idx % (D / 4) * 4;
             const int ht = NH == 4 ? h : (h >> 1) & 3;  // the t of the lanes that held head h
             const int slot = h * D + d / (D / 8) * (D / 8) + 4 * ((d % (D / 8) / 4 + ht) & (M4 - 1));

@@ -170,10 +170,10 @@ int resolve_ctas_per_sm(const pa_decode_shapes* sh) {
     return pa::fp4_ctas_per_sm(sh->num_q_heads > 8 * (int64_t)sh->num_kv_heads ? 16 : 8);
 }
 
-// Work items a CTA's share is cut into.  An item of 4-bit pages costs as much
-// beside its pages as six of them (below), so those are cut half as fine: 64
-// sequences of up to 4096 keys 37.6 us a call against 39.5, 128 of up to 8192
-// 111.6 against 113.8.
+// Work items a CTA's share is cut into.  4-bit pages are quick to take (0.4 us
+// each in one of an SM's three CTAs) next to the ends of an item (2.5 us), so
+// they are cut half as fine: 64 sequences of up to 4096 keys 37.6 us a call
+// against 39.7, 128 of up to 8192 111.6 against 114.0.
 int items_per_share(const pa_decode_shapes* sh) { return sh->kv_dtype == PA_KV_FP4_E2M1 ? 1 : 2; }
 
 }  // namespace
@@ -245,18 +245,13 @@ pa_status pa_get_metadata(const int32_t* seq_lens_host, const int32_t* block_tab
         indptr[b + 1] = indptr[b] + n;
     }
     const int64_t total_splits = indptr[B];
-    // What an item costs beside its pages, in pages.  4-bit pages are quick to
-    // take (0.40 us each in one of an SM's three CTAs) next to an item's ends
-    // (2.6 us); counted as 1, CTAs of three short items ended a batch of 64
-    // sequences 36 us in, those of two 26.
-    const int item_cost = sh->kv_dtype == PA_KV_FP4_E2M1 ? 6 : 1;
     std::vector<SchedItem> items;
     items.reserve((size_t)total_splits * Hk);
     for (int b = 0; b < B; ++b)
         for (int s = 0; s < nsplit[b]; ++s) {
             const int lo = (int)((int64_t)s * pages[b] / nsplit[b]);
             const int hi = (int)((int64_t)(s + 1) * pages[b] / nsplit[b]);
-            for (int g = 0; g < Hk; ++g) items.push_back({hi - lo + item_cost, (int)items.size(), b, s, g});
+            for (int g = 0; g < Hk; ++g) items.push_back({hi - lo + 1, (int)items.size(), b, s, g});
         }
     const int64_t nitems = (int64_t)items.size();
     const int64_t grid = std::min<int64_t>(nitems, cap);

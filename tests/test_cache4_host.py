@@ -25,11 +25,11 @@ def test_slab_bytes():
 
 
 def plain_plan(lens, hk, cap, forced):
-    """(splits per sequence, items of each CTA) of the 4-bit rule: one item per CTA share, an item counts pages + 6."""
+    """(splits per sequence, items of each CTA) of the 4-bit rule: one item per CTA share."""
     pages = [-(-n // 64) for n in lens]
     chunk = max(4, -(-sum(pages) * hk // cap))
     n = [1 if p <= 1 else min(forced, p, 64) if forced else min(-(-p // chunk), 64) for p in pages]
-    items = [((s + 1) * p // k - s * p // k + 6, b, s, g) for b, (p, k) in enumerate(zip(pages, n)) for s in range(k)
+    items = [((s + 1) * p // k - s * p // k + 1, b, s, g) for b, (p, k) in enumerate(zip(pages, n)) for s in range(k)
              for g in range(hk)]
     ctas = [[] for _ in range(min(len(items), cap))]
     loads = [[0, c] for c in range(len(ctas))]
