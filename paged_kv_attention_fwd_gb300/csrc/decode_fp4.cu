@@ -477,6 +477,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                             }
                         }
                     } else {
+                        // codes of one dim of two keys side by side: even and odd dims of a pair of keys' words
+                        uint32_t even[2][D / 64], odd[2][D / 64];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int k = 0; k < D / 64; ++k) {
+                                const uint32_t wa = w[2 * i][k], wb = w[2 * i + 1][k];
+                                even[i][k] = (wa & 0x0F0F0F0Fu) | ((wb << 4) & 0xF0F0F0F0u);
+                                odd[i][k] = ((wa >> 4) & 0x0F0F0F0Fu) | (wb & 0xF0F0F0F0u);
+                            }
                         uint32_t pb[NQ][2];
 #pragma unroll
                         for (int n = 0; n < NQ; ++n)
@@ -485,12 +495,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                                 pb[n][r] = transpose8x8(pack_half2(x[2 * n][2 * blk + r], x[(2 * n + 1) % HL][2 * blk + r]));
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
-                            const uint32_t h0 = code_pair(w[0][mt / 4], mt & 3), h1 = code_pair(w[1][mt / 4], mt & 3);
-                            const uint32_t h2 = code_pair(w[2][mt / 4], mt & 3), h3 = code_pair(w[3][mt / 4], mt & 3);
-                            const uint32_t a0 = mul2(__byte_perm(h0, h1, 0x5410), s01);
-                            const uint32_t a1 = mul2(__byte_perm(h0, h1, 0x7632), s01);
-                            const uint32_t a2 = mul2(__byte_perm(h2, h3, 0x5410), s23);
-                            const uint32_t a3 = mul2(__byte_perm(h2, h3, 0x7632), s23);
+                            const uint32_t a0 = mul2(code_pair(even[0][mt / 4], mt & 3), s01);
+                            const uint32_t a1 = mul2(code_pair(odd[0][mt / 4], mt & 3), s01);
+                            const uint32_t a2 = mul2(code_pair(even[1][mt / 4], mt & 3), s23);
+                            const uint32_t a3 = mul2(code_pair(odd[1][mt / 4], mt & 3), s23);
 #pragma unroll
                             for (int n = 0; n < NQ; ++n) mma16816(o[n][mt], a0, a1, a2, a3, pb[n][0], pb[n][1]);
                         }
