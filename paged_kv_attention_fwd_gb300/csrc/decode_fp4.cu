@@ -21,14 +21,22 @@
 //       scale blocks, one load per row;
 //   V   lane (g, t) takes dims [g D/8, (g + 1) D/8) of 4 keys: inside one
 //       scale block, one load per key.
-// A byte of V converts to two dims of one key, where an A operand wants two
-// keys of one dim side by side.  Up to 8 heads the products are arranged
-// around that instead of permuting: the contraction runs over (key, parity of
-// the dim) with P^T holding, for each head, one column with zeros at odd dims
-// and one with zeros at even ones.  That doubles the columns: with up to 4
-// heads they fill the 8 there are, with up to 8 it costs 8 more MMAs per 16
-// keys and saves 32 permutes; past 8 heads the MMAs would bound, and the
-// halves are permuted.
+// A byte of V holds two dims of one key, where an A operand wants two keys of
+// one dim side by side.  Past 4 heads the words of two keys trade nibbles
+// before the conversion (a shift and a select per 4 bytes).  Up to 4 heads,
+// whose columns fill half of N, the contraction runs over (key, parity of the
+// dim) instead, with one column of P^T per head for each parity, zero at the
+// other: no trade, half the softmax (a lane holds one head) and half the
+// output registers.  For 8 heads that costs 8 more MMAs per 16 keys and
+// measured slower (57 sequences of 8192 keys: 98 us a call against 92).
+//
+// Measured: 57 sequences of 8192 keys, 8 KV heads, D = 128 (539 MB), 83 us a
+// call with 4 query heads per KV head (6.5 TB/s, the memory's rate), 88 with 8
+// (issue slots: 250 instructions per 16 keys, 12 warps an SM), 145 with 16
+// (twice the MMAs, 8 warps an SM).  Shorter batches also see an item's ends
+// (about 2.5 us), 3 us until the first pages are asked for, and 2 to 3 us of
+// the merge kernel: 64 sequences of up to 4096 keys 37 us a call, where the
+// bytes alone take 23.
 //
 // code * scale is exact in fp16, so nothing is lost before the fp32
 // accumulators; P is rounded to fp16 (relative 2^-12) and q, scaled by a
@@ -137,6 +145,14 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+// a times the low or the high half of s (the product takes a broadcast half as it is)
+template <bool kHigh>
+__device__ __forceinline__ uint32_t mul2_by(uint32_t a, uint32_t s) {
+    const __half2 x = *reinterpret_cast<const __half2*>(&a), y = *reinterpret_cast<const __half2*>(&s);
+    const __half2 r = __hmul2(x, kHigh ? __high2half2(y) : __low2half2(y));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -344,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                 float c[NQ][KB][4];
 #pragma unroll
                 for (int blk = 0; blk < KB; ++blk) {
-                    uint32_t w[2][D / 32], sc[2][D / 64];
+                    uint32_t w[2][D / 32], sc[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint8_t* src = kbase + so + (blk * 16 + 8 * i) * (D / 2);
@@ -352,22 +368,22 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                         if constexpr (D == 128) {
                             const uint4 v = *reinterpret_cast<const uint4*>(src);
                             w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-                            const uint32_t h = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(scl));
-                            sc[i][0] = __byte_perm(h, 0, 0x1010);
-                            sc[i][1] = __byte_perm(h, 0, 0x3232);
+                            sc[i] = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(scl));
                         } else {
                             const uint2 v = *reinterpret_cast<const uint2*>(src);
                             w[i][0] = v.x; w[i][1] = v.y;
-                            sc[i][0] = __byte_perm(e4m3x2_to_half2(*scl), 0, 0x1010);
+                            sc[i] = e4m3x2_to_half2(*scl);
                         }
                     }
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk) {
                         const int wi = kk / 2, byte = (kk & 1) * 2;
-                        const uint32_t a0 = mul2(code_pair(w[0][wi], byte), sc[0][wi / 2]);
-                        const uint32_t a1 = mul2(code_pair(w[1][wi], byte), sc[1][wi / 2]);
-                        const uint32_t a2 = mul2(code_pair(w[0][wi], byte + 1), sc[0][wi / 2]);
-                        const uint32_t a3 = mul2(code_pair(w[1][wi], byte + 1), sc[1][wi / 2]);
+                        auto scaled = [&](int row, int at) {  // words 2, 3 are of the second scale block
+                            return wi < 2 ? mul2_by<false>(code_pair(w[row][wi], at), sc[row])
+                                          : mul2_by<true>(code_pair(w[row][wi], at), sc[row]);
+                        };
+                        const uint32_t a0 = scaled(0, byte), a1 = scaled(1, byte);
+                        const uint32_t a2 = scaled(0, byte + 1), a3 = scaled(1, byte + 1);
 #pragma unroll
                         for (int n = 0; n < NQ; ++n) {
                             if (kk == 0) mma16816_first(c[n][blk], a0, a1, a2, a3, q[n][0], q[n][1]);
@@ -466,13 +482,14 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                             const uint32_t y = transpose8x8(pack_half2(x[0][k], x[0][k]));
                             const uint32_t p0 = __byte_perm(y, 0, sel0), p1 = __byte_perm(y, 0, sel1);
                             const uint32_t sh = hf ? s23 : s01;
-                            const uint32_t sa = __byte_perm(sh, 0, 0x1010), sb = __byte_perm(sh, 0, 0x3232);
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) {
                                 const uint32_t wa = w[2 * hf][mt / 2], wb = w[2 * hf + 1][mt / 2];
                                 const int byte = (mt & 1) * 2;
-                                const uint32_t a0 = mul2(code_pair(wa, byte), sa), a1 = mul2(code_pair(wa, byte + 1), sa);
-                                const uint32_t a2 = mul2(code_pair(wb, byte), sb), a3 = mul2(code_pair(wb, byte + 1), sb);
+                                const uint32_t a0 = mul2_by<false>(code_pair(wa, byte), sh);
+                                const uint32_t a1 = mul2_by<false>(code_pair(wa, byte + 1), sh);
+                                const uint32_t a2 = mul2_by<true>(code_pair(wb, byte), sh);
+                                const uint32_t a3 = mul2_by<true>(code_pair(wb, byte + 1), sh);
                                 mma16816(o[0][mt], a0, a1, a2, a3, p0, p1);
                             }
                         }
@@ -617,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
 // One warp per (sequence, query head); its loads of all splits are in flight
 // together.  A kernel of its own: merged by the last CTA to finish a split
 // instead, the wait for the partials and two rounds of dependent loads fell
-// into that CTA's stream of pages (64 sequences of up to 4096 keys: 70 us a
-// call, XX this way).
+// into that CTA's stream of pages (64 sequences of up to 4096 keys: 70.7 us a
+// call, 51.1 with the merge moved here).
 template <int D>
 __global__ void __launch_bounds__(128) combine_fp4_kernel(const __grid_constant__ DecodeArgs a) {
     const int w = (int)(blockIdx.x * 4 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;

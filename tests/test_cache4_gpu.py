@@ -430,6 +430,35 @@ def test_captured_step_follows_new_lengths():
     assert B.pa_check_status(ws) == B.PA_OK and B.pa_check_status(aws) == B.PA_OK
 
 
+def test_decode_without_lse_and_with_stale_workspace_contents():
+    c = Cache([900, 10, 0], 2, 128, seed=101)
+    q, scale, out, lse, p = decode(c, 8)
+    k, v, ks, vs, table, lens = c.up()
+    p.workspace[B.PA_STATUS_BYTES:].fill_(0xFF)  # partials are written before they are read
+    o2 = torch.full_like(out, 7.0)
+    B.pa_decode(p.shapes, p.plan, ops.as_bf16(q, DEV), k, v, ks, vs, table, lens, p.meta_dev, scale, o2, None, p.workspace)
+    assert B.pa_check_status(p.workspace) == B.PA_OK
+    assert torch.equal(o2, out)
+
+
+def test_decode_of_a_grid_wider_than_its_items():
+    """A capacity plan's launch: most CTAs have nothing to do, none of the sequences is split."""
+    c = Cache([3, 200], 1, 64, seed=102)
+    sh = B.pa_decode_shapes(batch=2, num_q_heads=3, num_kv_heads=1, head_dim=64, page_size=64,
+                            max_pages_per_seq=c.table.shape[1], num_pool_pages=c.pages, kv_dtype=B.PA_KV_FP4_E2M1,
+                            num_sms=ops.num_sms(), ctas_per_sm=0, forced_splits=0)
+    plan = B.pa_get_static_plan(sh)
+    meta = torch.zeros(plan.meta_ints, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device=DEV)
+    k, v, ks, vs, table, lens = c.up()
+    q = W.bf16_normal(102, 1, (2, 3, 64))
+    out, lse = torch.empty((2, 3, 64), dtype=torch.bfloat16, device=DEV), torch.empty((2, 3), device=DEV)
+    B.pa_get_metadata_device(sh, plan, lens, meta)
+    B.pa_decode(sh, plan, ops.as_bf16(q, DEV), k, v, ks, vs, table, lens, meta, 0.125, out, lse, ws)
+    assert B.pa_check_status(ws) == B.PA_OK
+    check(c, q, 0.125, out, lse)
+
+
 def test_two_streams_with_their_own_workspaces():
     c = Cache([2000, 500], 2, 128, seed=99)
     k, v, ks, vs, table, lens = c.up()

@@ -128,6 +128,32 @@ def test_padding_tokens_and_bad_positions():
     assert (qo[2] == 7).all()
 
 
+@pytest.mark.parametrize("inter,axes,dtype", [(False, 1, "bf16"), (True, 3, "f16")])
+def test_more_tokens_than_warps(inter, axes, dtype):
+    """Every warp walks over several tokens, padding and bad positions among them."""
+    q, k, _, w, pos, sections, table = make(7001, 6, 3, 64, dtype, axes=axes, rot=48, seed=11)
+    pos[0, 5::97] = -1
+    pos[-1, 11::301] = 4096
+    sh = ops.rope_shapes(q, k, rope_dim=48, max_position=4096, interleaved=inter, sections=sections)
+    qo, ko = (torch.full(x.shape, 7.0, dtype=x.dtype, device=DEV) for x in (q, k))
+    ws = ops.qk_norm_rope(sh, q, k, w[0], w[1], pos, table, qo, ko)[2]
+    assert B.pa_check_status(ws) == B.PA_ERR_DEVICE_BOUNDS
+    skipped = ((pos < 0) | (pos >= 4096)).any(0)
+    assert (qo[skipped] == 7).all() and (ko[skipped] == 7).all()
+    keep = ~skipped
+    compare(qo[keep], q[keep], w[0], pos[:, keep], table, 48, inter, sections, 1e-6, True, dtype)
+    compare(ko[keep], k[keep], w[1], pos[:, keep], table, 48, inter, sections, 1e-6, True, dtype)
+
+
+def test_keys_alone_and_no_rotation():
+    q, k, _, w, _, _, _ = make(50, 4, 3, 128, "bf16", rot=0, seed=12)
+    none = k[:, :0]
+    sh = ops.rope_shapes(none, k, eps=1e-6)
+    _, ko, ws = ops.qk_norm_rope(sh, none, k, None, w[1])
+    assert B.pa_check_status(ws) == B.PA_OK
+    compare(ko, k, w[1], torch.zeros((1, 50)), None, 0, False, [0], 1e-6, True, "bf16")
+
+
 # ----------------------------------------------------------------- straight into the pages
 
 @pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3", "fp4"])
@@ -153,6 +179,49 @@ def test_append_is_the_two_calls(kv, d, hq, hk, inter, rot, axes):
     assert torch.equal(q1, qo)
     for a, b in zip(one, two):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and a.view(torch.uint8).any()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp4"])
+@pytest.mark.parametrize("batch,longest", [(3, 3000), (126, 90), (127, 90), (128, 90), (300, 40), (2000, 4)])
+def test_append_of_long_and_of_many_sequences(kv, batch, longest):
+    """Warps that walk from sequence to sequence and from page to page, empty
+    sequences among them, and batches past what one round of the search holds."""
+    rng = np.random.default_rng(batch)
+    new = rng.integers(0, longest + 1, size=batch).astype(np.int32)
+    new[rng.integers(0, batch, size=1 + batch // 5)] = 0
+    prior = rng.integers(0, 150, size=batch).astype(np.int32)
+    d, hq, hk = 64, 6, 2
+    t, pad = int(new.sum()), 5
+    q, k, v, w, _, _, table = make(t + pad, hq, hk, d, "bf16", seed=batch)
+    bt, pages = W.assign_pages(prior + new, batch, 2)
+    scales = [None, None] if kv == "bf16" else [torch.full((hk,), s, device=DEV) for s in (0.011, 0.017)]
+    one, two = ([ops.kv_pool(pages, hk, d, kv, DEV) for _ in range(2)] for _ in range(2))
+    cu, start, btd = dev(W.cu_seqlens(new)), dev(prior), dev(bt)
+    place = np.concatenate([prior[b] + np.arange(new[b]) for b in range(batch)] + [np.zeros(pad, int)]).astype(np.int32)
+    ash = ops.append_shapes(batch, hk, d, bt.shape[1], pages, t + pad, kv)
+    sh = ops.rope_shapes(q, k, v, rope_dim=d, max_position=4096)
+    qo, ko, ws = ops.qk_norm_rope(sh, q, k, w[0], w[1], dev(place[None]), table)
+    exact = ops.append_shapes(batch, hk, d, bt.shape[1], pages, t, kv)
+    ops.append_kv(exact, ko[:t].contiguous(), v[:t].contiguous(), cu, start, btd, *one, *scales, workspace=ws)
+    q1 = torch.full_like(qo, 7.0)
+    ops.norm_rope_append_kv(sh, ash, q, k, v, cu, start, btd, *two, w[0], w[1], None, table, *scales, q_out=q1, workspace=ws)
+    assert B.pa_check_status(ws) == B.PA_OK
+    assert torch.equal(q1[:t], qo[:t]) and (q1[t:] == 7).all()
+    for a, b in zip(one, two):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    # and back
+    ko2, vo2, _ = ops.gather_kv(exact, *two, cu, start, btd, *scales, workspace=ws)
+    if kv == "bf16":
+        assert torch.equal(ko2, ko[:t]) and torch.equal(vo2, v[:t].contiguous())
+    else:
+        host = [x.cpu().numpy() for x in two]
+        for got, pool, sc in zip((ko2, vo2), host, scales):
+            val = F.decode_pool(pool, sc.cpu().numpy(), d)
+            rows = np.concatenate([val[bt[b, p // 64], :, p % 64][None] for b in range(batch)
+                                   for p in range(prior[b], prior[b] + new[b])])
+            err = np.abs(got.double().cpu().numpy() - rows)
+            assert (err <= 2.0 ** -8 * np.abs(rows)).all()  # one bf16 rounding
+    assert B.pa_check_status(ws) == B.PA_OK
 
 
 def test_append_positions_default_to_the_cache_and_padding_is_skipped():
