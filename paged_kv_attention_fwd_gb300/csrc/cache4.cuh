@@ -2,7 +2,7 @@
 #pragma once
 
 #include "fp4.cuh"
-#include "pa_internal.h"
+#include "pa_step.h"
 
 namespace pa {
 

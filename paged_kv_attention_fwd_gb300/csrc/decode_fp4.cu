@@ -50,7 +50,7 @@
 #include <cstdint>
 
 #include "fp4.cuh"
-#include "pa_internal.h"
+#include "pa_step.h"
 #include "pa_launch.h"
 #include "pa_ptx.cuh"
 
