@@ -221,11 +221,21 @@ def rope_shapes(q, k, v=None, rope_dim: int = 0, max_position: int = 0, interlea
     return sh
 
 
+def _check_steps(sh: B.pa_rope_shapes, **tensors):
+    """Tensors as the shapes describe them: a step other than theirs would reach past an output."""
+    for name, x in tensors.items():
+        step = getattr(sh, name + "_stride")
+        if x.shape[0] != sh.total_tokens or (sh.total_tokens > 1 and x.shape[1] > 0 and x.stride(0) != step):
+            raise ValueError(f"{name}: {x.shape[0]} tokens of stride {x.stride(0)}, the shapes are for "
+                             f"{sh.total_tokens} of {step}")
+
+
 def qk_norm_rope(sh: B.pa_rope_shapes, q, k, q_weight=None, k_weight=None, positions=None, cos_sin=None, q_out=None,
                  k_out=None, workspace=None, stream=None):
     """RMS norm of every head, then the rotation.  Returns (q_out, k_out, workspace)."""
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
     k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    _check_steps(sh, q=q, k=k, q_out=q_out, k_out=k_out)
     workspace = _status(workspace, q.device)
     B.pa_qk_norm_rope(sh, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, workspace, stream=stream)
     return q_out, k_out, workspace
@@ -237,6 +247,7 @@ def norm_rope_append_kv(sh: B.pa_rope_shapes, append: B.pa_append_shapes, q, k, 
     """qk_norm_rope with the keys and values going straight into their pages.
     Returns (q_out, workspace)."""
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    _check_steps(sh, q=q, k=k, v=v, q_out=q_out)
     workspace = _status(workspace, q.device)
     B.pa_norm_rope_append_kv(sh, append, q, k, v, q_weight, k_weight, positions, cos_sin, cu_seqlens_new, start_pos,
                              block_table, q_out, k_pool, v_pool, k_scale, v_scale, workspace, stream=stream)

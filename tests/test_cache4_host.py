@@ -225,5 +225,12 @@ def test_python_shapes():
         ops.rope_shapes(q, k.transpose(1, 2).contiguous().transpose(1, 2), rope_dim=0)
     with pytest.raises(ValueError, match="v"):
         ops.rope_shapes(q, k, v.float(), rope_dim=0)
+    with pytest.raises(ValueError, match="q_out: 5 tokens of stride 512, the shapes are for 5 of 768"):
+        ops.qk_norm_rope(ops.rope_shapes(q, k, q_out=q, k_out=k), q, k)
+    with pytest.raises(ValueError, match="q_out: 5 tokens of stride 768, the shapes are for 5 of 512"):
+        ops.norm_rope_append_kv(ops.rope_shapes(q, k, v), ops.append_shapes(1, 2, 64, 1, 1, 5), q, k, v, *[None] * 5,
+                                q_out=q)
+    with pytest.raises(ValueError, match="k: 4 tokens"):
+        ops.qk_norm_rope(ops.rope_shapes(q, k), q, k[:4])
     t = ops.rope_table(10, 8, theta=100.0, device="cpu")
     assert t.shape == (10, 8) and torch.allclose(t[3, 1], torch.tensor(3 * 100 ** -0.25).cos())
