@@ -486,7 +486,7 @@ typedef struct {
  *                   an infinity saturates.
  *   workspace       >= PA_STATUS_BYTES (status word)
  * With 4-bit pools total_new may exceed cu_seqlens_new[B]: the tokens past it
- * are padding, and are not read.
+ * are padding; nothing of them is written, whatever they hold.
  * A position outside the block table or a page id outside the pool is skipped
  * and recorded as PA_ERR_DEVICE_BOUNDS.  Rows of different calls or tokens
  * must not collide (two writers to one row race).
@@ -564,7 +564,8 @@ typedef struct {
  *   q_out, k_out     [T, Hq, D], [T, Hk, D]; may be q and k themselves (same strides),
  *                    otherwise must not overlap them
  *   workspace        >= PA_STATUS_BYTES (status word)
- * positions and cos_sin may be NULL when rope_dim is 0.  A position at or past
+ * With rope_dim 0 neither positions (so no token is padding) nor cos_sin is
+ * read, and both may be NULL.  A position at or past
  * max_position (or a negative one of axis 1 or 2) is recorded as
  * PA_ERR_DEVICE_BOUNDS and its token left as it was.
  */
@@ -585,8 +586,10 @@ pa_status pa_qk_norm_rope(const pa_rope_shapes* shapes, const void* q, const voi
  *                    agree; fp16 tokens go to fp16 pools, bf16 tokens to the others
  *   v                [T, Hk, D], token stride v_stride
  *   positions        as above, or NULL: every axis at the token's cache position
- * T may exceed cu_seqlens_new[B]: the tokens past it are padding, and nothing
- * of them is read or written.  A token whose position, page or page id is out
+ *                    (with rope_dim 0 not read: padding is then what lies past
+ *                    cu_seqlens_new[B] only)
+ * T may exceed cu_seqlens_new[B]: the tokens past it are padding; nothing of
+ * them is written, whatever they hold.  A token whose position, page or page id is out
  * of range is skipped (queries too) and recorded as PA_ERR_DEVICE_BOUNDS.
  */
 pa_status pa_norm_rope_append_kv(const pa_rope_shapes* rope_shapes, const pa_append_shapes* append_shapes,

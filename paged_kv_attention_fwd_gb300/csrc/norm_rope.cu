@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     const long long id = (long long)blockIdx.x * kWarps + warp;
     int chunk = (int)(id % chunks);
     const int tok0 = (int)min(id / chunks * a.tokens_per_warp, (long long)a.total_tokens);
-    const int tok_end = min(a.total_tokens, tok0 + a.tokens_per_warp);
+    const int tok_end = (int)min((long long)a.total_tokens, (long long)tok0 + a.tokens_per_warp);
     if (tok0 >= tok_end) return;
     const int kind = chunk < qchunks ? 0 : chunk < qchunks + kchunks ? 1 : 2;  // queries, keys, values
     chunk -= kind == 0 ? 0 : kind == 1 ? qchunks : qchunks + kchunks;
@@ -362,8 +362,8 @@ cudaError_t launch(NormRopeArgs a, cudaStream_t stream) {
     const long long chunks = (a.num_q_heads + kPer - 1) / kPer + (kCache >= 0 ? 2 : 1) * ((a.num_kv_heads + kPer - 1) / kPer);
     // As many warps as stay on the SMs; each walks over its share of the tokens.
     const long long resident = (long long)sms * kCtas * kWarps;
-    a.tokens_per_warp = (int)((a.total_tokens * chunks + resident - 1) / resident);
-    const long long warps = (a.total_tokens + a.tokens_per_warp - 1) / a.tokens_per_warp * chunks;
+    a.tokens_per_warp = (int)min((a.total_tokens * chunks + resident - 1) / resident, (long long)a.total_tokens);
+    const long long warps = ((long long)a.total_tokens + a.tokens_per_warp - 1) / a.tokens_per_warp * chunks;
     return launch_overlapped(norm_rope_kernel<D, kInterleaved, kCache, kF16>, dim3((unsigned)((warps + kWarps - 1) / kWarps)),
                              dim3(kWarps * 32), 0, stream, a);
 }

@@ -823,9 +823,6 @@ pa_status fill_rope_args(const pa_rope_shapes* sh, const void* q, const void* k,
         return fail(PA_ERR_INVALID_ARG, "q, k, the weights, cos_sin and the outputs must be 16-byte aligned");
     if (workspace_bytes < PA_STATUS_BYTES)
         return fail(PA_ERR_WORKSPACE, "workspace needs %d bytes, got %zu", PA_STATUS_BYTES, workspace_bytes);
-    // one warp per 4 head rows of a token at least, 4 warps to a CTA
-    if ((int64_t)sh->total_tokens * ((Hq + 2 * (int64_t)Hk) / 4 + 1) > ((int64_t)1 << 32))
-        return fail(PA_ERR_UNSUPPORTED, "total_tokens * heads is too large for one launch");
     std::memset(a, 0, sizeof *a);
     a->q = static_cast<const uint16_t*>(q);
     a->k = static_cast<const uint16_t*>(k);

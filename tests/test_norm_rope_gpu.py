@@ -244,6 +244,33 @@ def test_append_positions_default_to_the_cache_and_padding_is_skipped():
     assert int((pools[0][1] != 0).any(-1).sum()) == 5 * 2  # five tokens' rows of two heads
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp4"])
+@pytest.mark.parametrize("rot", [0, 64])
+def test_append_in_place_and_without_rotation(kv, rot):
+    """Queries written over the packed projection they came from; without a rotation positions are not looked at."""
+    prior, new = np.array([60, 0, 7], np.int32), np.array([9, 1, 130], np.int32)
+    q, k, v, w, pos, _, table = make(140, 6, 2, 64, "bf16", rot=rot, seed=10)
+    bt, pages = W.assign_pages(prior + new, 4, 1)
+    cu, start, btd = dev(W.cu_seqlens(new)), dev(prior), dev(bt)
+    ash = ops.append_shapes(3, 2, 64, bt.shape[1], pages, 140, kv)
+    scale = torch.full((2,), 0.37, device=DEV) if kv == "fp4" else None
+    if rot == 0:
+        pos = torch.full_like(pos, -1)
+    runs = []
+    for out in (torch.empty_like(q), q):
+        kp, vp = (ops.kv_pool(pages, 2, 64, kv, DEV) for _ in range(2))
+        sh = ops.rope_shapes(q, k, v, rope_dim=rot, max_position=4096, q_out=out)
+        k0, v0 = k.clone(), v.clone()
+        _, ws = ops.norm_rope_append_kv(sh, ash, q, k, v, cu, start, btd, kp, vp, w[0], w[1], pos, table, scale, scale,
+                                        q_out=out)
+        assert B.pa_check_status(ws) == B.PA_OK
+        assert torch.equal(k, k0) and torch.equal(v, v0)
+        runs.append((out, kp, vp))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+    assert (runs[0][0] != 0).any(-1).all()
+
+
 def test_append_reports_what_is_out_of_range():
     q, k, v, w, _, _, table = make(4, 4, 2, 64, "bf16", seed=9)
     bt = np.array([[0, 5]], np.int32)  # page id 5 of a pool of 2
