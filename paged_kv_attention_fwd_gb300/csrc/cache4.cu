@@ -13,7 +13,8 @@
 //
 // Measured: 4-bit rows of 262k tokens, 8 heads of 128, read back in 238 us
 // (1.59 GB, 6.7 TB/s, the memory's copy rate); 4096 tokens written and 37k
-// read back, two launches, 40 us (215 MB); 64 written and 64 read back 7.8 us.
+// read back, two launches, 38.7 us (215 MB); 64 written and 64 read back 6.0 us.
+// Written alone, 32768 tokens of 8 heads take 32.2 us (172 MB, 5.3 TB/s).
 #include "cache4.cuh"
 #include "pa_launch.h"
 #include "token_place.cuh"
@@ -22,11 +23,14 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kHeads = 4;  // heads of a warp
+// Heads of a warp.  Writing has work to do between its loads and its stores, and wants more warps: 32768 tokens of 8
+// heads 32.3 us with 2, 37.2 with 4, 34.4 with 1; 512 tokens 3.3, 4.4, 2.9.  Reading back: 29.1 with 4, as with 2 and 1,
+// 262k rows 237.4, 238.3, 241.0.
+constexpr int kAppendHeads = 2, kGatherHeads = 4;
 
 // This thread's token and the first of its warp's heads.
 // grid: x = groups of tokens, kWarps to a CTA; y = groups of kHeads heads
-template <int D>
+template <int D, int kHeads>
 struct Share {
     static constexpr int kLanes = D / 16, kTokens = 32 / kLanes;
     int tok0, tok, piece, h0;  // tok0: the warp's first token
@@ -48,7 +52,8 @@ template <int D>
 __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_constant__ AppendArgs a) {
     grid_dependency_wait();
     allow_dependents_launch();
-    const Share<D> my;
+    constexpr int kHeads = kAppendHeads;
+    const Share<D, kHeads> my;
     if (my.tok0 >= a.total_new) return;
     const int nh = min(kHeads, a.num_kv_heads - my.h0);
     // rows first: they do not depend on the token's place
@@ -144,7 +149,8 @@ template <int D, int kType>
 __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_constant__ GatherArgs a) {
     grid_dependency_wait();
     allow_dependents_launch();
-    const Share<D> my;
+    constexpr int kHeads = kGatherHeads;
+    const Share<D, kHeads> my;
     if (my.tok0 >= a.total) return;
     const Sequence seq = my.sequence(a.cu, a.start_pos, a.batch);
     if (my.tok >= a.total) return;
@@ -179,15 +185,15 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
         }
 }
 
-template <int D>
+template <int D, int kHeads>
 dim3 token_grid(int tokens, int heads) {
-    constexpr int per_cta = kWarps * Share<D>::kTokens;
+    constexpr int per_cta = kWarps * Share<D, kHeads>::kTokens;
     return dim3((unsigned)((tokens + per_cta - 1) / per_cta), (unsigned)((heads + kHeads - 1) / kHeads));
 }
 
 template <int D>
 cudaError_t launch_gather_d(const GatherArgs& a, int kv_dtype, cudaStream_t stream) {
-    const dim3 grid = token_grid<D>(a.total, a.num_kv_heads), block(kWarps * 32);
+    const dim3 grid = token_grid<D, kGatherHeads>(a.total, a.num_kv_heads), block(kWarps * 32);
     switch (kv_dtype) {
         case PA_KV_FP4_E2M1: return launch_overlapped(gather_kernel<D, PA_KV_FP4_E2M1>, grid, block, 0, stream, a);
         case PA_KV_FP8_E4M3: return launch_overlapped(gather_kernel<D, PA_KV_FP8_E4M3>, grid, block, 0, stream, a);
@@ -200,8 +206,8 @@ cudaError_t launch_gather_d(const GatherArgs& a, int kv_dtype, cudaStream_t stre
 cudaError_t launch_append_fp4(const AppendArgs& a, cudaStream_t stream) {
     const dim3 block(kWarps * 32);
     return a.head_dim == 128
-               ? launch_overlapped(append_fp4_kernel<128>, token_grid<128>(a.total_new, a.num_kv_heads), block, 0, stream, a)
-               : launch_overlapped(append_fp4_kernel<64>, token_grid<64>(a.total_new, a.num_kv_heads), block, 0, stream, a);
+               ? launch_overlapped(append_fp4_kernel<128>, token_grid<128, kAppendHeads>(a.total_new, a.num_kv_heads), block, 0, stream, a)
+               : launch_overlapped(append_fp4_kernel<64>, token_grid<64, kAppendHeads>(a.total_new, a.num_kv_heads), block, 0, stream, a);
 }
 
 cudaError_t launch_gather(const GatherArgs& a, int head_dim, int kv_dtype, cudaStream_t stream) {

@@ -37,13 +37,10 @@ __device__ __forceinline__ void store_sector(void* p, const Sector& s, bool wide
 }
 
 // the bf16 elements of w, as floats
-__device__ __forceinline__ void bf16x8_to_float(const uint4& w, float (&x)[8]) {
+__device__ __forceinline__ void bf16x8_to_float(const uint4& w, F2 (&x)[4]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = f2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ uint32_t absmax_bf16x8(const uint4& w) {
@@ -57,8 +54,8 @@ __device__ __forceinline__ void fp4_store_block(uint8_t* slab, int row, int piec
     const uint32_t m2 = absmax_bf16x2(absmax_bf16x8(w0), absmax_bf16x8(w1));
     const uint32_t m = absmax_bf16x2(m2, m2 >> 16);
     float step;
-    const uint32_t byte = fp4_block_scale(__uint_as_float(m << 16), ks, step);
-    float x[8];
+    const uint32_t byte = fp4_block_scale(__uint_as_float((m & 0x7FFFu) << 16), ks, step);
+    F2 x[4];
     uint2 codes;
     bf16x8_to_float(w0, x);
     codes.x = fp4_codes8(x, byte, step);

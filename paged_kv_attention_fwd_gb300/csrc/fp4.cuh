@@ -24,13 +24,22 @@
 
 #include <cstdint>
 
+#include "f32x2.cuh"
+
 namespace pa {
 
 constexpr int kFp4Block = 16;
 __host__ __device__ constexpr int fp4_slab_bytes(int d) { return 64 * (d / 2 + d / kFp4Block); }
 
 // e2m1 codes of 8 elements, 4 bits each, element 0 lowest
-__device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8]) {
+__device__ __forceinline__ uint32_t e2m1x8(const F2 (&pairs)[4]) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = split(pairs[i]);
+        q[2 * i] = v.x;
+        q[2 * i + 1] = v.y;
+    }
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -70,10 +79,10 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t byte) {
     return __half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFFu)));
 }
 
-// largest magnitude of two 16-bit lanes each, NaN if any is NaN
+// largest magnitude of two 16-bit lanes each, NaN if any is NaN; the signs are anything
 __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -93,19 +102,23 @@ __device__ __forceinline__ uint32_t fp4_block_scale(float amax, float ks, float&
 // residual step, q' = q + (x - q S) r: the residual is exact, so q' is the
 // fp32 quotient wherever it lies between the smallest and the largest code
 // (smaller ones round to 0 either way).
-__device__ __forceinline__ uint32_t fp4_codes8(const float (&x)[8], uint32_t byte, float step) {
-    float q[8];
+__device__ __forceinline__ uint32_t fp4_codes8(const F2 (&x)[4], uint32_t byte, float step) {
+    F2 q[4];
     if (byte < 0x7Eu && step > 1e-30f && step < 1e30f) {
-        const float r = __frcp_rn(step);
+        const float r1 = __frcp_rn(step);
+        const F2 r = f2(r1, r1), minus_step = f2(-step, -step);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q0 = x[i] * r;
-            q[i] = fmaf(fmaf(-q0, step, x[i]), r, q0);
+        for (int i = 0; i < 4; ++i) {
+            const F2 q0 = x[i] * r;
+            q[i] = fma2(fma2(q0, minus_step, x[i]), r, q0);
         }
     } else {
         if (byte >= 0x7Fu || !(step > 0.f)) return 0;  // a zero or NaN scale
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], step);
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = split(x[i]);
+            q[i] = f2(__fdiv_rn(v.x, step), __fdiv_rn(v.y, step));
+        }
     }
     return e2m1x8(q);
 }

@@ -21,6 +21,7 @@
 // the append form, 8 x 512 tokens, 32 + 8 + 8 heads (103 MB), 21 us; one token
 // 3 us, a launch.
 #include "cache4.cuh"
+#include "f32x2.cuh"
 #include "pa_launch.h"
 #include "token_place.cuh"
 
@@ -30,34 +31,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kCtas = 4;    // CTAs of an SM
 constexpr int kPasses = 4;  // rows of a lane whose loads are in flight together
-
-struct F2 {  // two fp32 values in one 64-bit register pair
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 split(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 swapped(F2 a) {
-    const float2 s = split(a);
-    return f2(s.y, s.x);
-}
 
 __device__ __forceinline__ float2 unpack16(uint32_t w, bool f16) {
     if (f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
