@@ -101,17 +101,19 @@ __device__ __forceinline__ uint32_t fp4_block_scale(float amax, float ks, float&
 // of fp32 the quotient comes from the correctly rounded reciprocal with one
 // residual step, q' = q + (x - q S) r: the residual is exact, so q' is the
 // fp32 quotient wherever it lies between the smallest and the largest code
-// (smaller ones round to 0 either way).
+// (smaller ones round to 0 either way).  It is taken of -q, whose steps leave
+// a zero of x its sign.
 __device__ __forceinline__ uint32_t fp4_codes8(const F2 (&x)[4], uint32_t byte, float step) {
     F2 q[4];
     if (byte < 0x7Eu && step > 1e-30f && step < 1e30f) {
         const float r1 = __frcp_rn(step);
-        const F2 r = f2(r1, r1), minus_step = f2(-step, -step);
+        const F2 minus_r = f2(-r1, -r1), s = f2(step, step);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const F2 q0 = x[i] * r;
-            q[i] = fma2(fma2(q0, minus_step, x[i]), r, q0);
+            const F2 q0 = x[i] * minus_r;
+            q[i] = fma2(fma2(q0, s, x[i]), minus_r, q0);
         }
+        return e2m1x8(q) ^ 0x88888888u;
     } else {
         if (byte >= 0x7Fu || !(step > 0.f)) return 0;  // a zero or NaN scale
 #pragma unroll

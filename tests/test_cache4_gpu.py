@@ -139,6 +139,22 @@ def test_codes_of_every_bf16_magnitude():
     assert np.array_equal(k.cpu().numpy(), want) and np.array_equal(v.cpu().numpy(), want)
 
 
+def test_zeros_keep_their_signs():
+    d, hk = 64, 2
+    x = W.bf16_normal(9, 0, (40, hk, d))
+    x[:, :, 3::5] = 0x8000
+    x[:, :, 1::7] = 0
+    x[5:9, :, 2] = 0x8001  # rounds to -0
+    x[9, 0, :16] = 0x8000  # nothing but zeros: codes 0
+    head = np.array([0.37, 21.0], np.float32)
+    table, pool = np.zeros((1, 1), np.int32), np.zeros((1, hk, 64 * (d // 2 + d // 16)), np.uint8)
+    k, v, xb, h = dev(pool), dev(pool), ops.as_bf16(x, DEV), dev(head)
+    ops.append_kv(ops.append_shapes(1, hk, d, 1, 1, 40, "fp4"), xb, xb, dev(np.array([0, 40], np.int32)),
+                  dev(np.zeros(1, np.int32)), dev(table), k, v, h, h)
+    want = F.append(x, [0, 40], [0], table, pool, head, d)
+    assert np.array_equal(k.cpu().numpy(), want) and np.array_equal(v.cpu().numpy(), want)
+
+
 def gather_case(kv, d, hk, lens, start, seed=71):
     base = W.make_decode(len(lens), hk, hk, d, np.asarray(lens) + start, seed=seed, kv_dtype=kv, extra_pages=2)
     conv = {"bf16": ops.as_bf16, "f16": ops.as_f16, "e4m3": ops.as_e4m3}[kv]
