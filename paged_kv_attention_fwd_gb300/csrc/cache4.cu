@@ -46,8 +46,6 @@ struct Share {
     }
 };
 
-__device__ __forceinline__ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
-
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_constant__ AppendArgs a) {
     grid_dependency_wait();

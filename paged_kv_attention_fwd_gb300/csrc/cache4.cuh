@@ -6,6 +6,8 @@
 
 namespace pa {
 
+__device__ __forceinline__ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 // 32 bytes of global memory: one access -- a whole sector per thread, where
 // two of 16 bytes touch every sector of a warp's span twice (read-back of
 // 262k rows: 238 us against 301) -- when every address is 32-byte aligned.

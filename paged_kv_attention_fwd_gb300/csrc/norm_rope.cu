@@ -47,15 +47,33 @@ __device__ __forceinline__ uint32_t pack16(F2 a, bool f16) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// four e4m3 codes of x / scale, as pa_append_kv stores them
-__device__ __forceinline__ uint32_t e4m3x4(uint2 w, float scale) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fdiv_rn(__uint_as_float(w.x << 16), scale), __fdiv_rn(__uint_as_float(w.x & 0xFFFF0000u), scale)),
-        __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fdiv_rn(__uint_as_float(w.y << 16), scale), __fdiv_rn(__uint_as_float(w.y & 0xFFFF0000u), scale)),
-        __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+// Eight e4m3 codes of x / scale, the bits that pa_append_kv stores: fp32
+// quotients (nearest even), then nearest even, saturating.  Away from the ends
+// of fp32 the quotient is the correctly rounded reciprocal's with one residual
+// step, q' = q + (x - q scale) r: the residual is exact for every quotient that
+// does not round to code 0 either way.  It is taken of -q, whose steps leave a
+// zero of x its sign.
+__device__ __forceinline__ uint2 e4m3x8(uint2 w0, uint2 w1, float scale) {
+    const uint32_t u[4] = {w0.x, w0.y, w1.x, w1.y};
+    const uint32_t m2 = absmax_bf16x2(absmax_bf16x2(u[0], u[1]), absmax_bf16x2(u[2], u[3]));
+    const float largest = __uint_as_float((absmax_bf16x2(m2, m2 >> 16) & 0x7FFFu) << 16);
+    uint32_t c[4];
+    if (largest < 1e15f && fabsf(scale) > 1e-15f && fabsf(scale) < 1e15f) {
+        const float r1 = __frcp_rn(scale);
+        const F2 minus_r = f2(-r1, -r1), s = f2(scale, scale);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F2 x = f2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)), q = x * minus_r;
+            c[i] = __nv_cvt_float2_to_fp8x2(split(fma2(fma2(q, s, x), minus_r, q)), __NV_SATFINITE, __NV_E4M3) ^ 0x8080u;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(__uint_as_float(u[i] << 16), scale),
+                                                        __fdiv_rn(__uint_as_float(u[i] & 0xFFFF0000u), scale)),
+                                            __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 // The four cos and sin a lane needs: pairs pair0 .. pair0 + 3, whose positions
@@ -115,7 +133,28 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     struct Rows {
         uint2 x[kPasses][2];
     };
+    // 4-bit pages: kBlocks blocks of 16 elements to a row, every 32nd of the warp's a lane's.  Values are loaded that way,
+    // keys get there through shared memory.
+    constexpr bool kFp4 = kCache == PA_KV_FP4_E2M1;
+    constexpr int kBlocks = D / 16;
+    static_assert(kPasses % 2 == 0, "a lane holds kPasses / 2 blocks");
+    __shared__ __align__(16) uint16_t stage[kFp4 ? kWarps : 1][kFp4 ? kPer * D : 8];
+    const bool wide_v = kFp4 && aligned32(a.v) && a.v_stride % 16 == 0;
     auto load_rows = [&](Rows& to, int tok) {
+        if constexpr (kFp4) {
+            if (kind == 2) {
+#pragma unroll
+                for (int p = 0; p < kPasses; p += 2) {
+                    const int at = 16 * p + lane, r = min(first_row + at / kBlocks, row_end - 1);
+                    const Sector s = load_sector(src + tok * src_stride + r * D + at % kBlocks * 16, wide_v);
+                    to.x[p][0] = make_uint2(s.lo.x, s.lo.y);
+                    to.x[p][1] = make_uint2(s.lo.z, s.lo.w);
+                    to.x[p + 1][0] = make_uint2(s.hi.x, s.hi.y);
+                    to.x[p + 1][1] = make_uint2(s.hi.z, s.hi.w);
+                }
+                return;
+            }
+        }
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
             const int r = min(first_row + p * kRows + lane / kLanes, row_end - 1);  // past the last row: that row again
@@ -199,8 +238,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
         if (!by_place) find_place(where, pos, tok0);
     }
 
-    __shared__ __align__(16) uint16_t stage[kCache == PA_KV_FP4_E2M1 ? kWarps : 1][kCache == PA_KV_FP4_E2M1 ? kRows * D : 8];
-
 #pragma unroll 1
     for (int tok = tok0; tok < tok_end; ++tok) {
         // y = inv (x c1 + partner c2): elements 01, 23, 45, 67 of the lane
@@ -274,42 +311,56 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
                 out.x[p][1] = make_uint2(pack16(y[p][2], kF16), pack16(y[p][3], kF16));
             }
         }
+        if constexpr (kFp4) {
+            if (kind != 0) {
+                uint16_t* st = stage[warp];
+                if (kind == 1) {
+#pragma unroll
+                    for (int p = 0; p < kPasses; ++p) {
+                        uint16_t* row = st + (p * kRows + lane / kLanes) * D;
+                        *reinterpret_cast<uint2*>(row + off0) = out.x[p][0];
+                        *reinterpret_cast<uint2*>(row + off1) = out.x[p][1];
+                    }
+                    __syncwarp();
+                }
+                uint8_t* pool = static_cast<uint8_t*>(kind == 2 ? a.v_pool : a.k_pool);
+                const float* scales = kind == 2 ? a.v_scale : a.k_scale;
+#pragma unroll
+                for (int p = 0; p < kPasses; p += 2) {
+                    const int at = 16 * p + lane, r = first_row + at / kBlocks;
+                    uint4 lo = make_uint4(out.x[p][0].x, out.x[p][0].y, out.x[p][1].x, out.x[p][1].y);
+                    uint4 hi = make_uint4(out.x[p + 1][0].x, out.x[p + 1][0].y, out.x[p + 1][1].x, out.x[p + 1][1].y);
+                    if (kind == 1) {
+                        lo = *reinterpret_cast<const uint4*>(st + at * 16);
+                        hi = *reinterpret_cast<const uint4*>(st + at * 16 + 8);
+                    }
+                    if (r < row_end)
+                        fp4_store_block<D>(pool + ((long long)page * a.num_kv_heads + r) * fp4_slab_bytes(D), prow,
+                                           at % kBlocks, lo, hi, __ldg(&scales[r]));
+                }
+                __syncwarp();  // the stage is free again
+                continue;
+            }
+        }
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-            const int r0 = first_row + p * kRows;  // first row of the pass (warp-uniform)
-            const int r = r0 + lane / kLanes;
+            const int r = first_row + p * kRows + lane / kLanes;
             const bool mine = r < row_end;
             const uint2 y0 = out.x[p][0], y1 = out.x[p][1];
             uint16_t* dst = nullptr;  // a 16-bit destination row
             if (kind == 0) dst = a.q_out + tok * a.q_out_stride + (long long)r * D;
             else if constexpr (!kAppend) dst = a.k_out + tok * a.k_out_stride + (long long)r * D;
-            if constexpr (kAppend) {
+            if constexpr (kAppend && !kFp4) {
                 if (kind != 0) {
                     const long long slab = (long long)page * a.num_kv_heads + r;
                     uint8_t* pool = static_cast<uint8_t*>(kind == 2 ? a.v_pool : a.k_pool);
-                    const float* scales = kind == 2 ? a.v_scale : a.k_scale;
                     if constexpr (kCache == PA_KV_BF16) {  // either 16-bit type
                         dst = reinterpret_cast<uint16_t*>(pool) + (slab * kPage + prow) * D;
-                    } else if constexpr (kCache == PA_KV_FP8_E4M3) {
-                        if (mine) {
-                            uint8_t* out = pool + (slab * kPage + prow) * D;
-                            const float scale = __ldg(&scales[r]);
-                            *reinterpret_cast<uint32_t*>(out + off0) = e4m3x4(y0, scale);
-                            *reinterpret_cast<uint32_t*>(out + off1) = e4m3x4(y1, scale);
-                        }
-                    } else if (r0 < row_end) {  // through shared memory, so that one lane sees the 16 elements of a block
-                        uint16_t* st = stage[warp];
-                        *reinterpret_cast<uint2*>(st + (lane / kLanes) * D + off0) = y0;
-                        *reinterpret_cast<uint2*>(st + (lane / kLanes) * D + off1) = y1;
-                        __syncwarp();
-                        constexpr int kBlocks = D / 16;
-                        const int br = r0 + lane / kBlocks, piece = lane % kBlocks;
-                        if (lane < kRows * kBlocks && br < row_end) {
-                            const uint4* w = reinterpret_cast<const uint4*>(st + (lane / kBlocks) * D + piece * 16);
-                            fp4_store_block<D>(pool + ((long long)page * a.num_kv_heads + br) * fp4_slab_bytes(D), prow,
-                                               piece, w[0], w[1], __ldg(&scales[br]));
-                        }
-                        __syncwarp();
+                    } else if (mine) {
+                        uint8_t* to = pool + (slab * kPage + prow) * D;
+                        const uint2 codes = e4m3x8(y0, y1, __ldg(&(kind == 2 ? a.v_scale : a.k_scale)[r]));
+                        *reinterpret_cast<uint32_t*>(to + off0) = codes.x;
+                        *reinterpret_cast<uint32_t*>(to + off1) = codes.y;
                     }
                 }
             }

@@ -244,6 +244,27 @@ def test_append_positions_default_to_the_cache_and_padding_is_skipped():
     assert int((pools[0][1] != 0).any(-1).sum()) == 5 * 2  # five tokens' rows of two heads
 
 
+@pytest.mark.parametrize("kv", ["e4m3", "fp4"])
+@pytest.mark.parametrize("shuffled", [False, True])
+def test_append_of_every_value_bit_for_bit(kv, shuffled):
+    """Every bf16 bit pattern of a head, among neighbours of its size or of any, against scales of every size."""
+    scales = torch.tensor([1.0, 0.37, 3.1e-3, 448.0, 7e-16, 2e15, 3e-30, 5e30], device=DEV)
+    every = torch.arange(65536, dtype=torch.int32)
+    if shuffled:
+        every = every[torch.randperm(65536, generator=torch.Generator().manual_seed(3))]
+    v = every.to(torch.int16).view(torch.bfloat16).view(512, 1, 128).expand(512, 8, 128).contiguous().to(DEV)
+    bt = np.random.default_rng(4).permutation(9)[None].astype(np.int32)
+    cu, start, btd = dev(np.array([0, 512], np.int32)), dev(np.array([33], np.int32)), dev(bt)
+    ash = ops.append_shapes(1, 8, 128, 9, 9, 512, kv)
+    pools = [ops.kv_pool(9, 8, 128, kv, DEV) for _ in range(4)]
+    ops.append_kv(ash, v, v, cu, start, btd, pools[0], pools[1], scales, scales)
+    sh = ops.rope_shapes(v, v, v, norm=False)  # a key that neither turns nor is normed passes through but for NaN's bits
+    ops.norm_rope_append_kv(sh, ash, torch.zeros_like(v), v, v, cu, start, btd, pools[2], pools[3], k_scale=scales,
+                            v_scale=scales)
+    as_bytes = [p.view(torch.uint8) for p in pools]
+    assert torch.equal(as_bytes[1], as_bytes[3]) and torch.equal(as_bytes[0], as_bytes[2])
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp4"])
 @pytest.mark.parametrize("rot", [0, 64])
 def test_append_in_place_and_without_rotation(kv, rot):
