@@ -11,15 +11,17 @@
 // a head row is held by D / 8 lanes, 8 elements each, in two groups of 4 that
 // pair up with one another (the rotation needs no shuffle in either pairing);
 // a warp takes up to kPasses rows per lane of one kind (queries, keys or
-// values), with the weights multiplied into the cosines and sines,
+// values) at a time, with the weights multiplied into the cosines and sines,
 //   a' = inv (a (w_a cos) - b (w_b sin)),  b' = inv (b (w_b cos) + a (w_a sin)),
-// the arithmetic runs on pairs of fp32 (f32x2), and a warp goes on to the same
-// rows of the next tokens with their elements and angles already on the way.
+// the arithmetic runs on pairs of fp32 (f32x2), and a warp goes on to the next
+// such chunk with its elements and angles already on the way.
 //
-// Measured: 16384 tokens, 64 + 8 heads of 128 (613 MB), 100 us a call, 6.1
-// TB/s (103 us with 3 CTAs an SM, 116 with 5, 106 with 2 passes and 6 CTAs);
-// the append form, 8 x 512 tokens, 32 + 8 + 8 heads (103 MB), 21 us; one token
-// 3 us, a launch.
+// Measured: 16384 tokens, 64 + 8 heads of 128 (613 MB), 96.5 us a call, 6.4
+// TB/s; the append form, 8 x 512 tokens, 32 + 8 + 8 heads, 21 us with 16-bit
+// pages (103 MB); one token 3 us, a launch.  3 CTAs an SM 109 and 23.2 us, 5
+// 101 and 24.0, 2 passes and 6 CTAs 111 and 25.2.  Rows through a ring of bulk
+// copies in shared memory, 3 or 4 deep, were no faster (100 and 23): the loads
+// in flight are not what bounds it.
 #include "cache4.cuh"
 #include "f32x2.cuh"
 #include "pa_launch.h"
@@ -30,7 +32,15 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kCtas = 4;    // CTAs of an SM
-constexpr int kPasses = 4;  // rows of a lane whose loads are in flight together
+constexpr int kPasses = 4;  // rows of a lane in a chunk, whose loads are in flight together
+
+// Whether a warp goes from one chunk of a token to the next (else from one
+// token to the next with the same chunk).  With a cache the kinds differ in
+// work, keys and values that are quantised taking longest, and each warp needs
+// its share of all: 8 x 512 tokens, 32 + 8 + 8 heads, 21.0 us against 22.7 with
+// 16-bit pages, 23.6 against 26.9 with e4m3 ones, 22.0 against 26.1 with 4-bit
+// ones.  Without, one chunk keeps its weights: 16384 tokens 96.5 us against 99.2.
+constexpr bool walks_chunks(int cache) { return cache >= 0; }
 
 __device__ __forceinline__ float2 unpack16(uint32_t w, bool f16) {
     if (f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -109,24 +119,23 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     constexpr bool kAppend = kCache >= 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kLanes;
-    // this warp's kind of rows, its rows of a token, and its tokens
+    // A token's rows come in chunks of one kind: queries, keys, values
     constexpr int kPer = kPasses * kRows;
     const int qchunks = (a.num_q_heads + kPer - 1) / kPer, kchunks = (a.num_kv_heads + kPer - 1) / kPer;
     const int chunks = qchunks + (kAppend ? 2 : 1) * kchunks;
-    const long long id = (long long)blockIdx.x * kWarps + warp;
-    int chunk = (int)(id % chunks);
-    const int tok0 = (int)min(id / chunks * a.tokens_per_warp, (long long)a.total_tokens);
-    const int tok_end = (int)min((long long)a.total_tokens, (long long)tok0 + a.tokens_per_warp);
-    if (tok0 >= tok_end) return;
-    const int kind = chunk < qchunks ? 0 : chunk < qchunks + kchunks ? 1 : 2;  // queries, keys, values
-    chunk -= kind == 0 ? 0 : kind == 1 ? qchunks : qchunks + kchunks;
-    const int first_row = chunk * kPer, row_end = min(kind == 0 ? a.num_q_heads : a.num_kv_heads, first_row + kPer);
-    const uint16_t* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    const long long src_stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+    const int id = (int)blockIdx.x * kWarps + warp;
+    const long long from = walks_chunks(kCache) ? (long long)id * a.chunks_per_warp : id;
+    const int nth = from <= 0x7FFFFFFF ? (int)from / chunks : (int)min(from / chunks, (long long)a.total_tokens);
+    const long long first = walks_chunks(kCache) ? nth : (long long)nth * a.chunks_per_warp;
+    if (first >= a.total_tokens) return;
+    const int tok0 = (int)first;
+    auto kind_of = [&](int c) { return c < qchunks ? 0 : c < qchunks + kchunks ? 1 : 2; };
+    auto first_row_of = [&](int c) { return (c < qchunks ? c : c < qchunks + kchunks ? c - qchunks : c - qchunks - kchunks) * kPer; };
+    auto rows_of = [&](int c) { return c < qchunks ? a.num_q_heads : a.num_kv_heads; };
 
     // where this lane's two groups of 4 elements lie in a row, and whether they turn
     const int half = a.rope_dim / 2;
-    const bool turns = kind != 2 && (kInterleaved ? 8 * l < a.rope_dim : 4 * l < half);
+    const bool turns = kInterleaved ? 8 * l < a.rope_dim : 4 * l < half;
     const int off0 = kInterleaved ? 8 * l : 4 * l < half ? 4 * l : a.rope_dim + 8 * (l - half / 4);
     const int off1 = kInterleaved || 4 * l >= half ? off0 + 4 : half + 4 * l;
 
@@ -140,13 +149,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     static_assert(kPasses % 2 == 0, "a lane holds kPasses / 2 blocks");
     __shared__ __align__(16) uint16_t stage[kFp4 ? kWarps : 1][kFp4 ? kPer * D : 8];
     const bool wide_v = kFp4 && aligned32(a.v) && a.v_stride % 16 == 0;
-    auto load_rows = [&](Rows& to, int tok) {
+    auto load_rows = [&](Rows& to, int tok, int chunk) {
+        const int kind = kind_of(chunk), first_row = first_row_of(chunk), last_row = rows_of(chunk) - 1;
+        const uint16_t* src = kind == 0 ? a.q + tok * a.q_stride : kind == 1 ? a.k + tok * a.k_stride : a.v + tok * a.v_stride;
         if constexpr (kFp4) {
             if (kind == 2) {
 #pragma unroll
                 for (int p = 0; p < kPasses; p += 2) {
-                    const int at = 16 * p + lane, r = min(first_row + at / kBlocks, row_end - 1);
-                    const Sector s = load_sector(src + tok * src_stride + r * D + at % kBlocks * 16, wide_v);
+                    const int at = 16 * p + lane, r = min(first_row + at / kBlocks, last_row);
+                    const Sector s = load_sector(src + r * D + at % kBlocks * 16, wide_v);
                     to.x[p][0] = make_uint2(s.lo.x, s.lo.y);
                     to.x[p][1] = make_uint2(s.lo.z, s.lo.w);
                     to.x[p + 1][0] = make_uint2(s.hi.x, s.hi.y);
@@ -157,17 +168,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
         }
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-            const int r = min(first_row + p * kRows + lane / kLanes, row_end - 1);  // past the last row: that row again
-            {
-                const uint16_t* row = src + tok * src_stride + r * D;
-                if constexpr (kInterleaved) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(row + off0);
-                    to.x[p][0] = make_uint2(w.x, w.y);
-                    to.x[p][1] = make_uint2(w.z, w.w);
-                } else {
-                    to.x[p][0] = *reinterpret_cast<const uint2*>(row + off0);
-                    to.x[p][1] = *reinterpret_cast<const uint2*>(row + off1);
-                }
+            const uint16_t* row = src + min(first_row + p * kRows + lane / kLanes, last_row) * D;  // past the last row: that row again
+            if constexpr (kInterleaved) {
+                const uint4 w = *reinterpret_cast<const uint4*>(row + off0);
+                to.x[p][0] = make_uint2(w.x, w.y);
+                to.x[p][1] = make_uint2(w.z, w.w);
+            } else {
+                to.x[p][0] = *reinterpret_cast<const uint2*>(row + off0);
+                to.x[p][1] = *reinterpret_cast<const uint2*>(row + off1);
             }
         }
     };
@@ -219,16 +227,22 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     Pos pos{{0, 0, 0}}, pos1{{0, 0, 0}};
     Angles ang{{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
     Where where{0, 0, Place::kOk};
-    load_rows(rows, tok0);
-    load_pos(pos, tok0);
-    if (tok0 + 1 < tok_end) load_pos(pos1, tok0 + 1);
-    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-    const uint16_t* wp = kind == 0 ? a.q_weight : a.k_weight;
-    if (a.norm && wp != nullptr && kind != 2) {
-        const uint2 w0 = __ldg(reinterpret_cast<const uint2*>(wp + off0)), w1 = __ldg(reinterpret_cast<const uint2*>(wp + off1));
-        const float2 p0 = unpack16(w0.x, kF16), p1 = unpack16(w0.y, kF16), p2 = unpack16(w1.x, kF16), p3 = unpack16(w1.y, kF16);
-        w[0] = p0.x; w[1] = p0.y; w[2] = p1.x; w[3] = p1.y;
-        w[4] = p2.x; w[5] = p2.y; w[6] = p3.x; w[7] = p3.y;
+    int tok = tok0, chunk = (int)(from - (long long)nth * chunks);
+    load_rows(rows, tok, chunk);
+    load_pos(pos, tok);
+    if (tok + 1 < a.total_tokens) load_pos(pos1, tok + 1);
+    const uint32_t one = kF16 ? 0x3C003C00u : 0x3F803F80u;
+    uint2 wq[2] = {{one, one}, {one, one}}, wk[2] = {{one, one}, {one, one}};
+    auto load_weight = [&](uint2 (&to)[2], const uint16_t* from) {
+        if (!a.norm || from == nullptr) return;
+        to[0] = __ldg(reinterpret_cast<const uint2*>(from + off0));
+        to[1] = __ldg(reinterpret_cast<const uint2*>(from + off1));
+    };
+    if (walks_chunks(kCache)) {
+        load_weight(wq, a.q_weight);
+        load_weight(wk, a.k_weight);
+    } else {
+        load_weight(wq, kind_of(chunk) == 0 ? a.q_weight : a.k_weight);
     }
     if constexpr (kAppend) {
         if (by_place) find_place(where, pos, tok0);
@@ -239,19 +253,27 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     }
 
 #pragma unroll 1
-    for (int tok = tok0; tok < tok_end; ++tok) {
+    for (int left = a.chunks_per_warp;; --left) {
+        const int kind = kind_of(chunk), first_row = first_row_of(chunk), row_end = min(rows_of(chunk), first_row + kPer);
+        const int now_tok = tok;
         // y = inv (x c1 + partner c2): elements 01, 23, 45, 67 of the lane
         F2 c1[4], c2[4];
+        {
+            const bool second = walks_chunks(kCache) && kind != 0;
+            const uint2 w0 = second ? wk[0] : wq[0], w1 = second ? wk[1] : wq[1];
+            const float2 p0 = unpack16(w0.x, kF16), p1 = unpack16(w0.y, kF16), p2 = unpack16(w1.x, kF16), p3 = unpack16(w1.y, kF16);
+            const float w[8] = {p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (kInterleaved) {
-                c1[i] = f2(w[2 * i] * ang.c[i], w[2 * i + 1] * ang.c[i]);
-                c2[i] = f2(-w[2 * i + 1] * ang.s[i], w[2 * i] * ang.s[i]);
-            } else {
-                const int e = 2 * (i & 1), n = 2 * i, m = (n + 4) & 7;  // pairs e, e + 1; elements n, n + 1; partners m, m + 1
-                const float sg = i < 2 ? -1.f : 1.f;
-                c1[i] = f2(w[n] * ang.c[e], w[n + 1] * ang.c[e + 1]);
-                c2[i] = f2(sg * w[m] * ang.s[e], sg * w[m + 1] * ang.s[e + 1]);
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kInterleaved) {
+                    c1[i] = f2(w[2 * i] * ang.c[i], w[2 * i + 1] * ang.c[i]);
+                    c2[i] = f2(-w[2 * i + 1] * ang.s[i], w[2 * i] * ang.s[i]);
+                } else {
+                    const int e = 2 * (i & 1), n = 2 * i, m = (n + 4) & 7;  // pairs e, e + 1; elements n, n + 1; partners m, m + 1
+                    const float sg = i < 2 ? -1.f : 1.f;
+                    c1[i] = f2(w[n] * ang.c[e], w[n + 1] * ang.c[e + 1]);
+                    c2[i] = f2(sg * w[m] * ang.s[e], sg * w[m + 1] * ang.s[e + 1]);
+                }
             }
         }
         // a padding token, or one that is out of range: nothing is written
@@ -260,14 +282,25 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
         if (skip && !padding && lane == 0) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         const int page = where.page, prow = where.row;
         const Rows now = rows;
-        if (tok + 1 < tok_end) {  // the next token's loads
-            load_rows(rows, tok + 1);
-            pos = pos1;
-            if constexpr (kAppend) find_place(where, pos, tok + 1);
-            in_table = start_angles(ang, pos);
-            if (tok + 2 < tok_end) load_pos(pos1, tok + 2);
+        const bool new_token = !walks_chunks(kCache) || ++chunk == chunks;
+        if (new_token) {
+            if (walks_chunks(kCache)) chunk = 0;
+            ++tok;
         }
-        if (skip) continue;
+        const bool more = left > 1 && tok < a.total_tokens;
+        if (more) {  // the next chunk's loads
+            load_rows(rows, tok, chunk);
+            if (new_token) {
+                pos = pos1;
+                if constexpr (kAppend) find_place(where, pos, tok);
+                in_table = start_angles(ang, pos);
+                if (tok + 1 < a.total_tokens) load_pos(pos1, tok + 1);
+            }
+        }
+        if (skip) {
+            if (!more) return;
+            continue;
+        }
 
         // all passes of a stage side by side: their chains of dependent steps overlap
         Rows out = now;
@@ -339,6 +372,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
                                            at % kBlocks, lo, hi, __ldg(&scales[r]));
                 }
                 __syncwarp();  // the stage is free again
+                if (!more) return;
                 continue;
             }
         }
@@ -348,8 +382,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
             const bool mine = r < row_end;
             const uint2 y0 = out.x[p][0], y1 = out.x[p][1];
             uint16_t* dst = nullptr;  // a 16-bit destination row
-            if (kind == 0) dst = a.q_out + tok * a.q_out_stride + (long long)r * D;
-            else if constexpr (!kAppend) dst = a.k_out + tok * a.k_out_stride + (long long)r * D;
+            if (kind == 0) dst = a.q_out + now_tok * a.q_out_stride + (long long)r * D;
+            else if constexpr (!kAppend) dst = a.k_out + now_tok * a.k_out_stride + (long long)r * D;
             if constexpr (kAppend && !kFp4) {
                 if (kind != 0) {
                     const long long slab = (long long)page * a.num_kv_heads + r;
@@ -373,6 +407,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
                 }
             }
         }
+        if (!more) return;
     }
 }
 
@@ -384,10 +419,11 @@ cudaError_t launch(NormRopeArgs a, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const long long chunks = (a.num_q_heads + kPer - 1) / kPer + (kCache >= 0 ? 2 : 1) * ((a.num_kv_heads + kPer - 1) / kPer);
-    // As many warps as stay on the SMs; each walks over its share of the tokens.
-    const long long resident = (long long)sms * kCtas * kWarps;
-    a.tokens_per_warp = (int)min((a.total_tokens * chunks + resident - 1) / resident, (long long)a.total_tokens);
-    const long long warps = ((long long)a.total_tokens + a.tokens_per_warp - 1) / a.tokens_per_warp * chunks;
+    // As many warps as stay on the SMs; each walks over its share of the tokens' chunks.
+    const long long resident = (long long)sms * kCtas * kWarps, all = a.total_tokens * chunks;
+    a.chunks_per_warp = (int)min((all + resident - 1) / resident, (long long)INT32_MAX);
+    const long long warps = walks_chunks(kCache) ? (all + a.chunks_per_warp - 1) / a.chunks_per_warp
+                                                 : ((long long)a.total_tokens + a.chunks_per_warp - 1) / a.chunks_per_warp * chunks;
     return launch_overlapped(norm_rope_kernel<D, kInterleaved, kCache, kF16>, dim3((unsigned)((warps + kWarps - 1) / kWarps)),
                              dim3(kWarps * 32), 0, stream, a);
 }
