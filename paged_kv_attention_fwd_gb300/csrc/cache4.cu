@@ -5,16 +5,15 @@
 // against 0.5625 (4-bit), 1 (e4m3) or 2 bytes of a page row per element.  A
 // thread owns one 16-element piece of a row -- the block of the 4-bit type, so
 // neither its largest magnitude nor its scale crosses threads.  A warp takes
-// 32 / (D / 16) consecutive tokens, whose rows are neighbours in a page, of up
-// to kHeads heads: what it touches of a slab is contiguous (at D = 128, 256
+// 32 / (D / 16) consecutive tokens, whose rows are neighbours in a page, of
+// several heads: what it touches of a slab is contiguous (at D = 128, 256
 // bytes of codes and one 32-byte sector of scales), and the search for the
-// tokens' sequence and page is paid once for all heads.  All loads of a batch
-// of heads are issued before any store.
+// tokens' sequence and page is paid once for all its heads.
 //
 // Measured: 4-bit rows of 262k tokens, 8 heads of 128, read back in 238 us
-// (1.59 GB, 6.7 TB/s, the memory's copy rate); 4096 tokens written and 37k
-// read back, two launches, 38.7 us (215 MB); 64 written and 64 read back 6.0 us.
-// Written alone, 32768 tokens of 8 heads take 32.2 us (172 MB, 5.3 TB/s).
+// (1.59 GB, 6.7 TB/s, the memory's copy rate); 32768 tokens written in 28.5
+// us (172 MB, 6.0 TB/s); 4096 written and 37k read back, two launches, 38 us
+// (215 MB); 64 written and 64 read back 5.8 us.
 #include "cache4.cuh"
 #include "pa_launch.h"
 #include "token_place.cuh"
@@ -23,22 +22,17 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-// Heads of a warp.  Writing has work to do between its loads and its stores, and wants more warps: 32768 tokens of 8
-// heads 32.3 us with 2, 37.2 with 4, 34.4 with 1; 512 tokens 3.3, 4.4, 2.9.  Reading back: 29.1 with 4, as with 2 and 1,
-// 262k rows 237.4, 238.3, 241.0.
-constexpr int kAppendHeads = 2, kGatherHeads = 4;
+constexpr int kHeads = 4;  // heads of a warp that reads back (262k rows 237.4 us, with 2 238.3, with 1 241.0)
 
-// This thread's token and the first of its warp's heads.
-// grid: x = groups of tokens, kWarps to a CTA; y = groups of kHeads heads
-template <int D, int kHeads>
+// This thread's token and piece of its rows.  grid: x = groups of tokens, kWarps to a CTA
+template <int D>
 struct Share {
     static constexpr int kLanes = D / 16, kTokens = 32 / kLanes;
-    int tok0, tok, piece, h0;  // tok0: the warp's first token
+    int tok0, tok, piece;  // tok0: the warp's first token
     __device__ __forceinline__ Share()
         : tok0((int)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * kTokens),
           tok(tok0 + (int)(threadIdx.x & 31) / kLanes),
-          piece((int)(threadIdx.x & 31) % kLanes),
-          h0((int)blockIdx.y * kHeads) {}
+          piece((int)(threadIdx.x & 31) % kLanes) {}
     // that of this thread's token; the whole warp calls it
     __device__ __forceinline__ Sequence sequence(const int32_t* __restrict__ cu, const int32_t* __restrict__ start_pos,
                                                  int batch) const {
@@ -46,26 +40,25 @@ struct Share {
     }
 };
 
+// grid.y: a warp takes every gridDim.y-th head, the next one's rows on their way while this one's are quantised
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_constant__ AppendArgs a) {
     grid_dependency_wait();
     allow_dependents_launch();
-    constexpr int kHeads = kAppendHeads;
-    const Share<D, kHeads> my;
+    const Share<D> my;
     if (my.tok0 >= a.total_new) return;
-    const int nh = min(kHeads, a.num_kv_heads - my.h0);
-    // rows first: they do not depend on the token's place
-    const bool wide = aligned32(a.k_new) && aligned32(a.v_new);
-    Sector w[kHeads][2];
-    const long long src = ((long long)my.tok * a.num_kv_heads + my.h0) * D + my.piece * 16;
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-        if (i < nh && my.tok < a.total_new) {
-            w[i][0] = load_sector(a.k_new + src + i * D, wide);
-            w[i][1] = load_sector(a.v_new + src + i * D, wide);
+    const bool wide = aligned32(a.k_new) && aligned32(a.v_new), mine = my.tok < a.total_new;
+    Sector k, v;
+    auto load = [&](int h) {
+        if (h < a.num_kv_heads && mine) {
+            const long long src = ((long long)my.tok * a.num_kv_heads + h) * D + my.piece * 16;
+            k = load_sector(a.k_new + src, wide);
+            v = load_sector(a.v_new + src, wide);
         }
+    };
+    load((int)blockIdx.y);  // rows first: they do not depend on the token's place
     const Sequence seq = my.sequence(a.cu_new, a.start_pos, a.batch);
-    if (my.tok >= a.total_new) return;
+    if (!mine) return;
     int page, row;
     long long pos;
     const Place at = token_place(my.tok, seq, a.block_table, a.batch, a.max_pages, a.num_pool_pages, page, row, pos);
@@ -73,16 +66,13 @@ __global__ void __launch_bounds__(kWarps * 32) append_fp4_kernel(const __grid_co
         if (my.piece == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         return;
     }
-    const long long slab = ((long long)page * a.num_kv_heads + my.h0) * fp4_slab_bytes(D);
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-        if (i < nh) {
-            const long long at_head = slab + (long long)i * fp4_slab_bytes(D);
-            fp4_store_block<D>(static_cast<uint8_t*>(a.k_pool) + at_head, row, my.piece, w[i][0].lo, w[i][0].hi,
-                               __ldg(&a.k_scale[my.h0 + i]));
-            fp4_store_block<D>(static_cast<uint8_t*>(a.v_pool) + at_head, row, my.piece, w[i][1].lo, w[i][1].hi,
-                               __ldg(&a.v_scale[my.h0 + i]));
-        }
+    for (int h = (int)blockIdx.y; h < a.num_kv_heads; h += (int)gridDim.y) {
+        const Sector k_now = k, v_now = v;
+        load(h + (int)gridDim.y);
+        const long long slab = ((long long)page * a.num_kv_heads + h) * fp4_slab_bytes(D);
+        fp4_store_block<D>(static_cast<uint8_t*>(a.k_pool) + slab, row, my.piece, k_now.lo, k_now.hi, __ldg(&a.k_scale[h]));
+        fp4_store_block<D>(static_cast<uint8_t*>(a.v_pool) + slab, row, my.piece, v_now.lo, v_now.hi, __ldg(&a.v_scale[h]));
+    }
 }
 
 // 16 elements as they lie in a page, before conversion
@@ -142,13 +132,12 @@ __device__ __forceinline__ void store_piece(uint16_t* dst, const Piece<kType>& p
     store_sector(dst, Sector{out[0], out[1]}, wide);
 }
 
-// grid as for append_fp4_kernel
+// grid.y: groups of kHeads heads
 template <int D, int kType>
 __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_constant__ GatherArgs a) {
     grid_dependency_wait();
     allow_dependents_launch();
-    constexpr int kHeads = kGatherHeads;
-    const Share<D, kHeads> my;
+    const Share<D> my;
     if (my.tok0 >= a.total) return;
     const Sequence seq = my.sequence(a.cu, a.start_pos, a.batch);
     if (my.tok >= a.total) return;
@@ -159,8 +148,8 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
         if (my.piece == 0 && at == Place::kOutOfRange) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         return;
     }
-    const int nh = min(kHeads, a.num_kv_heads - my.h0);
-    const long long slab = (long long)page * a.num_kv_heads + my.h0;
+    const int h0 = (int)blockIdx.y * kHeads, nh = min(kHeads, a.num_kv_heads - h0);
+    const long long slab = (long long)page * a.num_kv_heads + h0;
     const bool wide_in = aligned32(a.k_pool) && aligned32(a.v_pool), wide_out = aligned32(a.k_out) && aligned32(a.v_out);
     Piece<kType> k[kHeads], v[kHeads];
 #pragma unroll
@@ -169,29 +158,43 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
             k[i] = load_piece<D, kType>(a.k_pool, slab + i, row, my.piece, wide_in);
             v[i] = load_piece<D, kType>(a.v_pool, slab + i, row, my.piece, wide_in);
         }
-    const long long dst = ((long long)my.tok * a.num_kv_heads + my.h0) * D + my.piece * 16;
+    const long long dst = ((long long)my.tok * a.num_kv_heads + h0) * D + my.piece * 16;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
         if (i < nh) {
             float ks = 1.f, vs = 1.f;
             if constexpr (kType == PA_KV_FP4_E2M1 || kType == PA_KV_FP8_E4M3) {
-                ks = __ldg(&a.k_scale[my.h0 + i]);
-                vs = __ldg(&a.v_scale[my.h0 + i]);
+                ks = __ldg(&a.k_scale[h0 + i]);
+                vs = __ldg(&a.v_scale[h0 + i]);
             }
             store_piece<kType>(a.k_out + dst + i * D, k[i], ks, wide_out);
             store_piece<kType>(a.v_out + dst + i * D, v[i], vs, wide_out);
         }
 }
 
-template <int D, int kHeads>
-dim3 token_grid(int tokens, int heads) {
-    constexpr int per_cta = kWarps * Share<D, kHeads>::kTokens;
-    return dim3((unsigned)((tokens + per_cta - 1) / per_cta), (unsigned)((heads + kHeads - 1) / kHeads));
+template <int D>
+unsigned token_groups(int tokens) {
+    constexpr int per_cta = kWarps * Share<D>::kTokens;
+    return (unsigned)((tokens + per_cta - 1) / per_cta);
+}
+
+// A token's heads are dealt to as many warps as find room on the SMs together, 8 CTAs of them each: 32768 tokens of 8
+// heads 28.5 us with all heads in one warp and 38 with one head each, 64 tokens 6.3 and 3.0.
+template <int D>
+cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const unsigned groups = token_groups<D>(a.total_new), room = (unsigned)sms * 8 / groups;
+    const unsigned heads = (unsigned)a.num_kv_heads, ways = room < 1 ? 1 : room < heads ? room : heads;
+    const unsigned each = (heads + ways - 1) / ways;  // heads of a warp, and as few warps as take them
+    return launch_overlapped(append_fp4_kernel<D>, dim3(groups, (heads + each - 1) / each), dim3(kWarps * 32), 0, stream, a);
 }
 
 template <int D>
 cudaError_t launch_gather_d(const GatherArgs& a, int kv_dtype, cudaStream_t stream) {
-    const dim3 grid = token_grid<D, kGatherHeads>(a.total, a.num_kv_heads), block(kWarps * 32);
+    const dim3 grid(token_groups<D>(a.total), (unsigned)((a.num_kv_heads + kHeads - 1) / kHeads)), block(kWarps * 32);
     switch (kv_dtype) {
         case PA_KV_FP4_E2M1: return launch_overlapped(gather_kernel<D, PA_KV_FP4_E2M1>, grid, block, 0, stream, a);
         case PA_KV_FP8_E4M3: return launch_overlapped(gather_kernel<D, PA_KV_FP8_E4M3>, grid, block, 0, stream, a);
@@ -202,10 +205,7 @@ cudaError_t launch_gather_d(const GatherArgs& a, int kv_dtype, cudaStream_t stre
 }  // namespace
 
 cudaError_t launch_append_fp4(const AppendArgs& a, cudaStream_t stream) {
-    const dim3 block(kWarps * 32);
-    return a.head_dim == 128
-               ? launch_overlapped(append_fp4_kernel<128>, token_grid<128, kAppendHeads>(a.total_new, a.num_kv_heads), block, 0, stream, a)
-               : launch_overlapped(append_fp4_kernel<64>, token_grid<64, kAppendHeads>(a.total_new, a.num_kv_heads), block, 0, stream, a);
+    return a.head_dim == 128 ? launch_append_d<128>(a, stream) : launch_append_d<64>(a, stream);
 }
 
 cudaError_t launch_gather(const GatherArgs& a, int head_dim, int kv_dtype, cudaStream_t stream) {

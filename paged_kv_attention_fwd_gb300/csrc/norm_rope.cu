@@ -18,8 +18,8 @@
 //
 // Measured: 16384 tokens, 64 + 8 heads of 128 (613 MB), 96.5 us a call, 6.4
 // TB/s; the append form, 8 x 512 tokens, 32 + 8 + 8 heads, 21 us with 16-bit
-// pages (103 MB); one token 3 us, a launch.  3 CTAs an SM 109 and 23.2 us, 5
-// 101 and 24.0, 2 passes and 6 CTAs 111 and 25.2.  Rows through a ring of bulk
+// pages (103 MB); one token 3 us, a launch.  3 CTAs an SM 105 and 23.0 us, 5
+// 107 and 24.2, 2 passes and 6 CTAs 110 and 24.8.  Rows through a ring of bulk
 // copies in shared memory, 3 or 4 deep, were no faster (100 and 23): the loads
 // in flight are not what bounds it.
 #include "cache4.cuh"
