@@ -10,18 +10,25 @@
 // element and a table row per token; what it must not be is issue-bound.  So
 // a head row is held by D / 8 lanes, 8 elements each, in two groups of 4 that
 // pair up with one another (the rotation needs no shuffle in either pairing);
-// a warp takes up to kPasses rows per lane of one kind (queries, keys or
-// values) at a time, with the weights multiplied into the cosines and sines,
+// a warp takes 32 / (D / 8) tokens and kPasses heads of one kind (queries, keys
+// or values) at a time, with the weights multiplied into the cosines and sines,
 //   a' = inv (a (w_a cos) - b (w_b sin)),  b' = inv (b (w_b cos) + a (w_a sin)),
 // the arithmetic runs on pairs of fp32 (f32x2), and a warp goes on to the next
-// such chunk with its elements and angles already on the way.
+// such chunk with its elements and angles already on the way.  The warps are as
+// many as the SMs hold, with equal shares: 4097 tokens, 16 + 4 heads of 64, 4.9
+// us, where whole multiples of the largest share, in fewer warps, took 5.9.
 //
-// Measured: 16384 tokens, 64 + 8 heads of 128 (613 MB), 96.5 us a call, 6.4
-// TB/s; the append form, 8 x 512 tokens, 32 + 8 + 8 heads, 21 us with 16-bit
-// pages (103 MB); one token 3 us, a launch.  3 CTAs an SM 105 and 23.0 us, 5
-// 107 and 24.2, 2 passes and 6 CTAs 110 and 24.8.  Rows through a ring of bulk
-// copies in shared memory, 3 or 4 deep, were no faster (100 and 23): the loads
-// in flight are not what bounds it.
+// Several tokens, not more heads, fill the lanes: a kind may have one head only.
+// One token at a time, 65536 tokens of 8 + 1 heads took 72 us (59 now), of 3 + 3
+// heads of 64 68 us (22.5).
+//
+// Measured: 16384 tokens, 64 + 8 heads of 128 (613 MB), 96.8 us a call, 6.3
+// TB/s; the append form, 8 x 512 tokens, 32 + 8 + 8 heads, 21.3 us with 16-bit
+// pages (103 MB), 22.1 with e4m3 ones, 20.3 with 4-bit ones; one token 3 us, a
+// launch.  Against 97 and 22 us, 3 CTAs an SM took 106 and 23.4, 5 104 and 26.7,
+// 2 passes and 6 CTAs 114 and 25.8.  Rows through a ring of bulk copies in
+// shared memory, 3 or 4 deep, were no faster: the loads in flight are not what
+// bounds it.
 #include "cache4.cuh"
 #include "f32x2.cuh"
 #include "pa_launch.h"
@@ -32,14 +39,14 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kCtas = 4;    // CTAs of an SM
-constexpr int kPasses = 4;  // rows of a lane in a chunk, whose loads are in flight together
+constexpr int kPasses = 4;  // heads of a chunk: rows of a lane whose loads are in flight together
 
-// Whether a warp goes from one chunk of a token to the next (else from one
-// token to the next with the same chunk).  With a cache the kinds differ in
+// Whether a warp goes from one chunk of its tokens to the next (else from some
+// tokens to the next with the same chunk).  With a cache the kinds differ in
 // work, keys and values that are quantised taking longest, and each warp needs
-// its share of all: 8 x 512 tokens, 32 + 8 + 8 heads, 21.0 us against 22.7 with
-// 16-bit pages, 23.6 against 26.9 with e4m3 ones, 22.0 against 26.1 with 4-bit
-// ones.  Without, one chunk keeps its weights: 16384 tokens 96.5 us against 99.2.
+// its share of all: 8 x 512 tokens, 32 + 8 + 8 heads, 21.8 us against 22.0 with
+// 16-bit pages, 23.3 against 32.6 with e4m3 ones, 21.0 against 31.9 with 4-bit
+// ones.  Without, one chunk keeps its weights: 16384 tokens 97.0 us against 98.9.
 constexpr bool walks_chunks(int cache) { return cache >= 0; }
 
 __device__ __forceinline__ float2 unpack16(uint32_t w, bool f16) {
@@ -119,19 +126,21 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     constexpr bool kAppend = kCache >= 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kLanes;
-    // A token's rows come in chunks of one kind: queries, keys, values
-    constexpr int kPer = kPasses * kRows;
-    const int qchunks = (a.num_q_heads + kPer - 1) / kPer, kchunks = (a.num_kv_heads + kPer - 1) / kPer;
+    // The heads of one kind -- queries, keys, values -- come in chunks of kPasses, tokens in groups of kRows; lanes of one
+    // sub hold the rows of one token
+    const int sub = lane / kLanes, last_token = a.total_tokens - 1;
+    const int qchunks = (a.num_q_heads + kPasses - 1) / kPasses, kchunks = (a.num_kv_heads + kPasses - 1) / kPasses;
     const int chunks = qchunks + (kAppend ? 2 : 1) * kchunks;
+    // This warp's share: a.share (the first a.longer warps one more) of the chunks of all groups, or of the groups
     const int id = (int)blockIdx.x * kWarps + warp;
-    const long long from = walks_chunks(kCache) ? (long long)id * a.chunks_per_warp : id;
-    const int nth = from <= 0x7FFFFFFF ? (int)from / chunks : (int)min(from / chunks, (long long)a.total_tokens);
-    const long long first = walks_chunks(kCache) ? nth : (long long)nth * a.chunks_per_warp;
-    if (first >= a.total_tokens) return;
-    const int tok0 = (int)first;
+    if (id >= a.warps) return;
+    const int nth = walks_chunks(kCache) ? id : id / chunks;
+    const long long from = (long long)nth * a.share + min(nth, a.longer);
+    const int share = a.share + (nth < a.longer);
+    const int first = !walks_chunks(kCache) ? (int)from : from <= 0x7FFFFFFF ? (int)from / chunks : (int)(from / chunks);
     auto kind_of = [&](int c) { return c < qchunks ? 0 : c < qchunks + kchunks ? 1 : 2; };
-    auto first_row_of = [&](int c) { return (c < qchunks ? c : c < qchunks + kchunks ? c - qchunks : c - qchunks - kchunks) * kPer; };
-    auto rows_of = [&](int c) { return c < qchunks ? a.num_q_heads : a.num_kv_heads; };
+    auto first_head_of = [&](int c) { return (c < qchunks ? c : c < qchunks + kchunks ? c - qchunks : c - qchunks - kchunks) * kPasses; };
+    auto heads_of = [&](int c) { return c < qchunks ? a.num_q_heads : a.num_kv_heads; };
 
     // where this lane's two groups of 4 elements lie in a row, and whether they turn
     const int half = a.rope_dim / 2;
@@ -142,22 +151,23 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     struct Rows {
         uint2 x[kPasses][2];
     };
-    // 4-bit pages: kBlocks blocks of 16 elements to a row, every 32nd of the warp's a lane's.  Values are loaded that way,
-    // keys get there through shared memory.
+    // 4-bit pages: a row has kBlocks blocks of 16 elements, and the chunk's rows kPasses / 2 for every lane, of the token
+    // block_sub and the heads block_head and that plus 2.  Values are loaded that way, keys get there through shared
+    // memory.
     constexpr bool kFp4 = kCache == PA_KV_FP4_E2M1;
     constexpr int kBlocks = D / 16;
     static_assert(kPasses % 2 == 0, "a lane holds kPasses / 2 blocks");
-    __shared__ __align__(16) uint16_t stage[kFp4 ? kWarps : 1][kFp4 ? kPer * D : 8];
+    __shared__ __align__(16) uint16_t stage[kFp4 ? kWarps : 1][kFp4 ? kPasses * kRows * D : 8];
     const bool wide_v = kFp4 && aligned32(a.v) && a.v_stride % 16 == 0;
+    const int block_sub = lane / kBlocks % kRows, block_head = lane / 16, piece = lane % kBlocks;
     auto load_rows = [&](Rows& to, int tok, int chunk) {
-        const int kind = kind_of(chunk), first_row = first_row_of(chunk), last_row = rows_of(chunk) - 1;
-        const uint16_t* src = kind == 0 ? a.q + tok * a.q_stride : kind == 1 ? a.k + tok * a.k_stride : a.v + tok * a.v_stride;
+        const int kind = kind_of(chunk), first_head = first_head_of(chunk), last_head = heads_of(chunk) - 1;
         if constexpr (kFp4) {
             if (kind == 2) {
+                const uint16_t* src = a.v + min(tok + block_sub, last_token) * a.v_stride + piece * 16;
 #pragma unroll
                 for (int p = 0; p < kPasses; p += 2) {
-                    const int at = 16 * p + lane, r = min(first_row + at / kBlocks, last_row);
-                    const Sector s = load_sector(src + r * D + at % kBlocks * 16, wide_v);
+                    const Sector s = load_sector(src + min(first_head + p + block_head, last_head) * D, wide_v);
                     to.x[p][0] = make_uint2(s.lo.x, s.lo.y);
                     to.x[p][1] = make_uint2(s.lo.z, s.lo.w);
                     to.x[p + 1][0] = make_uint2(s.hi.x, s.hi.y);
@@ -166,9 +176,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
                 return;
             }
         }
+        const int mine = min(tok + sub, last_token);  // past the last token or head: that one again
+        const uint16_t* src = kind == 0 ? a.q + mine * a.q_stride : kind == 1 ? a.k + mine * a.k_stride : a.v + mine * a.v_stride;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-            const uint16_t* row = src + min(first_row + p * kRows + lane / kLanes, last_row) * D;  // past the last row: that row again
+            const uint16_t* row = src + min(first_head + p, last_head) * D;
             if constexpr (kInterleaved) {
                 const uint4 w = *reinterpret_cast<const uint4*>(row + off0);
                 to.x[p][0] = make_uint2(w.x, w.y);
@@ -187,7 +199,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
         if (a.rope_dim == 0 || by_place) return;
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-            if (i < a.num_axes) to.at[i] = __ldg(&a.positions[(long long)i * a.total_tokens + tok]);
+            if (i < a.num_axes) to.at[i] = __ldg(&a.positions[(long long)i * a.total_tokens + min(tok + sub, last_token)]);
     };
     struct Where {  // a token's place in the cache
         int page, row;
@@ -195,18 +207,19 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     };
     // Tokens come in order: the sequence is searched for where it changes, its block table read where the page does.
     Sequence seq{-1, 0, 0};
-    int seq_end = tok0;  // the first token that is not seq's
+    int seq_end = 0;  // the first token that is not seq's
     auto find_place = [&](Where& to, Pos& pos, int tok) {
-        if (tok >= seq_end) {
-            seq = warp_sequences<1>(tok, 0, a.cu_new, a.start_pos, a.batch);
-            seq_end = seq.b >= a.batch ? 0x7FFFFFFF : seq.b < 0 ? tok + 1 : __ldg(&a.cu_new[seq.b + 1]);
-            to.row = kPage - 1;
+        const int mine = tok + sub;
+        const bool search = __any_sync(0xffffffffu, mine >= seq_end);
+        if (search) {
+            seq = warp_sequences<kRows>(tok, sub, a.cu_new, a.start_pos, a.batch);
+            seq_end = seq.b >= a.batch ? 0x7FFFFFFF : seq.b < 0 ? mine + 1 : __ldg(&a.cu_new[seq.b + 1]);
         }
-        long long cpos = (long long)seq.start + (tok - seq.cu);
-        if (to.row == kPage - 1 || to.place != Place::kOk)
-            to.place = token_place(tok, seq, a.block_table, a.batch, a.max_pages, a.num_pool_pages, to.page, to.row, cpos);
+        long long cpos = (long long)seq.start + (mine - seq.cu);
+        if (search || to.place != Place::kOk || to.row + kRows >= kPage)
+            to.place = token_place(mine, seq, a.block_table, a.batch, a.max_pages, a.num_pool_pages, to.page, to.row, cpos);
         else
-            ++to.row;
+            to.row += kRows;
         if (by_place) {
             const int p = to.place == Place::kOk ? (int)min(cpos, (long long)a.max_position) : 0;
             pos.at[0] = pos.at[1] = pos.at[2] = p;
@@ -227,10 +240,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
     Pos pos{{0, 0, 0}}, pos1{{0, 0, 0}};
     Angles ang{{1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
     Where where{0, 0, Place::kOk};
-    int tok = tok0, chunk = (int)(from - (long long)nth * chunks);
+    int tok = first * kRows;  // the group's first token
+    int chunk = walks_chunks(kCache) ? (int)(from - (long long)first * chunks) : id - nth * chunks;
     load_rows(rows, tok, chunk);
     load_pos(pos, tok);
-    if (tok + 1 < a.total_tokens) load_pos(pos1, tok + 1);
+    load_pos(pos1, tok + kRows);
     const uint32_t one = kF16 ? 0x3C003C00u : 0x3F803F80u;
     uint2 wq[2] = {{one, one}, {one, one}}, wk[2] = {{one, one}, {one, one}};
     auto load_weight = [&](uint2 (&to)[2], const uint16_t* from) {
@@ -245,17 +259,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
         load_weight(wq, kind_of(chunk) == 0 ? a.q_weight : a.k_weight);
     }
     if constexpr (kAppend) {
-        if (by_place) find_place(where, pos, tok0);
+        if (by_place) find_place(where, pos, tok);
     }
     bool in_table = start_angles(ang, pos);
     if constexpr (kAppend) {
-        if (!by_place) find_place(where, pos, tok0);
+        if (!by_place) find_place(where, pos, tok);
     }
 
 #pragma unroll 1
-    for (int left = a.chunks_per_warp;; --left) {
-        const int kind = kind_of(chunk), first_row = first_row_of(chunk), row_end = min(rows_of(chunk), first_row + kPer);
-        const int now_tok = tok;
+    for (int left = share;; --left) {
+        const int kind = kind_of(chunk), first_head = first_head_of(chunk), heads = heads_of(chunk);
+        const int my_tok = tok + sub;
         // y = inv (x c1 + partner c2): elements 01, 23, 45, 67 of the lane
         F2 c1[4], c2[4];
         {
@@ -277,27 +291,28 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
             }
         }
         // a padding token, or one that is out of range: nothing is written
-        const bool padding = where.place == Place::kPadding || (where.place == Place::kOk && a.rope_dim > 0 && pos.at[0] < 0);
+        const bool padding = my_tok > last_token || where.place == Place::kPadding ||
+                             (where.place == Place::kOk && a.rope_dim > 0 && pos.at[0] < 0);
         const bool skip = padding || where.place != Place::kOk || !in_table;
-        if (skip && !padding && lane == 0) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
+        if (skip && !padding && l == 0) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         const int page = where.page, prow = where.row;
         const Rows now = rows;
-        const bool new_token = !walks_chunks(kCache) || ++chunk == chunks;
-        if (new_token) {
+        const bool new_tokens = !walks_chunks(kCache) || ++chunk == chunks;
+        if (new_tokens) {
             if (walks_chunks(kCache)) chunk = 0;
-            ++tok;
+            tok += kRows;
         }
-        const bool more = left > 1 && tok < a.total_tokens;
+        const bool more = left > 1;
         if (more) {  // the next chunk's loads
             load_rows(rows, tok, chunk);
-            if (new_token) {
+            if (new_tokens) {
                 pos = pos1;
                 if constexpr (kAppend) find_place(where, pos, tok);
                 in_table = start_angles(ang, pos);
-                if (tok + 1 < a.total_tokens) load_pos(pos1, tok + 1);
+                load_pos(pos1, tok + kRows);
             }
         }
-        if (skip) {
+        if (__all_sync(0xffffffffu, skip)) {
             if (!more) return;
             continue;
         }
@@ -350,7 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
                 if (kind == 1) {
 #pragma unroll
                     for (int p = 0; p < kPasses; ++p) {
-                        uint16_t* row = st + (p * kRows + lane / kLanes) * D;
+                        uint16_t* row = st + (p * kRows + sub) * D;
                         *reinterpret_cast<uint2*>(row + off0) = out.x[p][0];
                         *reinterpret_cast<uint2*>(row + off1) = out.x[p][1];
                     }
@@ -358,18 +373,21 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
                 }
                 uint8_t* pool = static_cast<uint8_t*>(kind == 2 ? a.v_pool : a.k_pool);
                 const float* scales = kind == 2 ? a.v_scale : a.k_scale;
+                const int block_page = __shfl_sync(0xffffffffu, skip ? -1 : page, block_sub * kLanes);
+                const int block_row = __shfl_sync(0xffffffffu, prow, block_sub * kLanes);
 #pragma unroll
                 for (int p = 0; p < kPasses; p += 2) {
-                    const int at = 16 * p + lane, r = first_row + at / kBlocks;
+                    const int h = first_head + p + block_head;
                     uint4 lo = make_uint4(out.x[p][0].x, out.x[p][0].y, out.x[p][1].x, out.x[p][1].y);
                     uint4 hi = make_uint4(out.x[p + 1][0].x, out.x[p + 1][0].y, out.x[p + 1][1].x, out.x[p + 1][1].y);
                     if (kind == 1) {
-                        lo = *reinterpret_cast<const uint4*>(st + at * 16);
-                        hi = *reinterpret_cast<const uint4*>(st + at * 16 + 8);
+                        const uint4* w = reinterpret_cast<const uint4*>(st + (16 * p + lane) * 16);
+                        lo = w[0];
+                        hi = w[1];
                     }
-                    if (r < row_end)
-                        fp4_store_block<D>(pool + ((long long)page * a.num_kv_heads + r) * fp4_slab_bytes(D), prow,
-                                           at % kBlocks, lo, hi, __ldg(&scales[r]));
+                    if (h < heads && block_page >= 0)
+                        fp4_store_block<D>(pool + ((long long)block_page * a.num_kv_heads + h) * fp4_slab_bytes(D), block_row,
+                                           piece, lo, hi, __ldg(&scales[h]));
                 }
                 __syncwarp();  // the stage is free again
                 if (!more) return;
@@ -378,12 +396,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
         }
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-            const int r = first_row + p * kRows + lane / kLanes;
-            const bool mine = r < row_end;
+            const int r = first_head + p;
+            const bool mine = r < heads && !skip;
             const uint2 y0 = out.x[p][0], y1 = out.x[p][1];
             uint16_t* dst = nullptr;  // a 16-bit destination row
-            if (kind == 0) dst = a.q_out + now_tok * a.q_out_stride + (long long)r * D;
-            else if constexpr (!kAppend) dst = a.k_out + now_tok * a.k_out_stride + (long long)r * D;
+            if (kind == 0) dst = a.q_out + my_tok * a.q_out_stride + (long long)r * D;
+            else if constexpr (!kAppend) dst = a.k_out + my_tok * a.k_out_stride + (long long)r * D;
             if constexpr (kAppend && !kFp4) {
                 if (kind != 0) {
                     const long long slab = (long long)page * a.num_kv_heads + r;
@@ -413,18 +431,21 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
 
 template <int D, bool kInterleaved, int kCache, bool kF16>
 cudaError_t launch(NormRopeArgs a, cudaStream_t stream) {
-    constexpr int kPer = 32 / (D / 8) * kPasses;
+    constexpr int kRows = 32 / (D / 8);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const long long chunks = (a.num_q_heads + kPer - 1) / kPer + (kCache >= 0 ? 2 : 1) * ((a.num_kv_heads + kPer - 1) / kPer);
-    // As many warps as stay on the SMs; each walks over its share of the tokens' chunks.
-    const long long resident = (long long)sms * kCtas * kWarps, all = a.total_tokens * chunks;
-    a.chunks_per_warp = (int)min((all + resident - 1) / resident, (long long)INT32_MAX);
-    const long long warps = walks_chunks(kCache) ? (all + a.chunks_per_warp - 1) / a.chunks_per_warp
-                                                 : ((long long)a.total_tokens + a.chunks_per_warp - 1) / a.chunks_per_warp * chunks;
-    return launch_overlapped(norm_rope_kernel<D, kInterleaved, kCache, kF16>, dim3((unsigned)((warps + kWarps - 1) / kWarps)),
+    const long long chunks = (a.num_q_heads + kPasses - 1) / kPasses + (kCache >= 0 ? 2 : 1) * ((a.num_kv_heads + kPasses - 1) / kPasses);
+    const long long groups = (a.total_tokens - 1) / kRows + 1;
+    // As many warps as stay on the SMs, their shares as equal as can be
+    const long long resident = (long long)sms * kCtas * kWarps;
+    const long long columns = walks_chunks(kCache) ? 1 : chunks, all = walks_chunks(kCache) ? groups * chunks : groups;
+    const long long sharers = min(all, max(resident / columns, 1ll));
+    a.warps = (int)(sharers * columns);
+    a.share = (int)(all / sharers);
+    a.longer = (int)(all % sharers);
+    return launch_overlapped(norm_rope_kernel<D, kInterleaved, kCache, kF16>, dim3((unsigned)((a.warps + kWarps - 1) / kWarps)),
                              dim3(kWarps * 32), 0, stream, a);
 }
 

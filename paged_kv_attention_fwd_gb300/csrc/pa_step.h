@@ -45,7 +45,7 @@ struct NormRopeArgs {
     int* status;
     long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
     int32_t total_tokens, num_q_heads, num_kv_heads, rope_dim, interleaved, num_axes, max_position, f16, norm;
-    int32_t chunks_per_warp;  // set by the launch
+    int32_t warps, share, longer;  // set by the launch
     int32_t sections[2];  // pairs of the first two axes (the third takes the rest)
     float eps;
     // append only

@@ -56,7 +56,7 @@ def compare(got, x, weight, pos, table, rot, inter, sections, eps, norm, dtype):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("inter", [False, True])
-@pytest.mark.parametrize("t,hq,hk", [(1, 8, 2), (3, 1, 1), (5, 5, 3), (130, 16, 4), (1, 33, 7)])
+@pytest.mark.parametrize("t,hq,hk", [(1, 8, 2), (3, 1, 1), (5, 5, 3), (130, 16, 4), (1, 33, 7), (37, 32, 16)])
 def test_against_fp64(d, dtype, inter, t, hq, hk):
     q, k, _, w, pos, sections, table = make(t, hq, hk, d, dtype, seed=t + d)
     sh = ops.rope_shapes(q, k, rope_dim=d, max_position=4096, interleaved=inter, sections=sections, eps=1e-6)
@@ -157,7 +157,7 @@ def test_keys_alone_and_no_rotation():
 # ----------------------------------------------------------------- straight into the pages
 
 @pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3", "fp4"])
-@pytest.mark.parametrize("d,hq,hk", [(128, 8, 2), (128, 5, 5), (64, 7, 1), (64, 16, 8)])
+@pytest.mark.parametrize("d,hq,hk", [(128, 8, 2), (128, 5, 5), (64, 7, 1), (64, 16, 8), (128, 16, 8), (64, 16, 16)])
 @pytest.mark.parametrize("inter,rot,axes", [(False, None, 1), (True, 40, 2), (False, 24, 3)])
 def test_append_is_the_two_calls(kv, d, hq, hk, inter, rot, axes):
     dtype = "f16" if kv == "f16" else "bf16"
