@@ -629,58 +629,101 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
     }
 }
 
-// Merges the splits of every sequence that has more than one, in split order:
+// Merges the splits of every sequence that has more than one:
 //   lse = m + ln sum_s exp(lse_s - m),  out = sum_s exp(lse_s - lse) o_s
-// One warp per (sequence, query head); its loads of all splits are in flight
-// together.  A kernel of its own: merged by the last CTA to finish a split
-// instead, the wait for the partials and two rounds of dependent loads fell
-// into that CTA's stream of pages (64 sequences of up to 4096 keys: 70.7 us a
-// call, 51.1 with the merge moved here).
+// A kernel of its own: merged by the last CTA to finish a split instead, the
+// wait for the partials and two rounds of dependent loads fell into that CTA's
+// stream of pages (64 sequences of up to 4096 keys: 70.7 us a call, 51.1 with
+// the merge moved here).
+//
+// A CTA has kMergeWarps rows (sequence, query head), or one where that leaves
+// SMs empty.  A warp takes a row of its own if it has up to kTogether splits,
+// whose loads are then in flight together; the CTA's warps share those of a row
+// that has more, or is alone, every kMergeWarps-th each.  The order of the sums
+// depends on the number of splits and of rows only.  One sequence of 131072 keys
+// in 57 splits, 32 heads: 4 us of a 33 us call, 12 of 41 with a warp a row.
+constexpr int kMergeWarps = 4, kTogether = 8;
+
 template <int D>
-__global__ void __launch_bounds__(128) combine_fp4_kernel(const __grid_constant__ DecodeArgs a) {
-    const int w = (int)(blockIdx.x * 4 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const bool any = w < a.batch * a.num_q_heads;
-    const int b = any ? w / a.num_q_heads : 0, h = any ? w % a.num_q_heads : 0;
-    const int n = any ? __ldg(&a.meta[kMetaHeader + b]) : 0;
-    const long long base = (long long)__ldg(&a.meta[kMetaHeader + a.batch + b]) * a.num_q_heads + h;
+__global__ void __launch_bounds__(kMergeWarps * 32) combine_fp4_kernel(const __grid_constant__ DecodeArgs a, int rows) {
+    constexpr int E = D / 32;  // elements of a lane
+    __shared__ float part[kMergeWarps][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long all = (long long)a.batch * a.num_q_heads, row0 = (long long)blockIdx.x * rows;
+    int splits = 0;  // lane r: of the CTA's row r
+    long long base = 0;
+    if (lane < rows && row0 + lane < all) {
+        const int b = (int)((row0 + lane) / a.num_q_heads), h = (int)(row0 + lane - (long long)b * a.num_q_heads);
+        splits = __ldg(&a.meta[kMetaHeader + b]);
+        base = (long long)__ldg(&a.meta[kMetaHeader + a.batch + b]) * a.num_q_heads + h;
+    }
     // The metadata was complete before the attention kernel let this one in;
     // its partials are now.  Every warp waits, also one with nothing to do:
     // this kernel must not be complete before that one.
     grid_dependency_wait();
-    if (n <= 1) return;
-    // lanes hold the splits' log-sum-exps (at most PA_MAX_SPLITS = 64)
-    const float l0 = lane < n ? a.lse_part[base + (long long)lane * a.num_q_heads] : -INFINITY;
-    const float l1 = lane + 32 < n ? a.lse_part[base + (long long)(lane + 32) * a.num_q_heads] : -INFINITY;
-    float mm = fmaxf(l0, l1);
+    for (int r = 0; r < rows; ++r) {
+        const int n = __shfl_sync(0xffffffffu, splits, r);
+        const bool alone = rows > 1 && n <= kTogether;  // of a warp: its own row
+        if (n <= 1 || (alone && r != warp)) continue;
+        const long long at = __shfl_sync(0xffffffffu, base, r);
+        const int s0 = alone ? 0 : warp, step = alone ? 1 : kMergeWarps;
+        // lanes hold the splits' log-sum-exps (at most PA_MAX_SPLITS = 64)
+        const float l0 = lane < n ? a.lse_part[at + (long long)lane * a.num_q_heads] : -INFINITY;
+        const float l1 = lane + 32 < n ? a.lse_part[at + (long long)(lane + 32) * a.num_q_heads] : -INFINITY;
+        float acc[E] = {}, o[kTogether][E];
+        auto load = [&](int first) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    // a split without keys weighs nothing; a NaN stays one
-    const float w0 = l0 == -INFINITY ? 0.f : __expf(l0 - mm), w1 = l1 == -INFINITY ? 0.f : __expf(l1 - mm);
-    float sum = 0.f, acc[D / 32] = {};
-#pragma unroll 8
-    for (int s = 0; s < n; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
-        const float* o = a.o_part + (base + (long long)s * a.num_q_heads) * D + lane * (D / 32);
-        sum += ws;
-        if constexpr (D == 128) {
-            const float4 v = *reinterpret_cast<const float4*>(o);
-            acc[0] = fmaf(ws, v.x, acc[0]);
-            acc[1] = fmaf(ws, v.y, acc[1]);
-            acc[2] = fmaf(ws, v.z, acc[2]);
-            acc[3] = fmaf(ws, v.w, acc[3]);
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(o);
-            acc[0] = fmaf(ws, v.x, acc[0]);
-            acc[1] = fmaf(ws, v.y, acc[1]);
+            for (int i = 0; i < kTogether; ++i) {
+                const int s = first + i * step;
+                if (s < n) {
+                    const float* src = a.o_part + (at + (long long)s * a.num_q_heads) * D + lane * E;
+                    if constexpr (D == 128) *reinterpret_cast<float4*>(o[i]) = *reinterpret_cast<const float4*>(src);
+                    else *reinterpret_cast<float2*>(o[i]) = *reinterpret_cast<const float2*>(src);
+                }
+            }
+        };
+        load(s0);
+        float mm = fmaxf(l0, l1);
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+        // a split without keys weighs nothing; a NaN stays one
+        const float w0 = l0 == -INFINITY ? 0.f : __expf(l0 - mm), w1 = l1 == -INFINITY ? 0.f : __expf(l1 - mm);
+        float sum = w0 + w1;
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        for (int first = s0;;) {
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i) {
+                const int s = first + i * step;
+                const float ws = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
+                if (s < n) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(ws, o[i][e], acc[e]);
+                }
+            }
+            first += kTogether * step;
+            if (first >= n) break;
+            load(first);
         }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const long long row = (long long)b * a.num_q_heads + h;
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * D + lane * (D / 32));
+        if (!alone) {
+            if (r > 0) __syncthreads();  // the row before is written
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i)
-        out[i] = (uint32_t)to_bf16(acc[2 * i] * inv) | ((uint32_t)to_bf16(acc[2 * i + 1] * inv) << 16);
-    if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : mm + __logf(sum);
+            for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+            __syncthreads();
+            if (warp != 0) continue;
+#pragma unroll
+            for (int w = 1; w < kMergeWarps; ++w)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += part[w][lane * E + e];
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const long long row = row0 + r;
+        uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * D + lane * E);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            out[i] = (uint32_t)to_bf16(acc[2 * i] * inv) | ((uint32_t)to_bf16(acc[2 * i + 1] * inv) << 16);
+        if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : mm + __logf(sum);
+    }
 }
 
 template <int D, int NH>
@@ -704,9 +747,15 @@ cudaError_t launch_decode_fp4(int head_dim, const DecodeArgs& a, int grid, cudaS
 }
 
 cudaError_t launch_combine_fp4(int head_dim, const DecodeArgs& a, cudaStream_t stream) {
-    const dim3 grid((unsigned)(((int64_t)a.batch * a.num_q_heads + 3) / 4));
-    return head_dim == 128 ? launch_overlapped(combine_fp4_kernel<128>, grid, dim3(128), 0, stream, a)
-                           : launch_overlapped(combine_fp4_kernel<64>, grid, dim3(128), 0, stream, a);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int64_t all = (int64_t)a.batch * a.num_q_heads;
+    const int rows = all <= 8 * (int64_t)sms ? 1 : kMergeWarps;
+    const dim3 grid((unsigned)((all + rows - 1) / rows)), block(kMergeWarps * 32);
+    return head_dim == 128 ? launch_overlapped(combine_fp4_kernel<128>, grid, block, 0, stream, a, rows)
+                           : launch_overlapped(combine_fp4_kernel<64>, grid, block, 0, stream, a, rows);
 }
 
 }  // namespace pa

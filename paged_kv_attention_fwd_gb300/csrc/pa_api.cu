@@ -486,6 +486,19 @@ pa_status pa_decode_combine(const pa_decode_shapes* sh, const pa_decode_plan* pl
     pa_status st = validate_decode_common(sh, plan, out, meta_dev, workspace, workspace_bytes);
     if (st != PA_OK || sh->batch == 0) return st;
     if (plan->total_splits == sh->batch) return PA_OK;
+    if (sh->kv_dtype == PA_KV_FP4_E2M1) {  // the merge that pa_decode launches, and so its bits
+        pa::DecodeArgs d = {};
+        d.meta = meta_dev;
+        d.o_part = partial_o(workspace);
+        d.lse_part = d.o_part + (size_t)plan->total_splits * sh->num_q_heads * sh->head_dim;
+        d.out = static_cast<uint16_t*>(out);
+        d.lse = lse;
+        d.batch = sh->batch;
+        d.num_q_heads = sh->num_q_heads;
+        cudaError_t e = pa::launch_combine_fp4(sh->head_dim, d, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "combine launch");
+        return PA_OK;
+    }
     pa::CombineArgs c;
     c.meta = meta_dev;
     c.o_part = partial_o(workspace);

@@ -339,6 +339,18 @@ def test_decode_nan_reaches_its_rows_only():
     assert torch.equal(out.isnan().all(-1), bad) and torch.equal(lse.isnan(), bad)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,hk,group,forced", [([4090, 70], 1, 8, 64), ([2000], 2, 3, 31),
+                                                  ([4090, 300, 0, 64, 700, 513] + [50] * 120, 1, 15, 40)])
+def test_merge_of_few_and_of_many_splits(d, lens, hk, group, forced):
+    """Rows of up to 64 splits, alone or beside others: shared by the warps of a CTA, or a warp's own."""
+    c = Cache(lens, hk, d, seed=95)
+    q, scale, out, lse, p = decode(c, hk * group, forced_splits=forced)
+    splits = [max(1, min(forced, 64, -(-n // 64))) if n > 64 else 1 for n in lens]
+    assert p.plan.total_splits == sum(splits)
+    check(c, q, scale, out, lse)
+
+
 def test_attend_then_combine_and_noalloc():
     c = Cache([3000, 100, 0, 900], 2, 128, seed=94)
     q, scale, out, lse, p = decode(c, 8)
