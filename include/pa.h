@@ -114,7 +114,8 @@ typedef struct {
  * Split rule (integers only, deterministic):
  *   pages_b = ceil(len_b / 64); units = sum_b pages_b * Hk;
  *   cap = num_sms * ctas_per_sm; chunk = max(4, ceil(units / (2 * cap)))
- *   (with 4-bit pages ceil(units / cap));
+ *   (with 4-bit pages ceil(units / cap), or the first of the 12 next values that
+ *   makes at most cap work items where that one makes more);
  *   n_b = 1 if pages_b <= 1, else min(forced, pages_b, 64) if forced > 0,
  *   else min(ceil(pages_b / chunk), 64).  Split s of b covers pages
  *   [floor(s * pages_b / n_b), floor((s + 1) * pages_b / n_b)).

@@ -72,7 +72,7 @@ __device__ void block_exclusive_scan(const int* in, int* out, int n, int* tmp) {
 template <int T>
 __global__ void __launch_bounds__(T, 1)
     schedule_kernel(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int per_share,
-                    int forced, int p2cap, int32_t* meta) {
+                    int slack, int forced, int p2cap, int32_t* meta) {
     constexpr int kPer = T == kMaxThreads ? kMaxPer : 4;
     allow_dependents_launch();  // the decode kernel's prologue overlaps this one
     extern __shared__ unsigned long long dyn[];
@@ -92,7 +92,16 @@ __global__ void __launch_bounds__(T, 1)
     }
     const long long units = block_sum(local, tmp64) * Hk;
     const long long shares = (long long)per_share * cap;  // items per CTA share: two, or one (4-bit pages)
-    const long long chunk = max(4LL, (units + shares - 1) / shares);
+    long long chunk = max(4LL, (units + shares - 1) / shares);
+    // where a chunk of up to `slack` pages more leaves no CTA with two items, the smallest such
+    for (long long c = chunk; slack > 0 && c <= chunk + slack; ++c) {
+        long long n = 0;
+        for (int b = threadIdx.x; b < B; b += T) n += pages[b] <= 1 ? 1 : min((long long)PA_MAX_SPLITS, (pages[b] + c - 1) / c);
+        if (block_sum(n, tmp64) * Hk <= cap) {
+            chunk = c;
+            break;
+        }
+    }
     for (int b = threadIdx.x; b < B; b += T) {
         const int p = pages[b];
         int n;
@@ -292,11 +301,11 @@ size_t schedule_smem_bytes(int B, int p2cap) { return (size_t)p2cap * 8 + (size_
 
 cudaError_t launch_schedule(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int forced,
                             int p2cap, int32_t* meta, cudaStream_t stream) {
-    return launch_schedule_shares(seq_lens, B, Hk, max_pages, cps, cap, 2, forced, p2cap, meta, stream);
+    return launch_schedule_shares(seq_lens, B, Hk, max_pages, cps, cap, 2, 0, forced, p2cap, meta, stream);
 }
 
 cudaError_t launch_schedule_shares(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap,
-                                   int per_share, int forced, int p2cap, int32_t* meta, cudaStream_t stream) {
+                                   int per_share, int slack, int forced, int p2cap, int32_t* meta, cudaStream_t stream) {
     const size_t smem = schedule_smem_bytes(B, p2cap);
     // a power of two with one sort key and at most 4 sequences a thread, up to
     // 1024 threads (then at most kMaxPer = 16 keys, p2cap <= 16384); the e4m3
@@ -310,7 +319,7 @@ cudaError_t launch_schedule_shares(const int32_t* seq_lens, int B, int Hk, int m
     auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
         cudaError_t e = ensure_dynamic_smem(kernel, (int)schedule_smem_bytes(kMaxBatch, 16384), done);
         if (e != cudaSuccess) return e;
-        kernel<<<1, threads, smem, stream>>>(seq_lens, B, Hk, max_pages, cps, cap, per_share, forced, p2cap, meta);
+        kernel<<<1, threads, smem, stream>>>(seq_lens, B, Hk, max_pages, cps, cap, per_share, slack, forced, p2cap, meta);
         return cudaGetLastError();
     };
     switch (threads) {

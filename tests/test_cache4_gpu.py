@@ -6,6 +6,7 @@ import torch
 
 import oracle
 from oracle import fp4 as F
+from oracle import scheduler as S
 from paged_kv_attention_fwd_gb300 import binding as B
 from paged_kv_attention_fwd_gb300 import ops
 from paged_kv_attention_fwd_gb300 import workloads as W
@@ -407,6 +408,26 @@ def test_decode_many_items_per_cta():
     c.poison()
     q, scale, out, lse, _ = decode(c, 4, sms=2, ctas_per_sm=3)
     check(c, q, scale, out, lse)
+
+
+@pytest.mark.parametrize("batch,longest,hk,sms", [(4, 32768, 8, 152), (20, 6000, 8, 152), (64, 4096, 1, 152),
+                                                  (300, 500, 2, 152), (7, 900, 3, 5), (1, 70, 1, 1)])
+def test_device_plan_is_the_host_plan(batch, longest, hk, sms):
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        lens = rng.integers(0, longest + 1, size=batch).astype(np.int32)
+        if seed == 3:
+            lens[:] = longest
+        sh = B.pa_decode_shapes(batch=batch, num_q_heads=hk, num_kv_heads=hk, head_dim=128, page_size=64,
+                                max_pages_per_seq=-(-longest // 64), num_pool_pages=1, kv_dtype=B.PA_KV_FP4_E2M1,
+                                num_sms=sms, ctas_per_sm=0, forced_splits=0)
+        host, _ = B.pa_get_metadata(lens, None, sh)
+        plan = B.pa_get_static_plan(sh)
+        meta = torch.zeros(plan.meta_ints, dtype=torch.int32, device=DEV)
+        B.pa_get_metadata_device(sh, plan, dev(lens), meta)
+        one, two = S.unpack(host.tolist()), S.unpack(meta.cpu().tolist())
+        assert one["n_splits"] == two["n_splits"] and one["grid"] == two["grid"]
+        assert sorted(one["items"]) == sorted(two["items"][:len(one["items"])])
 
 
 def test_captured_step_follows_new_lengths():

@@ -25,9 +25,12 @@ def test_slab_bytes():
 
 
 def plain_plan(lens, hk, cap, forced):
-    """(splits per sequence, items of each CTA) of the 4-bit rule: one item per CTA share."""
+    """(splits per sequence, items of each CTA) of the 4-bit rule: one item per CTA share, and chunks up to 12 pages
+    longer where that leaves no CTA with two."""
     pages = [-(-n // 64) for n in lens]
     chunk = max(4, -(-sum(pages) * hk // cap))
+    one_each = [c for c in range(chunk, chunk + 13) if sum(max(1, min(64, -(-p // c))) for p in pages) * hk <= cap]
+    chunk = one_each[0] if one_each else chunk
     n = [1 if p <= 1 else min(forced, p, 64) if forced else min(-(-p // chunk), 64) for p in pages]
     items = [((s + 1) * p // k - s * p // k + 1, b, s, g) for b, (p, k) in enumerate(zip(pages, n)) for s in range(k)
              for g in range(hk)]
@@ -41,7 +44,8 @@ def plain_plan(lens, hk, cap, forced):
 
 
 @pytest.mark.parametrize("lens,hq,forced", [([10, 3000, 0, 777], 32, 0), ([5000], 32, 0), ([4096] * 9, 128, 0),
-                                            (list(range(0, 4000, 130)), 32, 0), ([640, 1000], 64, 5)])
+                                            (list(range(0, 4000, 130)), 32, 0), ([640, 1000], 64, 5),
+                                            ([2500], 32, 0), ([900, 1000], 32, 0), ([5120, 64], 128, 0)])
 def test_plan_of_4_bit_pages(lens, hq, forced):
     for cps, want in ((0, 2 if hq > 64 else 3), (1, 1), (5, 5)):
         sh = shapes(len(lens), hq=hq, max_pages=80, sms=7, cps=cps, forced=forced, kv=B.PA_KV_FP4_E2M1)
