@@ -93,14 +93,22 @@ __global__ void __launch_bounds__(T, 1)
     const long long units = block_sum(local, tmp64) * Hk;
     const long long shares = (long long)per_share * cap;  // items per CTA share: two, or one (4-bit pages)
     long long chunk = max(4LL, (units + shares - 1) / shares);
-    // where a chunk of up to `slack` pages more leaves no CTA with two items, the smallest such
-    for (long long c = chunk; slack > 0 && c <= chunk + slack; ++c) {
+    // Where a chunk of up to `slack` pages more leaves no CTA with two items, the
+    // smallest such: longer chunks never make more items.
+    auto one_each = [&](int c) {
         long long n = 0;
-        for (int b = threadIdx.x; b < B; b += T) n += pages[b] <= 1 ? 1 : min((long long)PA_MAX_SPLITS, (pages[b] + c - 1) / c);
-        if (block_sum(n, tmp64) * Hk <= cap) {
-            chunk = c;
-            break;
+        for (int b = threadIdx.x; b < B; b += T) n += pages[b] <= 1 ? 1 : min(PA_MAX_SPLITS, (pages[b] + c - 1) / c);
+        return block_sum(n, tmp64) * Hk <= cap;
+    };
+    if (slack > 0 && (long long)B * Hk <= cap && chunk <= max_pages && !one_each((int)chunk) &&
+        one_each((int)chunk + slack)) {
+        int lo = (int)chunk, hi = (int)chunk + slack;  // too short, long enough
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (one_each(mid)) hi = mid;
+            else lo = mid;
         }
+        chunk = hi;
     }
     for (int b = threadIdx.x; b < B; b += T) {
         const int p = pages[b];
