@@ -33,10 +33,10 @@
 // Measured: 57 sequences of 8192 keys, 8 KV heads, D = 128 (539 MB), 83 us a
 // call with 4 query heads per KV head (6.5 TB/s, the memory's rate), 88 with 8
 // (issue slots: 250 instructions per 16 keys, 12 warps an SM), 145 with 16
-// (twice the MMAs, 8 warps an SM).  Shorter batches also see an item's ends
-// (about 2.5 us), 3 us until the first pages are asked for, and 2 to 3 us of
-// the merge kernel: 64 sequences of up to 4096 keys 37 us a call, where the
-// bytes alone take 23.
+// (twice the MMAs, 8 warps an SM; 158 as it is planned, 456 whole sequences for
+// 304 CTAs).  Shorter batches also see an item's ends (about 2.5 us), 3 us until
+// the first pages are asked for, and 2 to 3 us of the merge kernel: 64 sequences
+// of up to 4096 keys 37 us a call, where the bytes alone take 23.
 //
 // code * scale is exact in fp16, so nothing is lost before the fp32
 // accumulators; P is rounded to fp16 (relative 2^-12) and q, scaled by a
