@@ -62,9 +62,12 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kItems = 64;  // items of a CTA decoded once, in the prologue
 constexpr float kLn2 = 0.69314718055994531f;
 // The running maximum is only raised when a logit (in bits) exceeds it by more
-// than this: P then reaches 2^8 in fp16, and most steps rescale nothing.
+// than this: P then reaches 2^8 in fp16, and most steps rescale nothing.  It is
+// kept as a product q k, not as a logit: the difference of two products is exact
+// where it matters, however large the logits are, and so P never passes 2^8.
 constexpr float kSlack = 8.f;
 constexpr float kNone = -3e38f;  // the running maximum before any key: finite, so that its differences are
+constexpr float kLeastScale = 1e-37f;  // of a logit in bits to its product: kNone still lies below every logit
 
 // D: head dim; NH: query heads of a KV group the kernel has room for (4, 8 or 16)
 template <int D, int NH>
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[kWarps][S];
     __shared__ Item items_sh[kItems];
-    __shared__ float red_m[kWarps][NH], red_l[kWarps][NH];
+    __shared__ float red_m[kWarps][NH], red_l[kWarps][NH], red_scale[NH];  // the last one every warp's
     __shared__ int scratch_at[kWarps];  // the page buffer that holds each warp's output
     __shared__ int abort_store;
     volatile int* abort_sh = &abort_store;
@@ -335,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
         }
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
+            if (sl2[i] < kLeastScale) sl2[i] = kLeastScale;
             m[i] = kNone;
             l[i] = 0.f;
         }
@@ -414,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                     top[i] = x[i][0];
 #pragma unroll
                     for (int k = 1; k < 2 * KB; ++k) top[i] = fmaxf(top[i], x[i][k]);
-                    top[i] *= sl2[i];
-                    raise |= top[i] > m[i] + kSlack;
+                    raise |= (top[i] - m[i]) * sl2[i] > kSlack;
                 }
                 if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
                         const float mn = fmaxf(m[i], v);
-                        const float alpha = ex2(m[i] - mn);
+                        const float alpha = ex2((m[i] - mn) * sl2[i]);
                         m[i] = mn;
                         l[i] *= alpha;
 #pragma unroll
@@ -437,17 +440,20 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                                     if (NH == 4 || (n == i >> 1 && (e & 1) == (i & 1))) o[n][k][e] *= alpha;
                     }
                 }
+                if constexpr (HL == 1) {
 #pragma unroll
-                for (int i = 0; i < HL; ++i)
+                    for (int k = 0; k < 2 * KB; ++k) x[0][k] = ex2((x[0][k] - m[0]) * sl2[0]);
+                } else {  // two heads at a time, as the products lie
 #pragma unroll
-                    for (int k = 0; k < 2 * KB; ++k) x[i][k] = ex2(fmaf(x[i][k], sl2[i], -m[i]));
-                if (tail) {  // whatever -inf times a scale of 0 came to
+                    for (int i = 0; i < HL; i += 2) {
+                        const F2 from = f2(-m[i], -m[i + 1]), by = f2(sl2[i], sl2[i + 1]);
 #pragma unroll
-                    for (int k = 0; k < 2 * KB; ++k)
-                        if (8 * k + krow >= live) {
-#pragma unroll
-                            for (int i = 0; i < HL; ++i) x[i][k] = 0.f;
+                        for (int k = 0; k < 2 * KB; ++k) {
+                            const float2 e = split((f2(x[i][k], x[i + 1][k]) + from) * by);
+                            x[i][k] = ex2(e.x);
+                            x[i + 1][k] = ex2(e.y);
                         }
+                    }
                 }
                 // ---- O^T += V^T P^T
 #pragma unroll
@@ -545,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
             if (g == 0) {
                 red_m[warp][h] = m[i];
                 red_l[warp][h] = l[i];
+                red_scale[h] = sl2[i];
             }
             if (owed && h < G) {
 #pragma unroll
@@ -577,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
             const int h = idx / (D / 4), d = idx % (D / 4) * 4;
             const int ht = NH == 4 ? h : (h >> 1) & 3;  // the t of the lanes that held head h
             const int slot = h * D + d / (D / 8) * (D / 8) + 4 * ((d % (D / 8) / 4 + ht) & (M4 - 1));
+            const float bits_of = red_scale[h];
             float mw[kWarps], lw[kWarps], mm = kNone, ll = 0.f;
             float4 v[kWarps], val = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -589,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const bool any = lw[w] != 0.f;                // else no live key, and the buffer holds anything;
-                const float f = any ? ex2(mw[w] - mm) : 0.f;  // a NaN logit leaves a NaN sum, and so a NaN output
+                const float f = any ? ex2((mw[w] - mm) * bits_of) : 0.f;  // a NaN logit leaves a NaN sum, and so a NaN output
                 ll = fmaf(f, lw[w], ll);
                 val.x = fmaf(f, any ? v[w].x : 0.f, val.x);
                 val.y = fmaf(f, any ? v[w].y : 0.f, val.y);
@@ -606,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                                (uint32_t)to_bf16(val.z) | ((uint32_t)to_bf16(val.w) << 16));
             }
             if (d == 0) {
-                const float lse = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+                const float lse = ll == 0.f ? -INFINITY : fmaf(mm, bits_of, log2f(ll)) * kLn2;
                 if (partial) a.lse_part[orow + h] = lse;
                 else if (a.lse) a.lse[orow + h] = lse;
             }

@@ -551,3 +551,30 @@ def test_chunk_through_the_cache_and_a_prefill():
                            for b, n in enumerate(prefix + new)])
     got = kr.float().cpu().numpy()
     assert (np.abs(got - rows) <= 2.0 ** -8 * np.abs(rows)).all()  # one bf16 rounding
+
+
+@pytest.mark.parametrize("hq", [4, 8, 16])
+@pytest.mark.parametrize("top", [1e3, 1e6, 1.3e7, 3e7, 6e7, 1e9, 1e12])
+def test_decode_of_huge_logits_stays_finite(hq, top):
+    """Logits whose fp32 steps are up to whole bits, the later pages' a few steps above the first ones': no weight
+    overflows on the way, whichever way the steps round."""
+    d, n = 128, 320
+    j = [(a, b) for a in range(8) for b in (0, 2)]  # codes: step a's value, and 8 times b's
+    c = Cache([n] * len(j), 1, d, seed=104)
+    c.ks = c.vs = one = np.ones(1, np.float32)
+    c.k, c.v = (F.make_pool(np.full((c.pages, 1, 64, d), 6, np.float32), one) for _ in range(2))
+    codes, _ = F.rows_of_slab(c.k, d)  # scales are 1 throughout
+    codes[:, 0, :, :8] = 0
+    for i, (a, b) in enumerate(j):  # a warp's first page holds the first block's zeros, its second one the codes
+        codes[c.table[i, 4], 0, :, 0] = a + 16 * b
+    x = np.ones((len(j), hq, d), np.float32)
+    x[..., 0], x[..., 1] = 2.0 ** -14, 2.0 ** -11  # 2^-14: an fp32 step of 672, the other blocks' product
+    q = ops.as_bf16(W.f32_to_bf16_bits(x), DEV)
+    p = ops.plan_decode(c.lens, None, hq, 1, d, c.table.shape[1], c.pages, kv_dtype="fp4", forced_splits=1)
+    k, v, ks, vs, table, lens = c.up()
+    for at in range(24):
+        out, lse = ops.decode(p, q, k, v, table, lens, top * (1 + at / 37) / 672, ks, vs)
+        assert B.pa_check_status(p.workspace) == B.PA_OK
+        # every value is 6, so is every mean of them, but for P's fp16 (2^-11) and the output's bf16 rounding (2^-8),
+        # and a few fp32 ones
+        assert (out.float() - 6).abs().max() <= 6 * (2.0 ** -8 + 2.0 ** -10) and torch.isfinite(lse).all()
