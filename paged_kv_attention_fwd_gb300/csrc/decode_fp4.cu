@@ -39,7 +39,8 @@
 // of up to 4096 keys 37 us a call, where the bytes alone take 23.
 //
 // code * scale is exact in fp16, so nothing is lost before the fp32
-// accumulators; P is rounded to fp16 (relative 2^-12) and q, scaled by a
+// accumulators; P is rounded to fp16 -- relative 2^-11, and 2^-32 of the
+// largest weight where that leaves fp16's normal range -- and q, scaled by a
 // power of two per head, is exact but for elements 2^14 below its largest.
 //
 // Each warp streams its own pages (every fourth of the item's) through its
@@ -62,10 +63,14 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kItems = 64;  // items of a CTA decoded once, in the prologue
 constexpr float kLn2 = 0.69314718055994531f;
 // The running maximum is only raised when a logit (in bits) exceeds it by more
-// than this: P then reaches 2^8 in fp16, and most steps rescale nothing.  It is
-// kept as a product q k, not as a logit: the difference of two products is exact
-// where it matters, however large the logits are, and so P never passes 2^8.
+// than this, and most steps rescale nothing.  It is kept as a product q k, not as
+// a logit: the difference of two products is exact where it matters, however large
+// the logits are, and so P never passes 2^(kShift + kSlack) = 2^15.
 constexpr float kSlack = 8.f;
+// P and its sum are 2^kShift times the weights beside the running maximum, which
+// fp16 has room for: of thousands of keys far below one, none is lost that is more
+// than 2^-32 of it (2^-25 with no shift).
+constexpr float kShift = 7.f;
 constexpr float kNone = -3e38f;  // the running maximum before any key: finite, so that its differences are
 constexpr float kLeastScale = 1e-37f;  // of a logit in bits to its product: kNone still lies below every logit
 
@@ -442,14 +447,14 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                 }
                 if constexpr (HL == 1) {
 #pragma unroll
-                    for (int k = 0; k < 2 * KB; ++k) x[0][k] = ex2((x[0][k] - m[0]) * sl2[0]);
+                    for (int k = 0; k < 2 * KB; ++k) x[0][k] = ex2(fmaf(x[0][k] - m[0], sl2[0], kShift));
                 } else {  // two heads at a time, as the products lie
 #pragma unroll
                     for (int i = 0; i < HL; i += 2) {
-                        const F2 from = f2(-m[i], -m[i + 1]), by = f2(sl2[i], sl2[i + 1]);
+                        const F2 from = f2(-m[i], -m[i + 1]), by = f2(sl2[i], sl2[i + 1]), shift = f2(kShift, kShift);
 #pragma unroll
                         for (int k = 0; k < 2 * KB; ++k) {
-                            const float2 e = split((f2(x[i][k], x[i + 1][k]) + from) * by);
+                            const float2 e = split(fma2(f2(x[i][k], x[i + 1][k]) + from, by, shift));
                             x[i][k] = ex2(e.x);
                             x[i + 1][k] = ex2(e.y);
                         }
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NH>::kCtas) decode_fp4_ker
                                (uint32_t)to_bf16(val.z) | ((uint32_t)to_bf16(val.w) << 16));
             }
             if (d == 0) {
-                const float lse = ll == 0.f ? -INFINITY : fmaf(mm, bits_of, log2f(ll)) * kLn2;
+                const float lse = ll == 0.f ? -INFINITY : fmaf(mm, bits_of, log2f(ll) - kShift) * kLn2;
                 if (partial) a.lse_part[orow + h] = lse;
                 else if (a.lse) a.lse[orow + h] = lse;
             }

@@ -578,3 +578,35 @@ def test_decode_of_huge_logits_stays_finite(hq, top):
         # every value is 6, so is every mean of them, but for P's fp16 (2^-11) and the output's bf16 rounding (2^-8),
         # and a few fp32 ones
         assert (out.float() - 6).abs().max() <= 6 * (2.0 ** -8 + 2.0 ** -10) and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("group", [1, 4, 8, 16])
+@pytest.mark.parametrize("bits", [20.0, 24.3, 27.7, 30.4])
+def test_decode_of_many_keys_far_below_a_dominant_one(group, bits):
+    """One key whose value row is zero, thousands of keys 2^-bits below it: what they weigh is the whole output, beside
+    a sum that the dominant key makes."""
+    d, n = 128, 4096
+    c = Cache([n], 1, d, seed=103)
+    c.ks = c.vs = one = np.ones(1, np.float32)
+    # keys are 0 but for two blocks of key 0; values are 6 but for key 0's, which are 0
+    x = np.zeros((c.pages, 1, 64, d), np.float32)
+    x[c.table[0, 0], 0, 0, :32] = 6
+    y = np.full((c.pages, 1, 64, d), 6, np.float32)
+    y[c.table[0, 0], 0, 0] = 0
+    c.k, c.v = F.make_pool(x, one), F.make_pool(y, one)
+    kv, vv = c.values()
+    assert np.array_equal(kv, x) and np.array_equal(vv, y)
+    q = W.f32_to_bf16_bits(np.ones((1, group, d), np.float32))
+    scale = float(np.float32(bits * np.log(2.0) / 192))  # the dominant logit: 192 scale, that is `bits` bits
+    p = ops.plan_decode(c.lens, None, group, 1, d, c.table.shape[1], c.pages, kv_dtype="fp4", forced_splits=1)
+    k, v, ks, vs, table, lens = c.up()
+    out, lse = ops.decode(p, ops.as_bf16(q, DEV), k, v, table, lens, scale, ks, vs)
+    assert B.pa_check_status(p.workspace) == B.PA_OK
+    ro, rl, *_ = F.attend(q, kv, vv, c.table, c.lens, scale)
+    # A weight lies within 2^-11 of itself, or 2^-32 of the largest where fp16 has no normal number for it: half a step
+    # 2^-25 beside a largest weight of 2^7.  The logits' fp32 steps, at up to 31 bits, and the exponential's come to
+    # less than 2^-17 relative.  The output is about 6 (n - 1) 2^-bits, and its bf16 rounding 2^-8 of it.
+    tol = ro * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -17) + 6 * n * 2.0 ** -32
+    err = np.abs(out.double().cpu().numpy() - ro)
+    assert (ro > 0).all() and (err <= tol).all(), float((err / ro).max())
+    assert (np.abs(lse.cpu().numpy() - rl) <= 2.0 ** -19 * (1 + np.abs(rl))).all()
