@@ -586,12 +586,16 @@ pa_status pa_qk_norm_rope(const pa_rope_shapes* shapes, const void* q, const voi
  *                    pa_append_kv; tokens, KV heads and head_dim of the two shapes
  *                    agree; fp16 tokens go to fp16 pools, bf16 tokens to the others
  *   v                [T, Hk, D], token stride v_stride
- *   positions        as above, or NULL: every axis at the token's cache position
+ *   positions        as above (a negative entry of axis 0 marks a padding token
+ *                    wherever in the cache it would lie: start_pos and block_table
+ *                    of idle sequences may hold anything), or NULL: every axis at
+ *                    the token's cache position
  *                    (with rope_dim 0 not read: padding is then what lies past
  *                    cu_seqlens_new[B] only)
- * T may exceed cu_seqlens_new[B]: the tokens past it are padding; nothing of
- * them is written, whatever they hold.  A token whose position, page or page id is out
- * of range is skipped (queries too) and recorded as PA_ERR_DEVICE_BOUNDS.
+ * T may exceed cu_seqlens_new[B]: the tokens past it are padding.  Nothing of a
+ * padding token is written, whatever it holds.  Any other token whose position, page
+ * or page id is out of range is skipped (queries too) and recorded as
+ * PA_ERR_DEVICE_BOUNDS.
  */
 pa_status pa_norm_rope_append_kv(const pa_rope_shapes* rope_shapes, const pa_append_shapes* append_shapes,
                                  const void* q, const void* k, const void* v, const void* q_weight,

@@ -290,9 +290,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) norm_rope_kernel(const __g
                 }
             }
         }
-        // a padding token, or one that is out of range: nothing is written
-        const bool padding = my_tok > last_token || where.place == Place::kPadding ||
-                             (where.place == Place::kOk && a.rope_dim > 0 && pos.at[0] < 0);
+        // a padding token (a negative given position makes it one wherever it lies), or one that is out of range:
+        // nothing is written
+        const bool padding = my_tok > last_token || where.place == Place::kPadding || (a.rope_dim > 0 && pos.at[0] < 0);
         const bool skip = padding || where.place != Place::kOk || !in_table;
         if (skip && !padding && l == 0) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
         const int page = where.page, prow = where.row;

@@ -376,3 +376,29 @@ def test_whole_decode_steps(kv):
         start += 1
         lens += 1
     assert B.pa_check_status(ws) == B.PA_OK and B.pa_check_status(rws) == B.PA_OK
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "fp4"])
+@pytest.mark.parametrize("axes", [1, 2])
+def test_append_padding_by_position_wherever_the_token_lies(kv, axes):
+    """Idle slots of a fixed batch: a token with a negative axis-0 position
+    inside its sequence's range is padding, whatever its place in the cache
+    is -- valid, an unset page id, or past the block table."""
+    d, hq, hk, pages = 64, 5, 2, 4
+    start = np.array([7, 70, 5, 500, 130], np.int32)   # the third's page id is unset, the fourth lies past the table
+    bt = np.array([[0, -1], [1, 2], [-1, 2 ** 31 - 1], [3, 3], [-1, -1]], np.int32)
+    q, k, v, w, pos, sections, table = make(5, hq, hk, d, "bf16", axes=axes, seed=13)
+    idle = [1, 2, 3, 4]
+    pos[0, idle] = torch.tensor([-1, -1, -5, -2 ** 31], dtype=torch.int32, device=DEV)
+    scales = [None, None] if kv == "bf16" else [torch.full((hk,), s, device=DEV) for s in (0.011, 0.017)]
+    kp, vp = (ops.kv_pool(pages, hk, d, kv, DEV) for _ in range(2))
+    qo = torch.full((5, hq, d), 7.0, dtype=q.dtype, device=DEV)
+    sh = ops.rope_shapes(q, k, v, rope_dim=d, max_position=4096, sections=sections)
+    _, ws = ops.norm_rope_append_kv(sh, ops.append_shapes(5, hk, d, 2, pages, 5, kv), q, k, v,
+                                    dev(np.arange(6, dtype=np.int32)), dev(start), dev(bt), kp, vp, w[0], w[1], pos, table,
+                                    *scales, q_out=qo)
+    assert B.pa_check_status(ws) == B.PA_OK
+    assert (qo[idle] == 7).all() and (qo[0] != 7).any()
+    assert not kp[1:].view(torch.uint8).any() and not vp[1:].view(torch.uint8).any()
+    assert kp[0].view(torch.uint8).any() and vp[0].view(torch.uint8).any()
+    compare(qo[:1], q[:1], w[0], pos[:, :1], table, d, False, sections, 1e-6, True, "bf16")
