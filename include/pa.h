@@ -459,7 +459,7 @@ typedef struct {
     int32_t page_size;         /* must be 64 */
     int32_t max_pages_per_seq; /* block_table row stride */
     int32_t num_pool_pages;
-    int32_t total_new;         /* cu_seqlens_new[B] */
+    int32_t total_new;         /* tokens of k_new and v_new, padding included: at least cu_seqlens_new[B] */
     int32_t kv_dtype;          /* pa_kv_dtype of the pools */
 } pa_append_shapes;
 
@@ -486,8 +486,8 @@ typedef struct {
  *                   (codes 0 where bs is 0).  A NaN makes its block's scale NaN,
  *                   an infinity saturates.
  *   workspace       >= PA_STATUS_BYTES (status word)
- * With 4-bit pools total_new may exceed cu_seqlens_new[B]: the tokens past it
- * are padding; nothing of them is written, whatever they hold.
+ * total_new may exceed cu_seqlens_new[B]: the tokens past it (and any before
+ * cu_seqlens_new[0]) are padding; nothing of them is written, whatever they hold.
  * A position outside the block table or a page id outside the pool is skipped
  * and recorded as PA_ERR_DEVICE_BOUNDS.  Rows of different calls or tokens
  * must not collide (two writers to one row race).
@@ -517,7 +517,8 @@ size_t pa_page_slab_bytes(int32_t head_dim, int32_t kv_dtype);
  *                   bf16(x * scale), a 4-bit one as bf16(code * (bs * scale)),
  *                   the products in fp32
  *   workspace       >= PA_STATUS_BYTES (status word)
- * total_new may exceed cu_seqlens[B]: rows past it are left as they were.  A
+ * total_new may exceed cu_seqlens[B]: rows past it (and any before
+ * cu_seqlens[0]) are left as they were.  A
  * position outside the block table or a page id outside the pool is skipped
  * (its row left as it was) and recorded as PA_ERR_DEVICE_BOUNDS.
  */

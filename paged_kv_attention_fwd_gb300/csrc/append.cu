@@ -28,6 +28,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
     if (tok >= a.total_new) return;
     const int h0 = (int)blockIdx.y * kHeadsPerWarp;
     const int nh = min(kHeadsPerWarp, hk - h0);
+    const int first = __ldg(&a.cu_new[0]), end = __ldg(&a.cu_new[a.batch]);  // on their way during the search
     // segment holding this token: last b with cu[b] <= tok
     int lo = 0, hi = a.batch - 1;
     while (lo < hi) {
@@ -35,6 +36,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         if (__ldg(&a.cu_new[mid]) <= tok) lo = mid;
         else hi = mid - 1;
     }
+    if (tok < first || tok >= end) return;  // padding
     const int b = lo;
     const long long pos = (long long)__ldg(&a.start_pos[b]) + (tok - __ldg(&a.cu_new[b]));
     if (pos < 0 || pos / kPage >= a.max_pages) {

@@ -402,3 +402,32 @@ def test_append_padding_by_position_wherever_the_token_lies(kv, axes):
     assert not kp[1:].view(torch.uint8).any() and not vp[1:].view(torch.uint8).any()
     assert kp[0].view(torch.uint8).any() and vp[0].view(torch.uint8).any()
     compare(qo[:1], q[:1], w[0], pos[:, :1], table, d, False, sections, 1e-6, True, "bf16")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3", "fp4"])
+def test_append_padding_is_the_two_calls(kv):
+    """Tokens behind the last sequence (and before the first) are padding in every form of the append and for every
+    page type: nothing of them is written."""
+    dtype = "f16" if kv == "f16" else "bf16"
+    prior, new = np.array([10, 100, 3], np.int32), np.array([3, 40, 0], np.int32)
+    d, hq, hk, lead, pad = 64, 3, 2, 2, 25
+    t = lead + int(new.sum()) + pad
+    q, k, v, w, pos, _, table = make(t, hq, hk, d, dtype, seed=14)
+    bt, pages = W.assign_pages(prior + new + 64, 4, 1)   # room for the padding behind the last sequence
+    scales = [None, None] if kv in TORCH else [torch.full((hk,), s, device=DEV) for s in (0.011, 0.017)]
+    one, two, bare = ([ops.kv_pool(pages, hk, d, kv, DEV) for _ in range(2)] for _ in range(3))
+    cu, start, btd = dev(lead + W.cu_seqlens(new)), dev(prior), dev(bt)
+    ash = ops.append_shapes(3, hk, d, bt.shape[1], pages, t, kv)
+    sh = ops.rope_shapes(q, k, v, rope_dim=d, max_position=4096)
+    qo, ko, ws = ops.qk_norm_rope(sh, q, k, w[0], w[1], pos, table)
+    ops.append_kv(ash, ko, v.contiguous(), cu, start, btd, *one, *scales, workspace=ws)
+    q1 = torch.full_like(qo, 7.0)
+    ops.norm_rope_append_kv(sh, ash, q, k, v, cu, start, btd, *two, w[0], w[1], pos, table, *scales, q_out=q1, workspace=ws)
+    live = slice(lead, t - pad)
+    exact = ops.append_shapes(3, hk, d, bt.shape[1], pages, t - lead - pad, kv)
+    ops.append_kv(exact, ko[live].contiguous(), v[live].contiguous(), cu - lead, start, btd, *bare, *scales, workspace=ws)
+    assert B.pa_check_status(ws) == B.PA_OK
+    assert torch.equal(q1[live], qo[live]) and (q1[:lead] == 7).all() and (q1[t - pad:] == 7).all()
+    for a, b, c in zip(one, two, bare):
+        assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+        assert torch.equal(b.view(torch.uint8), c.view(torch.uint8)) and c.view(torch.uint8).any()
