@@ -670,9 +670,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) combine_fp4_kernel(const __g
         splits = __ldg(&a.meta[kMetaHeader + b]);
         base = (long long)__ldg(&a.meta[kMetaHeader + a.batch + b]) * a.num_q_heads + h;
     }
-    // The metadata was complete before the attention kernel let this one in;
-    // its partials are now.  Every warp waits, also one with nothing to do:
-    // this kernel must not be complete before that one.
+    // Let in by the attention kernel: the metadata was complete before that one
+    // did so, its partials are now.  Every warp waits, also one with nothing to
+    // do: this kernel must not be complete before that one.  (Launched plainly:
+    // everything before it was complete.)
     grid_dependency_wait();
     for (int r = 0; r < rows; ++r) {
         const int n = __shfl_sync(0xffffffffu, splits, r);
@@ -759,7 +760,7 @@ cudaError_t launch_decode_fp4(int head_dim, const DecodeArgs& a, int grid, cudaS
     return head_dim == 128 ? launch_heads<128>(a, grid, stream) : launch_heads<64>(a, grid, stream);
 }
 
-cudaError_t launch_combine_fp4(int head_dim, const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_combine_fp4(int head_dim, const DecodeArgs& a, bool behind_attention, cudaStream_t stream) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -767,8 +768,12 @@ cudaError_t launch_combine_fp4(int head_dim, const DecodeArgs& a, cudaStream_t s
     const int64_t all = (int64_t)a.batch * a.num_q_heads;
     const int rows = all <= 8 * (int64_t)sms ? 1 : kMergeWarps;
     const dim3 grid((unsigned)((all + rows - 1) / rows)), block(kMergeWarps * 32);
-    return head_dim == 128 ? launch_overlapped(combine_fp4_kernel<128>, grid, block, 0, stream, a, rows)
-                           : launch_overlapped(combine_fp4_kernel<64>, grid, block, 0, stream, a, rows);
+    if (behind_attention)
+        return head_dim == 128 ? launch_overlapped(combine_fp4_kernel<128>, grid, block, 0, stream, a, rows)
+                               : launch_overlapped(combine_fp4_kernel<64>, grid, block, 0, stream, a, rows);
+    if (head_dim == 128) combine_fp4_kernel<128><<<grid, block, 0, stream>>>(a, rows);
+    else combine_fp4_kernel<64><<<grid, block, 0, stream>>>(a, rows);
+    return cudaGetLastError();
 }
 
 }  // namespace pa

@@ -486,7 +486,7 @@ pa_status decode_launch(bool fused, const pa_decode_shapes* sh, const pa_decode_
     }
     cudaError_t e = fp4 ? pa::launch_decode_fp4(D, a, plan->grid, stream)
                         : pa::launch_decode(D, fp8, a, &mk, &mv, &mq, plan->grid, stream);
-    if (e == cudaSuccess && fp4 && fused && plan->total_splits > B) e = pa::launch_combine_fp4(D, a, stream);
+    if (e == cudaSuccess && fp4 && fused && plan->total_splits > B) e = pa::launch_combine_fp4(D, a, true, stream);
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
     if (!fp4 && fused && plan->total_splits > B && !a.counters) {
         // no room for the arrival counters: merge in a second kernel
@@ -511,7 +511,7 @@ pa_status pa_decode_combine(const pa_decode_shapes* sh, const pa_decode_plan* pl
         d.lse = lse;
         d.batch = sh->batch;
         d.num_q_heads = sh->num_q_heads;
-        cudaError_t e = pa::launch_combine_fp4(sh->head_dim, d, stream);
+        cudaError_t e = pa::launch_combine_fp4(sh->head_dim, d, false, stream);
         if (e != cudaSuccess) return cuda_fail(e, "combine launch");
         return PA_OK;
     }

@@ -8,7 +8,8 @@
 // allocation: the wait returns once the previous kernel has completed and its
 // memory operations are visible (at once when the launch has no such
 // predecessor), so stream order holds for every byte the kernel reads or
-// writes.  A kernel that calls allow_dependents_launch() lets such a
+// writes.  (One exception: the merge of 4-bit splits inside pa_decode reads the
+// metadata earlier, which the attention kernel before it has waited for.)  A kernel that calls allow_dependents_launch() lets such a
 // dependent be scheduled once every one of its CTAs has issued the call or
 // exited.  Under stream capture the launch becomes a programmatic edge of the
 // graph.

@@ -9,8 +9,11 @@ namespace pa {
 // 4-bit pages (decode_fp4.cu): CTAs that fit on one SM, by query heads per KV head
 __host__ __device__ constexpr int fp4_ctas_per_sm(int group) { return group > 8 ? 2 : 3; }
 cudaError_t launch_decode_fp4(int head_dim, const DecodeArgs& a, int grid, cudaStream_t stream);
-// merges the splits that launch_decode_fp4 left in a.o_part and a.lse_part
-cudaError_t launch_combine_fp4(int head_dim, const DecodeArgs& a, cudaStream_t stream);
+// Merges the splits that launch_decode_fp4 left in a.o_part and a.lse_part.
+// behind_attention: that was the launch just before, so that the merge may be
+// let in as its CTAs leave and read the metadata, which it waited for, at once.
+// Else what came before may still be writing the metadata: a plain launch.
+cudaError_t launch_combine_fp4(int head_dim, const DecodeArgs& a, bool behind_attention, cudaStream_t stream);
 
 // 4-bit pages and the read-back (cache4.cu)
 cudaError_t launch_append_fp4(const AppendArgs& a, cudaStream_t stream);

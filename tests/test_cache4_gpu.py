@@ -610,3 +610,36 @@ def test_decode_of_many_keys_far_below_a_dominant_one(group, bits):
     err = np.abs(out.double().cpu().numpy() - ro)
     assert (ro > 0).all() and (err <= tol).all(), float((err / ro).max())
     assert (np.abs(lse.cpu().numpy() - rl) <= 2.0 ** -19 * (1 + np.abs(rl))).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_combine_right_behind_the_device_metadata(d):
+    """The merge called on its own, directly after the metadata was written on
+    the device: it reads what was written, not what the buffer held before."""
+    c = Cache([4000, 100, 0, 900, 3000], 2, d, seed=105)
+    hq, nb = 16, len(c.lens)
+    sh = B.pa_decode_shapes(batch=nb, num_q_heads=hq, num_kv_heads=2, head_dim=d, page_size=64,
+                            max_pages_per_seq=c.table.shape[1], num_pool_pages=c.pages, kv_dtype=B.PA_KV_FP4_E2M1,
+                            num_sms=ops.num_sms(), ctas_per_sm=0, forced_splits=0)
+    plan = B.pa_get_static_plan(sh)
+    meta = torch.zeros(plan.meta_ints, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device=DEV)
+    k, v, ks, vs, table, lens = c.up()
+    q = W.bf16_normal(105, 1, (nb, hq, d))
+    out, lse = torch.empty((nb, hq, d), dtype=torch.bfloat16, device=DEV), torch.empty((nb, hq), device=DEV)
+    B.pa_get_metadata_device(sh, plan, lens, meta)
+    B.pa_decode_attend(sh, plan, ops.as_bf16(q, DEV), k, v, ks, vs, table, lens, meta, d ** -0.5, out, lse, ws)
+    splits = S.unpack(meta.cpu().tolist())["n_splits"]
+    split = torch.tensor([n > 1 for n in splits], device=DEV)
+    assert split.any() and not split.all()
+    B.pa_decode_combine(sh, plan, meta, out, lse, ws)
+    assert B.pa_check_status(ws) == B.PA_OK
+    check(c, q, d ** -0.5, out, lse)
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    for _ in range(50):
+        meta.zero_()  # a merge that looked too early would find no splits
+        o2.fill_(7.0)
+        B.pa_get_metadata_device(sh, plan, lens, meta)
+        B.pa_decode_combine(sh, plan, meta, o2, l2, ws)
+        assert torch.equal(o2[split], out[split]) and torch.equal(l2[split], lse[split]) and (o2[~split] == 7).all()
+    assert B.pa_check_status(ws) == B.PA_OK
