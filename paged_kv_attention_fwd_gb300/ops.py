@@ -159,13 +159,66 @@ def append_shapes(batch: int, num_kv_heads: int, head_dim: int, max_pages: int, 
                               kv_dtype=KV_DTYPES[kv_dtype])
 
 
+# The library sees addresses only: a tensor of another type, shape, layout or
+# device than a call takes it to be would be misread, or read or written past
+# its end, without an error.  The helpers below refuse such tensors.
+
+def _refuse(name: str, x, expected: str):
+    raise ValueError(f"{name}: {x.dtype} {tuple(x.shape)} with strides {tuple(x.stride())} on {x.device}, expected {expected}")
+
+
+def _check_flat(name: str, x, dtype, count: int, device, what: str):
+    """A contiguous tensor of at least `count` elements."""
+    if x.dtype != dtype or x.device != device or not x.is_contiguous() or x.numel() < count:
+        _refuse(name, x, f"contiguous {what} of {dtype} on {device}")
+
+
+def _check_rows(name: str, x, sh: B.pa_append_shapes, device):
+    """Ragged 16-bit rows [total_new, Hk, D]; a longer buffer will do."""
+    dtype = torch.float16 if sh.kv_dtype == B.PA_KV_FP16 else torch.bfloat16
+    if x.dim() != 3 or x.shape[0] < sh.total_new or tuple(x.shape[1:]) != (sh.num_kv_heads, sh.head_dim):
+        _refuse(name, x, f"[{sh.total_new}, {sh.num_kv_heads}, {sh.head_dim}]")
+    _check_flat(name, x, dtype, 0, device, f"[{sh.total_new}, {sh.num_kv_heads}, {sh.head_dim}]")
+
+
+def _check_cache(sh: B.pa_append_shapes, device, k_pool, v_pool, k_scale, v_scale, cu_seqlens, start_pos, block_table,
+                 workspace):
+    """What every call on a paged cache takes."""
+    slab = B.pa_page_slab_bytes(sh.head_dim, sh.kv_dtype)
+    types = {B.PA_KV_BF16: (torch.bfloat16,), B.PA_KV_FP16: (torch.float16,),
+             B.PA_KV_FP8_E4M3: (torch.float8_e4m3fn, torch.uint8), B.PA_KV_FP4_E2M1: (torch.uint8,)}.get(sh.kv_dtype, ())
+    for name, x in (("k_pool", k_pool), ("v_pool", v_pool)):
+        if (x.dtype not in types or x.device != device or not x.is_contiguous()
+                or x.numel() * x.element_size() < sh.num_pool_pages * sh.num_kv_heads * slab):
+            _refuse(name, x, f"{sh.num_pool_pages} contiguous pages of {sh.num_kv_heads} heads of {slab} bytes, "
+                             f"{' or '.join(map(str, types))} on {device}")
+    if sh.kv_dtype in (B.PA_KV_FP8_E4M3, B.PA_KV_FP4_E2M1):
+        for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if x is not None:
+                _check_flat(name, x, torch.float32, sh.num_kv_heads, device, f"[{sh.num_kv_heads}]")
+    _check_flat("cu_seqlens", cu_seqlens, torch.int32, sh.batch + 1, device, f"[{sh.batch + 1}]")
+    _check_flat("start_pos", start_pos, torch.int32, sh.batch, device, f"[{sh.batch}]")
+    t = block_table
+    if (t.dtype != torch.int32 or t.device != device or t.dim() != 2 or t.shape[0] < sh.batch
+            or (t.shape[1] > 1 and t.stride(1) != 1) or (sh.batch > 1 and t.stride(0) != sh.max_pages_per_seq)
+            or (sh.batch == 1 and t.shape[1] < sh.max_pages_per_seq)):
+        _refuse("block_table", t, f"{sh.batch} rows of {sh.max_pages_per_seq} int32, one behind the other, on {device}")
+    if workspace is not None:
+        _check_flat("workspace", workspace, workspace.dtype, 0, device, "bytes")
+
+
 def _status(workspace, device):
     return torch.zeros(B.PA_STATUS_BYTES, dtype=torch.uint8, device=device) if workspace is None else workspace
 
 
 def append_kv(sh: B.pa_append_shapes, k_new, v_new, cu_seqlens_new, start_pos, block_table, k_pool, v_pool,
               k_scale=None, v_scale=None, workspace=None, stream=None):
-    """Write new tokens' keys and values into their pages.  Returns the workspace."""
+    """Write new tokens' keys and values, contiguous [total_new, Hk, D], into
+    their pages.  Returns the workspace."""
+    if sh.batch > 0 and sh.total_new > 0:
+        _check_rows("k_new", k_new, sh, k_new.device)
+        _check_rows("v_new", v_new, sh, k_new.device)
+        _check_cache(sh, k_new.device, k_pool, v_pool, k_scale, v_scale, cu_seqlens_new, start_pos, block_table, workspace)
     workspace = _status(workspace, k_new.device)
     B.pa_append_kv(sh, k_new, v_new, cu_seqlens_new, start_pos, block_table, k_pool, v_pool, k_scale, v_scale,
                    workspace, stream=stream)
@@ -178,6 +231,11 @@ def gather_kv(sh: B.pa_append_shapes, k_pool, v_pool, cu_seqlens, start_pos, blo
     fp16 pools, else bf16).  Returns (k_out, v_out, workspace)."""
     dt = torch.float16 if sh.kv_dtype == B.PA_KV_FP16 else torch.bfloat16
     shape = (sh.total_new, sh.num_kv_heads, sh.head_dim)
+    if sh.batch > 0 and sh.total_new > 0:
+        _check_cache(sh, k_pool.device, k_pool, v_pool, k_scale, v_scale, cu_seqlens, start_pos, block_table, workspace)
+        for name, x in (("k_out", k_out), ("v_out", v_out)):
+            if x is not None:
+                _check_rows(name, x, sh, k_pool.device)
     k_out = torch.empty(shape, dtype=dt, device=k_pool.device) if k_out is None else k_out
     v_out = torch.empty(shape, dtype=dt, device=k_pool.device) if v_out is None else v_out
     workspace = _status(workspace, k_pool.device)
@@ -248,6 +306,8 @@ def norm_rope_append_kv(sh: B.pa_rope_shapes, append: B.pa_append_shapes, q, k, 
     Returns (q_out, workspace)."""
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
     _check_steps(sh, q=q, k=k, v=v, q_out=q_out)
+    if append.batch > 0 and sh.total_tokens > 0:
+        _check_cache(append, q.device, k_pool, v_pool, k_scale, v_scale, cu_seqlens_new, start_pos, block_table, workspace)
     workspace = _status(workspace, q.device)
     B.pa_norm_rope_append_kv(sh, append, q, k, v, q_weight, k_weight, positions, cos_sin, cu_seqlens_new, start_pos,
                              block_table, q_out, k_pool, v_pool, k_scale, v_scale, workspace, stream=stream)

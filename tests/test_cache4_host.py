@@ -238,3 +238,68 @@ def test_python_shapes():
         ops.qk_norm_rope(ops.rope_shapes(q, k), q, k[:4])
     t = ops.rope_table(10, 8, theta=100.0, device="cpu")
     assert t.shape == (10, 8) and torch.allclose(t[3, 1], torch.tensor(3 * 100 ** -0.25).cos())
+
+
+# ----------------------------------------------------------------- tensors that the library would misread
+
+def cache_tensors(kv="fp4", **change):
+    """Everything ops.append_kv and ops.gather_kv take for 3 sequences and 10 tokens, 2 heads of 64, 9 pages."""
+    t = dict(k_new=torch.zeros((10, 2, 64), dtype=torch.bfloat16), v_new=torch.zeros((10, 2, 64), dtype=torch.bfloat16),
+             cu=torch.zeros(4, dtype=torch.int32), start=torch.zeros(3, dtype=torch.int32),
+             table=torch.zeros((3, 5), dtype=torch.int32), k_pool=ops.kv_pool(9, 2, 64, kv, "cpu"),
+             v_pool=ops.kv_pool(9, 2, 64, kv, "cpu"), k_scale=torch.ones(2), v_scale=torch.ones(2),
+             k_out=torch.zeros((10, 2, 64), dtype=torch.bfloat16), v_out=torch.zeros((10, 2, 64), dtype=torch.bfloat16),
+             workspace=torch.zeros(256, dtype=torch.uint8))
+    t.update(change)
+    return t
+
+
+def ops_cache_call(name, t, kv="fp4"):
+    sh = ops.append_shapes(3, 2, 64, 5, 9, 10, kv)
+    if name == "append":
+        return ops.append_kv(sh, t["k_new"], t["v_new"], t["cu"], t["start"], t["table"], t["k_pool"], t["v_pool"],
+                             t["k_scale"], t["v_scale"], t["workspace"], stream=1)
+    return ops.gather_kv(sh, t["k_pool"], t["v_pool"], t["cu"], t["start"], t["table"], t["k_scale"], t["v_scale"],
+                         t["k_out"], t["v_out"], t["workspace"], stream=1)
+
+
+PACKED = torch.zeros((10, 6, 64), dtype=torch.bfloat16)
+CACHE_TENSORS = [
+    ("cu", torch.zeros(4, dtype=torch.int64)), ("cu", torch.zeros(3, dtype=torch.int32)),
+    ("start", torch.zeros(3, dtype=torch.int64)), ("start", torch.zeros((3, 2), dtype=torch.int32)[:, 0]),
+    ("table", torch.zeros((3, 5), dtype=torch.int64)), ("table", torch.zeros((3, 8), dtype=torch.int32)[:, :5]),
+    ("table", torch.zeros((3, 4), dtype=torch.int32)), ("table", torch.zeros((2, 5), dtype=torch.int32)),
+    ("table", torch.zeros((5, 3), dtype=torch.int32).T), ("table", torch.zeros(15, dtype=torch.int32)),
+    ("k_pool", torch.zeros((8, 2, 2304), dtype=torch.uint8)), ("v_pool", torch.zeros((9, 2, 64, 64), dtype=torch.bfloat16)),
+    ("k_pool", torch.zeros((2, 9, 2304), dtype=torch.uint8).transpose(0, 1)),
+    ("k_scale", torch.ones(1)), ("v_scale", torch.ones(2, dtype=torch.bfloat16)), ("v_scale", torch.ones(4)[::2]),
+    ("workspace", torch.zeros(512, dtype=torch.uint8)[::2]),
+]
+ROWS = [PACKED[:, 2:4], torch.zeros((9, 2, 64), dtype=torch.bfloat16), torch.zeros((10, 1, 64), dtype=torch.bfloat16),
+        torch.zeros((10, 2, 64)), torch.zeros((2, 10, 64), dtype=torch.bfloat16).transpose(0, 1),
+        torch.zeros((10, 128), dtype=torch.bfloat16), torch.zeros((10, 2, 64), dtype=torch.float16)]
+
+
+@pytest.mark.parametrize("name,key,tensor",
+                         [(n, k, x) for n in ("append", "gather") for k, x in CACHE_TENSORS]
+                         + [("append", k, x) for k in ("k_new", "v_new") for x in ROWS]
+                         + [("gather", k, x) for k in ("k_out", "v_out") for x in ROWS])
+def test_cache_calls_refuse_tensors_of_another_layout(name, key, tensor):
+    with pytest.raises(ValueError, match={"cu": "cu_seqlens", "start": "start_pos", "table": "block_table"}.get(key, key)):
+        ops_cache_call(name, cache_tensors(**{key: tensor}))
+
+
+@pytest.mark.parametrize("name", ["append", "gather"])
+@pytest.mark.parametrize("kv,change", [
+    ("fp4", {}), ("bf16", {"k_scale": None, "v_scale": None}), ("bf16", {"k_scale": torch.ones(1), "v_scale": None}),
+    ("e4m3", {}), ("e4m3", {"k_pool": torch.zeros((9, 2, 64, 64), dtype=torch.uint8)}),
+    ("fp4", {"table": torch.zeros((4, 5), dtype=torch.int32)[:, :3]}), ("fp4", {"cu": torch.zeros(9, dtype=torch.int32)}),
+    ("fp4", {"k_pool": torch.zeros((12, 2, 2304), dtype=torch.uint8)}),
+    ("fp4", {k: torch.zeros((16, 2, 64), dtype=torch.bfloat16) for k in ("k_new", "v_out")}),
+])
+def test_cache_calls_take_what_the_library_reads_right(name, kv, change):
+    """These reach the library: a NULL workspace pointer is what it refuses."""
+    t = cache_tensors(kv, **change)
+    t["workspace"] = torch.zeros(0, dtype=torch.uint8)
+    with pytest.raises(B.PaError):
+        ops_cache_call(name, t, kv)
