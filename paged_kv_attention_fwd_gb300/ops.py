@@ -288,12 +288,34 @@ def _check_steps(sh: B.pa_rope_shapes, **tensors):
                              f"{sh.total_tokens} of {step}")
 
 
+def _check_rope(sh: B.pa_rope_shapes, q, q_weight, k_weight, positions, cos_sin):
+    if sh.norm:
+        for name, x in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if x is not None:
+                _check_flat(name, x, q.dtype, sh.head_dim, q.device, f"[{sh.head_dim}]")
+    if sh.rope_dim == 0:  # neither is read
+        return
+    if positions is not None:
+        _check_flat("positions", positions, torch.int32, sh.num_axes * sh.total_tokens, q.device,
+                    f"[{sh.num_axes}, {sh.total_tokens}]")
+        if positions.shape[-1] != sh.total_tokens:
+            _refuse("positions", positions, f"[{sh.num_axes}, {sh.total_tokens}]")
+    if cos_sin is not None:
+        _check_flat("cos_sin", cos_sin, torch.float32, sh.max_position * sh.rope_dim, q.device,
+                    f"[{sh.max_position}, {sh.rope_dim}]")
+        if cos_sin.shape[-1] != sh.rope_dim:
+            _refuse("cos_sin", cos_sin, f"[{sh.max_position}, {sh.rope_dim}]")
+
+
 def qk_norm_rope(sh: B.pa_rope_shapes, q, k, q_weight=None, k_weight=None, positions=None, cos_sin=None, q_out=None,
                  k_out=None, workspace=None, stream=None):
     """RMS norm of every head, then the rotation.  Returns (q_out, k_out, workspace)."""
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
     k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
     _check_steps(sh, q=q, k=k, q_out=q_out, k_out=k_out)
+    _check_rope(sh, q, q_weight, k_weight, positions, cos_sin)
+    if workspace is not None:
+        _check_flat("workspace", workspace, workspace.dtype, 0, q.device, "bytes")
     workspace = _status(workspace, q.device)
     B.pa_qk_norm_rope(sh, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, workspace, stream=stream)
     return q_out, k_out, workspace
@@ -306,6 +328,7 @@ def norm_rope_append_kv(sh: B.pa_rope_shapes, append: B.pa_append_shapes, q, k, 
     Returns (q_out, workspace)."""
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
     _check_steps(sh, q=q, k=k, v=v, q_out=q_out)
+    _check_rope(sh, q, q_weight, k_weight, positions, cos_sin)
     if append.batch > 0 and sh.total_tokens > 0:
         _check_cache(append, q.device, k_pool, v_pool, k_scale, v_scale, cu_seqlens_new, start_pos, block_table, workspace)
     workspace = _status(workspace, q.device)

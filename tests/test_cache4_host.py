@@ -303,3 +303,68 @@ def test_cache_calls_take_what_the_library_reads_right(name, kv, change):
     t["workspace"] = torch.zeros(0, dtype=torch.uint8)
     with pytest.raises(B.PaError):
         ops_cache_call(name, t, kv)
+
+
+def rope_tensors(tokens=5, **change):
+    qkv = torch.zeros((tokens, 12 * 64), dtype=torch.bfloat16)
+    q, k, v = (x.unflatten(-1, (-1, 64)) for x in qkv.split([8 * 64, 2 * 64, 2 * 64], -1))
+    t = dict(q=q, k=k, v=v, q_weight=torch.ones(64, dtype=torch.bfloat16), k_weight=torch.ones(64, dtype=torch.bfloat16),
+             positions=torch.zeros((2, tokens), dtype=torch.int32), cos_sin=torch.zeros((7, 32)),
+             q_out=torch.zeros((tokens, 8, 64), dtype=torch.bfloat16), k_out=torch.zeros((tokens, 2, 64), dtype=torch.bfloat16))
+    sh = ops.rope_shapes(q, k, v, rope_dim=32, max_position=7, sections=[10, 6])
+    t.update(change)
+    return sh, t
+
+
+def ops_rope_call(name, sh, t, workspace=None):
+    ws = torch.zeros(0, dtype=torch.uint8) if workspace is None else workspace
+    if name == "rope":
+        return ops.qk_norm_rope(sh, t["q"], t["k"], t["q_weight"], t["k_weight"], t["positions"], t["cos_sin"], t["q_out"],
+                                t["k_out"], ws, stream=1)
+    c = cache_tensors()
+    ap = ops.append_shapes(3, 2, 64, 5, 9, sh.total_tokens, "fp4")
+    return ops.norm_rope_append_kv(sh, ap, t["q"], t["k"], t["v"], c["cu"], t.get("start", c["start"]), c["table"],
+                                   t.get("k_pool", c["k_pool"]), c["v_pool"], t["q_weight"], t["k_weight"], t["positions"],
+                                   t["cos_sin"], c["k_scale"], c["v_scale"], t["q_out"], ws, stream=1)
+
+
+ROPE_TENSORS = [
+    ("positions", torch.zeros((2, 5), dtype=torch.int64)), ("positions", torch.zeros((1, 5), dtype=torch.int32)),
+    ("positions", torch.zeros((5, 2), dtype=torch.int32).T), ("positions", torch.zeros((5, 2), dtype=torch.int32)),
+    ("positions", torch.zeros((2, 8), dtype=torch.int32)), ("cos_sin", torch.zeros((7, 32), dtype=torch.bfloat16)),
+    ("cos_sin", torch.zeros((7, 32), dtype=torch.float64)), ("cos_sin", torch.zeros((6, 32))),
+    ("cos_sin", torch.zeros((14, 16))), ("cos_sin", torch.zeros((32, 7)).T), ("q_weight", torch.ones(64)),
+    ("k_weight", torch.ones(64, dtype=torch.float16)), ("q_weight", torch.ones(63, dtype=torch.bfloat16)),
+    ("k_weight", torch.ones(128, dtype=torch.bfloat16)[::2]),
+]
+
+
+@pytest.mark.parametrize("name", ["rope", "fused"])
+@pytest.mark.parametrize("key,tensor", ROPE_TENSORS)
+def test_rope_calls_refuse_tensors_of_another_layout(name, key, tensor):
+    sh, t = rope_tensors(**{key: tensor})
+    with pytest.raises(ValueError, match=f"^{key}: "):
+        ops_rope_call(name, sh, t)
+
+
+def test_fused_call_checks_its_cache_and_workspace():
+    for key, x in (("start", torch.zeros(3, dtype=torch.int64)), ("k_pool", torch.zeros((8, 2, 2304), dtype=torch.uint8))):
+        sh, t = rope_tensors(**{key: x})
+        with pytest.raises(ValueError, match="start_pos" if key == "start" else key):
+            ops_rope_call("fused", sh, t)
+    for name in ("rope", "fused"):
+        with pytest.raises(ValueError, match="workspace"):
+            ops_rope_call(name, *rope_tensors(), workspace=torch.zeros(512, dtype=torch.uint8)[::2])
+
+
+@pytest.mark.parametrize("name", ["rope", "fused"])
+@pytest.mark.parametrize("change", [{}, {"q_weight": None, "k_weight": None}, {"cos_sin": torch.zeros((9, 32))},
+                                    {"positions": torch.zeros((3, 5), dtype=torch.int32)}])
+def test_rope_calls_take_what_the_library_reads_right(name, change):
+    sh, t = rope_tensors(**change)
+    with pytest.raises(B.PaError):
+        ops_rope_call(name, sh, t)
+    sh.norm = 0  # weights that are not read
+    t["q_weight"] = torch.ones(3)
+    with pytest.raises(B.PaError):
+        ops_rope_call(name, sh, t)
