@@ -264,6 +264,8 @@ def rope_shapes(q, k, v=None, rope_dim: int = 0, max_position: int = 0, interlea
         if x is not None and (x.shape[0] != t or x.shape[2] != d or (x.shape[1] > 1 and x.stride(1) != d)
                               or x.stride(2) != 1 or x.dtype != q.dtype):
             raise ValueError(f"{name}: heads must be contiguous rows of q's head_dim and type, one per token")
+        if x is not None and x.shape[1] != (hq if name in ("q", "q_out") else hk):
+            raise ValueError(f"{name}: {x.shape[1]} heads, {hq} query and {hk} key heads given")
     sections = list(sections) if sections is not None else [rope_dim // 2]
 
     def step(x, heads):  # a single token's stride is never used
@@ -281,11 +283,16 @@ def rope_shapes(q, k, v=None, rope_dim: int = 0, max_position: int = 0, interlea
 
 def _check_steps(sh: B.pa_rope_shapes, **tensors):
     """Tensors as the shapes describe them: a step other than theirs would reach past an output."""
+    dtype = torch.float16 if sh.dtype == B.PA_KV_FP16 else torch.bfloat16
     for name, x in tensors.items():
-        step = getattr(sh, name + "_stride")
+        step, d = getattr(sh, name + "_stride"), sh.head_dim
         if x.shape[0] != sh.total_tokens or (sh.total_tokens > 1 and x.shape[1] > 0 and x.stride(0) != step):
             raise ValueError(f"{name}: {x.shape[0]} tokens of stride {x.stride(0)}, the shapes are for "
                              f"{sh.total_tokens} of {step}")
+        heads = sh.num_q_heads if name in ("q", "q_out") else sh.num_kv_heads
+        if (tuple(x.shape[1:]) != (heads, d) or x.dtype != dtype or x.device != tensors["q"].device
+                or (heads > 1 and x.stride(1) != d) or (heads > 0 and x.stride(2) != 1)):
+            _refuse(name, x, f"{heads} contiguous heads of {d} of {dtype} on {tensors['q'].device}")
 
 
 def _check_rope(sh: B.pa_rope_shapes, q, q_weight, k_weight, positions, cos_sin):

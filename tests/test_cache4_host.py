@@ -336,6 +336,10 @@ ROPE_TENSORS = [
     ("cos_sin", torch.zeros((14, 16))), ("cos_sin", torch.zeros((32, 7)).T), ("q_weight", torch.ones(64)),
     ("k_weight", torch.ones(64, dtype=torch.float16)), ("q_weight", torch.ones(63, dtype=torch.bfloat16)),
     ("k_weight", torch.ones(128, dtype=torch.bfloat16)[::2]),
+    ("q", torch.zeros((5, 12, 64), dtype=torch.float16)[:, :8]), ("q", torch.zeros((5, 12, 64), dtype=torch.bfloat16)[:, :7]),
+    ("q", torch.zeros((5, 6, 128), dtype=torch.bfloat16)[:, :4]), ("k", torch.zeros((5, 12, 64), dtype=torch.bfloat16)[:, :1]),
+    ("q", torch.zeros((5, 6, 2, 64), dtype=torch.bfloat16).transpose(1, 2).reshape(5, 12, 64)[:, :12:2][:, :8]),
+    ("q_out", torch.zeros((5, 4, 64), dtype=torch.bfloat16)), ("q_out", torch.zeros((5, 8, 64), dtype=torch.float16)),
 ]
 
 
@@ -345,6 +349,22 @@ def test_rope_calls_refuse_tensors_of_another_layout(name, key, tensor):
     sh, t = rope_tensors(**{key: tensor})
     with pytest.raises(ValueError, match=f"^{key}: "):
         ops_rope_call(name, sh, t)
+
+
+@pytest.mark.parametrize("name,key,shape", [("rope", "q_out", (1, 4, 64)), ("rope", "k_out", (1, 1, 64)), ("rope", "k", (1, 1, 64)),
+                                            ("fused", "v", (1, 1, 64)), ("fused", "q_out", (1, 4, 64)), ("fused", "q", (1, 16, 64))])
+def test_one_token_of_other_heads_is_refused(name, key, shape):
+    """A single token's stride is never used, so that its heads alone tell a tensor that is too small."""
+    sh, t = rope_tensors(1, **{key: torch.zeros(shape, dtype=torch.bfloat16)})
+    with pytest.raises(ValueError, match=f"^{key}: "):
+        ops_rope_call(name, sh, t)
+
+
+def test_shapes_of_other_head_counts_are_refused():
+    _, t = rope_tensors()
+    for key, x in (("v", t["q"]), ("q_out", t["k"]), ("k_out", t["q"])):
+        with pytest.raises(ValueError, match=f"^{key}: . heads"):
+            ops.rope_shapes(t["q"], t["k"], rope_dim=32, max_position=7, **{key: x})
 
 
 def test_fused_call_checks_its_cache_and_workspace():
