@@ -6,6 +6,7 @@ runs in the library's CUDA kernels.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Optional
 
@@ -207,8 +208,27 @@ def _check_cache(sh: B.pa_append_shapes, device, k_pool, v_pool, k_scale, v_scal
         _check_flat("workspace", workspace, workspace.dtype, 0, device, "bytes")
 
 
-def _status(workspace, device):
-    return torch.zeros(B.PA_STATUS_BYTES, dtype=torch.uint8, device=device) if workspace is None else workspace
+def _on(stream):
+    """What a call allocates is allocated, and cleared, on the stream it runs on."""
+    if stream is None:
+        return nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _status(workspace, device, stream):
+    if workspace is not None:
+        return workspace
+    with _on(stream):
+        return torch.zeros(B.PA_STATUS_BYTES, dtype=torch.uint8, device=device)
+
+
+def _output(given, shape, dtype, device, stream):
+    if given is not None:
+        return given
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def append_kv(sh: B.pa_append_shapes, k_new, v_new, cu_seqlens_new, start_pos, block_table, k_pool, v_pool,
@@ -219,7 +239,7 @@ def append_kv(sh: B.pa_append_shapes, k_new, v_new, cu_seqlens_new, start_pos, b
         _check_rows("k_new", k_new, sh, k_new.device)
         _check_rows("v_new", v_new, sh, k_new.device)
         _check_cache(sh, k_new.device, k_pool, v_pool, k_scale, v_scale, cu_seqlens_new, start_pos, block_table, workspace)
-    workspace = _status(workspace, k_new.device)
+    workspace = _status(workspace, k_new.device, stream)
     B.pa_append_kv(sh, k_new, v_new, cu_seqlens_new, start_pos, block_table, k_pool, v_pool, k_scale, v_scale,
                    workspace, stream=stream)
     return workspace
@@ -236,9 +256,9 @@ def gather_kv(sh: B.pa_append_shapes, k_pool, v_pool, cu_seqlens, start_pos, blo
         for name, x in (("k_out", k_out), ("v_out", v_out)):
             if x is not None:
                 _check_rows(name, x, sh, k_pool.device)
-    k_out = torch.empty(shape, dtype=dt, device=k_pool.device) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=dt, device=k_pool.device) if v_out is None else v_out
-    workspace = _status(workspace, k_pool.device)
+    k_out = _output(k_out, shape, dt, k_pool.device, stream)
+    v_out = _output(v_out, shape, dt, k_pool.device, stream)
+    workspace = _status(workspace, k_pool.device, stream)
     B.pa_gather_kv(sh, k_pool, v_pool, k_scale, v_scale, cu_seqlens, start_pos, block_table, k_out, v_out, workspace,
                    stream=stream)
     return k_out, v_out, workspace
@@ -317,13 +337,13 @@ def _check_rope(sh: B.pa_rope_shapes, q, q_weight, k_weight, positions, cos_sin)
 def qk_norm_rope(sh: B.pa_rope_shapes, q, k, q_weight=None, k_weight=None, positions=None, cos_sin=None, q_out=None,
                  k_out=None, workspace=None, stream=None):
     """RMS norm of every head, then the rotation.  Returns (q_out, k_out, workspace)."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    q_out = _output(q_out, q.shape, q.dtype, q.device, stream)
+    k_out = _output(k_out, k.shape, k.dtype, k.device, stream)
     _check_steps(sh, q=q, k=k, q_out=q_out, k_out=k_out)
     _check_rope(sh, q, q_weight, k_weight, positions, cos_sin)
     if workspace is not None:
         _check_flat("workspace", workspace, workspace.dtype, 0, q.device, "bytes")
-    workspace = _status(workspace, q.device)
+    workspace = _status(workspace, q.device, stream)
     B.pa_qk_norm_rope(sh, q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, workspace, stream=stream)
     return q_out, k_out, workspace
 
@@ -333,12 +353,12 @@ def norm_rope_append_kv(sh: B.pa_rope_shapes, append: B.pa_append_shapes, q, k, 
                         k_scale=None, v_scale=None, q_out=None, workspace=None, stream=None):
     """qk_norm_rope with the keys and values going straight into their pages.
     Returns (q_out, workspace)."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    q_out = _output(q_out, q.shape, q.dtype, q.device, stream)
     _check_steps(sh, q=q, k=k, v=v, q_out=q_out)
     _check_rope(sh, q, q_weight, k_weight, positions, cos_sin)
     if append.batch > 0 and sh.total_tokens > 0:
         _check_cache(append, q.device, k_pool, v_pool, k_scale, v_scale, cu_seqlens_new, start_pos, block_table, workspace)
-    workspace = _status(workspace, q.device)
+    workspace = _status(workspace, q.device, stream)
     B.pa_norm_rope_append_kv(sh, append, q, k, v, q_weight, k_weight, positions, cos_sin, cu_seqlens_new, start_pos,
                              block_table, q_out, k_pool, v_pool, k_scale, v_scale, workspace, stream=stream)
     return q_out, workspace

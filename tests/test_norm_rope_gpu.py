@@ -431,3 +431,37 @@ def test_append_padding_is_the_two_calls(kv):
     for a, b, c in zip(one, two, bare):
         assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
         assert torch.equal(b.view(torch.uint8), c.view(torch.uint8)) and c.view(torch.uint8).any()
+
+
+@pytest.mark.parametrize("call", ["append", "gather", "rope", "fused"])
+@pytest.mark.parametrize("handle", [False, True])
+def test_buffers_that_a_call_makes_belong_to_its_stream(call, handle):
+    """A call on a stream of its own while the current one is busy: the status word that it makes is cleared before the
+    kernel records its fault in it, not by a fill that the current stream comes to later."""
+    t, d, hk = 6, 64, 2
+    q, k, v, w, pos, _, table = make(t, 4, hk, d, "bf16", seed=15, packed=False)
+    pos[0, 3] = 4096  # past the table
+    pools = [ops.kv_pool(3, hk, d, "bf16", DEV) for _ in range(2)]
+    cu, start, bt = dev(np.array([0, t], np.int32)), dev(np.array([60], np.int32)), dev(np.array([[1, 9]], np.int32))
+    ash, sh = ops.append_shapes(1, hk, d, 2, 3, t), ops.rope_shapes(q, k, v, rope_dim=d, max_position=4096)
+    busy = torch.zeros(1 << 28, device=DEV)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+
+    def run():
+        if call == "append":
+            return ops.append_kv(ash, k, v, cu, start, bt, *pools, stream=stream)
+        if call == "gather":
+            return ops.gather_kv(ash, *pools, cu, start, bt, stream=stream)[2]
+        if call == "rope":
+            return ops.qk_norm_rope(sh, q, k, w[0], w[1], pos, table, stream=stream)[2]
+        return ops.norm_rope_append_kv(sh, ash, q, k, v, cu, start, bt, *pools, w[0], w[1], None, table, stream=stream)[1]
+
+    run()  # kernels are loaded at their first launch, which waits for the device
+    busy.add_(1)
+    torch.cuda.synchronize()
+    for _ in range(40):
+        busy.add_(1)
+    ws = run()
+    torch.cuda.synchronize()
+    assert B.pa_check_status(ws) == B.PA_ERR_DEVICE_BOUNDS
