@@ -43,6 +43,22 @@ def as_e4m3(bits: np.ndarray, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(bits)).to(device).view(torch.float8_e4m3fn)
 
 
+def _on(stream):
+    """What a call allocates is allocated, and cleared, on the stream it runs on."""
+    if stream is None:
+        return nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _output(given, shape, dtype, device, stream):
+    if given is not None:
+        return given
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 @dataclass
 class DecodePlan:
     shapes: B.pa_decode_shapes
@@ -71,11 +87,9 @@ def plan_decode(seq_lens_host, block_table_host, num_q_heads: int, num_kv_heads:
 def decode(p: DecodePlan, q, k_pool, v_pool, block_table, seq_lens, scale: float, k_scale=None, v_scale=None,
            out=None, lse=None, stream=None):
     sh = p.shapes
-    if out is None:
-        odt = torch.float16 if sh.kv_dtype == B.PA_KV_FP16 else torch.bfloat16
-        out = torch.empty((sh.batch, sh.num_q_heads, sh.head_dim), dtype=odt, device=q.device)
-    if lse is None:
-        lse = torch.empty((sh.batch, sh.num_q_heads), dtype=torch.float32, device=q.device)
+    odt = torch.float16 if sh.kv_dtype == B.PA_KV_FP16 else torch.bfloat16
+    out = _output(out, (sh.batch, sh.num_q_heads, sh.head_dim), odt, q.device, stream)
+    lse = _output(lse, (sh.batch, sh.num_q_heads), torch.float32, q.device, stream)
     B.pa_decode(sh, p.plan, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, p.meta_dev, scale, out,
                 lse, p.workspace, stream=stream)
     return out, lse
@@ -134,13 +148,12 @@ def prefill_mla_rope_fp8(inp, device, causal: bool = True, qo_offset=None, strea
 def prefill(sh: B.pa_prefill_shapes, q, k, v, cu_seqlens_q, cu_seqlens_k, scale: float, causal: bool = True,
             block_table=None, k_rope=None, qo_offset=None, out=None, lse=None, workspace=None, stream=None):
     dev = q.device
-    if out is None:
-        odt = torch.float16 if sh.dtype == B.PA_KV_FP16 else torch.bfloat16
-        out = torch.empty((sh.total_q, sh.num_q_heads, sh.head_dim_v), dtype=odt, device=dev)
-    if lse is None:
-        lse = torch.empty((sh.total_q, sh.num_q_heads), dtype=torch.float32, device=dev)
+    odt = torch.float16 if sh.dtype == B.PA_KV_FP16 else torch.bfloat16
+    out = _output(out, (sh.total_q, sh.num_q_heads, sh.head_dim_v), odt, dev, stream)
+    lse = _output(lse, (sh.total_q, sh.num_q_heads), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.zeros(B.pa_prefill_workspace_size(sh), dtype=torch.uint8, device=dev)
+        with _on(stream):
+            workspace = torch.zeros(B.pa_prefill_workspace_size(sh), dtype=torch.uint8, device=dev)
     B.pa_prefill(sh, q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k, block_table, qo_offset, causal, scale, out, lse,
                  workspace, stream=stream)
     return out, lse, workspace
@@ -208,27 +221,11 @@ def _check_cache(sh: B.pa_append_shapes, device, k_pool, v_pool, k_scale, v_scal
         _check_flat("workspace", workspace, workspace.dtype, 0, device, "bytes")
 
 
-def _on(stream):
-    """What a call allocates is allocated, and cleared, on the stream it runs on."""
-    if stream is None:
-        return nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
-
-
 def _status(workspace, device, stream):
     if workspace is not None:
         return workspace
     with _on(stream):
         return torch.zeros(B.PA_STATUS_BYTES, dtype=torch.uint8, device=device)
-
-
-def _output(given, shape, dtype, device, stream):
-    if given is not None:
-        return given
-    with _on(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def append_kv(sh: B.pa_append_shapes, k_new, v_new, cu_seqlens_new, start_pos, block_table, k_pool, v_pool,

@@ -352,3 +352,27 @@ def test_prefill_in_cuda_graph_replayed_with_new_inputs():
         ref_out, ref_lse = reference(case)
         assert_close(out.float().cpu().numpy(), lse.cpu().numpy(), ref_out, ref_lse)
     assert B.pa_check_status(ws) == B.PA_OK
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_prefill_clears_its_workspace_on_its_own_stream(handle):
+    """A call on a stream of its own while the current one is busy, with the buffers that it makes itself: its work
+    counters are clear before the kernel reads them."""
+    inp = W.make_paged_prefill([300, 130], [700, 1100], 8, 4, 128, seed=14)
+    dev = "cuda"
+    q, k, v = (ops.as_16(x, dev, inp.dtype) for x in (inp.q, inp.k, inp.v))
+    cq, ck, bt = (torch.from_numpy(x).to(dev) for x in (inp.cu_seqlens_q, inp.cu_seqlens_k, inp.block_table))
+    sh = ops.prefill_shapes(inp.batch, 8, 4, 128, 128, 0, inp.max_seqlen_q, int(inp.cu_seqlens_q[-1]),
+                            int(inp.cu_seqlens_k[-1]), max_pages=inp.block_table.shape[1], num_pool_pages=inp.k.shape[0],
+                            dtype=inp.dtype)
+    want = ops.prefill(sh, q, k, v, cq, ck, inp.scale, True, block_table=bt)
+    busy = torch.zeros(1 << 28, device=dev)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(40):
+        busy.add_(1)
+    out, lse, ws = ops.prefill(sh, q, k, v, cq, ck, inp.scale, True, block_table=bt,
+                               stream=side.cuda_stream if handle else side)
+    torch.cuda.synchronize()
+    assert B.pa_check_status(ws) == B.PA_OK
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
