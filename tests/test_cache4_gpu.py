@@ -643,3 +643,24 @@ def test_combine_right_behind_the_device_metadata(d):
         B.pa_decode_combine(sh, plan, meta, o2, l2, ws)
         assert torch.equal(o2[split], out[split]) and torch.equal(l2[split], lse[split]) and (o2[~split] == 7).all()
     assert B.pa_check_status(ws) == B.PA_OK
+
+
+@pytest.mark.parametrize("kv", ["fp4", "bf16", "e4m3"])
+def test_gather_past_the_table_leaves_rows_as_they_were(kv):
+    """Positions 100 .. 299 of a sequence whose block table has 256: the rows of 256 and beyond keep what they held,
+    in the keys and in the values."""
+    d, hk, n = 128, 2, 200
+    sc = (None, None) if kv == "bf16" else (torch.full((hk,), 0.02, device=DEV), torch.full((hk,), 0.03, device=DEV))
+    pools = [ops.kv_pool(5, hk, d, kv, DEV) for _ in range(2)]
+    table = dev(np.array([[4, 1, 0, 3]], np.int32))
+    new = [ops.as_bf16(W.bf16_normal(75, s, (256, hk, d)), DEV) for s in (1, 2)]
+    cu = lambda m: dev(np.array([0, m], np.int32))
+    zero = dev(np.zeros(1, np.int32))
+    ws = ops.append_kv(ops.append_shapes(1, hk, d, 4, 5, 256, kv), *new, cu(256), zero, table, *pools, *sc)
+    whole = ops.gather_kv(ops.append_shapes(1, hk, d, 4, 5, 256, kv), *pools, cu(256), zero, table, *sc, workspace=ws)[:2]
+    assert B.pa_check_status(ws) == B.PA_OK
+    out = [torch.full((n, hk, d), x, dtype=torch.bfloat16, device=DEV) for x in (7.0, 9.0)]
+    ops.gather_kv(ops.append_shapes(1, hk, d, 4, 5, n, kv), *pools, cu(n), dev(np.array([100], np.int32)), table, *sc, *out, ws)
+    assert B.pa_check_status(ws) == B.PA_ERR_DEVICE_BOUNDS
+    for got, want, x in zip(out, whole, (7.0, 9.0)):
+        assert torch.equal(got[:156], want[100:]) and (got[156:] == x).all()
