@@ -1264,10 +1264,9 @@ pa_status pa_get_metadata_device(const pa_decode_shapes* sh, const pa_decode_pla
     while (p2 < plan->total_splits) p2 <<= 1;
     const size_t smem = pa::schedule_smem_bytes(sh->batch, p2);
     if (smem > 227 * 1024) return fail(PA_ERR_UNSUPPORTED, "schedule needs %zu bytes of shared memory", smem);
-    cudaError_t e = pa::launch_schedule_shares(seq_lens_dev, sh->batch, sh->num_kv_heads, sh->max_pages_per_seq,
+    cudaError_t e = pa::launch_schedule(seq_lens_dev, sh->batch, sh->num_kv_heads, sh->max_pages_per_seq,
                                         plan->ctas_per_sm, plan->grid, items_per_share(sh), one_wave_slack(sh),
-                                        sh->forced_splits, p2,
-                                        meta_dev, stream);
+                                        sh->forced_splits, p2, meta_dev, stream);
     if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
     return PA_OK;
 }

@@ -121,8 +121,11 @@ size_t schedule_smem_bytes(int B, int p2cap);
 // block table rows from a flat list of page ids (pa_page_table_from_flat)
 cudaError_t launch_page_table(const int32_t* kv_indices, int64_t num_indices, const int32_t* kv_lens, int B,
                               int max_pages, int32_t* block_table, int* status, cudaStream_t stream);
-cudaError_t launch_schedule(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int forced,
-                            int p2cap, int32_t* meta, cudaStream_t stream);
+// per_share: work items that a CTA's share of the pages is cut into (2; 4-bit
+// pages 1).  slack: pages that a chunk may grow by where that leaves no CTA with
+// a second item (0; 4-bit pages 12).
+cudaError_t launch_schedule(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int per_share,
+                            int slack, int forced, int p2cap, int32_t* meta, cudaStream_t stream);
 
 // Record a message for pa_last_error() on this host thread (pa_api.cu).
 void set_last_error(const char* msg);

@@ -65,9 +65,4 @@ struct NormRopeArgs {
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int head_dim, cudaStream_t stream);
 cudaError_t launch_norm_rope_append(const NormRopeArgs& a, int head_dim, int kv_dtype, cudaStream_t stream);
 
-// launch_schedule with the work items a CTA's share is cut into (2 there), and
-// the pages that a chunk may grow by to leave each CTA one item (0 there)
-cudaError_t launch_schedule_shares(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap,
-                                   int per_share, int slack, int forced, int p2cap, int32_t* meta, cudaStream_t stream);
-
 }  // namespace pa

@@ -10,7 +10,7 @@
 // per-sequence page counts, split counts and split offsets.
 #include <algorithm>
 
-#include "pa_step.h"
+#include "pa_internal.h"
 #include "pa_launch.h"
 
 namespace pa {
@@ -307,13 +307,8 @@ __global__ void __launch_bounds__(kPtThreads) page_table_kernel(const int32_t* _
 
 size_t schedule_smem_bytes(int B, int p2cap) { return (size_t)p2cap * 8 + (size_t)(3 * B + 1) * 4; }
 
-cudaError_t launch_schedule(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int forced,
-                            int p2cap, int32_t* meta, cudaStream_t stream) {
-    return launch_schedule_shares(seq_lens, B, Hk, max_pages, cps, cap, 2, 0, forced, p2cap, meta, stream);
-}
-
-cudaError_t launch_schedule_shares(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap,
-                                   int per_share, int slack, int forced, int p2cap, int32_t* meta, cudaStream_t stream) {
+cudaError_t launch_schedule(const int32_t* seq_lens, int B, int Hk, int max_pages, int cps, int cap, int per_share,
+                            int slack, int forced, int p2cap, int32_t* meta, cudaStream_t stream) {
     const size_t smem = schedule_smem_bytes(B, p2cap);
     // a power of two with one sort key and at most 4 sequences a thread, up to
     // 1024 threads (then at most kMaxPer = 16 keys, p2cap <= 16384); the e4m3
