@@ -10,7 +10,7 @@
 // bytes of codes and one 32-byte sector of scales), and the search for the
 // tokens' sequence and page is paid once for all its heads.
 //
-// Measured: 4-bit rows of 262k tokens, 8 heads of 128, read back in 238 us
+// Measured: 4-bit rows of 302k tokens, 8 heads of 128, read back in 238 us
 // (1.59 GB, 6.7 TB/s, the memory's copy rate); 32768 tokens written in 28.5
 // us (172 MB, 6.0 TB/s); 4096 written and 37k read back, two launches, 38 us
 // (215 MB); 64 written and 64 read back 5.8 us.
@@ -22,7 +22,7 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kHeads = 4;  // heads of a warp that reads back (262k rows 237.4 us, with 2 238.3, with 1 241.0)
+constexpr int kHeads = 4;  // heads of a warp that reads back (302k rows 237.4 us, with 2 238.3, with 1 241.0)
 
 // This thread's token and piece of its rows.  grid: x = groups of tokens, kWarps to a CTA
 template <int D>

@@ -30,11 +30,11 @@
 // output registers.  For 8 heads that costs 8 more MMAs per 16 keys and
 // measured slower (57 sequences of 8192 keys: 98 us a call against 92).
 //
-// Measured: 57 sequences of 8192 keys, 8 KV heads, D = 128 (539 MB), 83 us a
-// call with 4 query heads per KV head (6.5 TB/s, the memory's rate), 88 with 8
-// (issue slots: 250 instructions per 16 keys, 12 warps an SM), 145 with 16
-// (twice the MMAs, 8 warps an SM; 158 as it is planned, 456 whole sequences for
-// 304 CTAs).  Shorter batches also see an item's ends (about 2.5 us), 3 us until
+// Measured: 57 sequences of 8192 keys, 8 KV heads, D = 128 (539 MB), 85 us a
+// call with 4 query heads per KV head (6.3 TB/s, near the memory's rate), 87 with
+// 8 (issue slots: 250 instructions per 16 keys, 12 warps an SM), 162 with 16
+// (twice the MMAs, 8 warps an SM; 138 in two splits each, where the plan has 456
+// whole sequences for 304 CTAs).  Shorter batches also see an item's ends (about 2.5 us), 3 us until
 // the first pages are asked for, and 2 to 3 us of the merge kernel: 64 sequences
 // of up to 4096 keys 37 us a call, where the bytes alone take 23.
 //

@@ -22,9 +22,9 @@
 // One token at a time, 65536 tokens of 8 + 1 heads took 72 us (59 now), of 3 + 3
 // heads of 64 68 us (22.5).
 //
-// Measured: 16384 tokens, 64 + 8 heads of 128 (613 MB), 96.8 us a call, 6.3
-// TB/s; the append form, 8 x 512 tokens, 32 + 8 + 8 heads, 21.3 us with 16-bit
-// pages (103 MB), 22.1 with e4m3 ones, 20.3 with 4-bit ones; one token 3 us, a
+// Measured: 16384 tokens, 64 + 8 heads of 128 (613 MB), 96.7 us a call, 6.3
+// TB/s; the append form, 8 x 512 tokens, 32 + 8 + 8 heads, 21.5 us with 16-bit
+// pages (103 MB), 22.3 with e4m3 ones, 20.5 with 4-bit ones; one token 3 us, a
 // launch.  Against 97 and 22 us, 3 CTAs an SM took 106 and 23.4, 5 104 and 26.7,
 // 2 passes and 6 CTAs 114 and 25.8.  Rows through a ring of bulk copies in
 // shared memory, 3 or 4 deep, were no faster: the loads in flight are not what
@@ -44,9 +44,9 @@ constexpr int kPasses = 4;  // heads of a chunk: rows of a lane whose loads are 
 // Whether a warp goes from one chunk of its tokens to the next (else from some
 // tokens to the next with the same chunk).  With a cache the kinds differ in
 // work, keys and values that are quantised taking longest, and each warp needs
-// its share of all: 8 x 512 tokens, 32 + 8 + 8 heads, 21.8 us against 22.0 with
-// 16-bit pages, 23.3 against 32.6 with e4m3 ones, 21.0 against 31.9 with 4-bit
-// ones.  Without, one chunk keeps its weights: 16384 tokens 97.0 us against 98.9.
+// its share of all: 8 x 512 tokens, 32 + 8 + 8 heads, 21.5 us against 21.7 with
+// 16-bit pages, 22.3 against 31.4 with e4m3 ones, 20.5 against 25.7 with 4-bit
+// ones.  Without, one chunk keeps its weights: 16384 tokens 96.7 us against 98.4.
 constexpr bool walks_chunks(int cache) { return cache >= 0; }
 
 __device__ __forceinline__ float2 unpack16(uint32_t w, bool f16) {
@@ -67,9 +67,9 @@ __device__ __forceinline__ uint32_t pack16(F2 a, bool f16) {
 // Eight e4m3 codes of x / scale, the bits that pa_append_kv stores: fp32
 // quotients (nearest even), then nearest even, saturating.  Away from the ends
 // of fp32 the quotient is the correctly rounded reciprocal's with one residual
-// step, q' = q + (x - q scale) r: the residual is exact for every quotient that
-// does not round to code 0 either way.  It is taken of -q, whose steps leave a
-// zero of x its sign.
+// step, as for 4-bit codes, q' = q + (x - q scale) r: the residual is exact for
+// every quotient that does not round to code 0 either way.  It is taken of -q,
+// whose steps leave a zero of x its sign.
 __device__ __forceinline__ uint2 e4m3x8(uint2 w0, uint2 w1, float scale) {
     const uint32_t u[4] = {w0.x, w0.y, w1.x, w1.y};
     const uint32_t m2 = absmax_bf16x2(absmax_bf16x2(u[0], u[1]), absmax_bf16x2(u[2], u[3]));
