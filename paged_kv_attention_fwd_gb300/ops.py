@@ -47,8 +47,10 @@ def _on(stream):
     """What a call allocates is allocated, and cleared, on the stream it runs on."""
     if stream is None:
         return nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        # 0, 1, 2: CUDA's names of the default streams, which wait for one another
+        stream = torch.cuda.ExternalStream(handle) if handle > 2 else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 

@@ -465,3 +465,20 @@ def test_buffers_that_a_call_makes_belong_to_its_stream(call, handle):
     ws = run()
     torch.cuda.synchronize()
     assert B.pa_check_status(ws) == B.PA_ERR_DEVICE_BOUNDS
+
+
+@pytest.mark.parametrize("stream", [0, 1, 2, "object"])
+def test_streams_by_other_names(stream):
+    """CUDA's handles of the default streams, and any object with a handle: the call makes its buffers and runs."""
+    q, k, _, w, pos, _, table = make(5, 4, 2, 64, "bf16", seed=16)
+    sh = ops.rope_shapes(q, k, rope_dim=64, max_position=4096)
+    want = ops.qk_norm_rope(sh, q, k, w[0], w[1], pos, table)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+
+    class Named:
+        cuda_stream = side.cuda_stream
+
+    got = ops.qk_norm_rope(sh, q, k, w[0], w[1], pos, table, stream=Named() if stream == "object" else stream)
+    torch.cuda.synchronize()
+    assert B.pa_check_status(got[2]) == B.PA_OK and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
