@@ -605,6 +605,162 @@ pa_status pa_norm_rope_append_kv(const pa_rope_shapes* rope_shapes, const pa_app
                                  void* q_out, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ----------------------------------------------------------------- latent cache */
+
+/*
+ * Latent attention, absorbed form.  A token is cached as one row of 576
+ * elements shared by all heads: 512 latent ones c and 64 rotary ones r.  With a
+ * head's key and value up-projections W_uk[h], W_uv[h] (128 x 512 each) its key
+ * is (W_uk[h] c, r) and its value W_uv[h] c, so that with a query (a, b) of 128
+ * + 64 elements
+ *   <a, W_uk[h] c> + <b, r> = <(W_uk[h]^T a, b), (c, r)>     (pa_mla_query)
+ *   sum_j p_j W_uv[h] c_j   = W_uv[h] sum_j p_j c_j          (pa_mla_output)
+ * and attention itself runs on the rows as they are cached (pa_mla_decode).
+ *
+ * A pool is [num_pool_pages, 64, 576], bf16 or fp16, latent elements first;
+ * block tables, lengths and positions are those of the other caches.  Weights,
+ * queries, pool and outputs of a call share one type.  e4m3 and 4-bit latent
+ * pages are refused (PA_ERR_UNSUPPORTED).
+ */
+typedef struct {
+    int32_t total_tokens;  /* T */
+    int32_t num_heads;     /* H */
+    int32_t head_dim;      /* 128: a head's query elements without the rotary ones, and its value elements */
+    int32_t latent_dim;    /* 512 */
+    int32_t rope_dim;      /* 64 */
+    int32_t dtype;         /* PA_KV_BF16 or PA_KV_FP16 */
+    int32_t interleaved;   /* pairs of the rotation: 0 = (i, i + 32), 1 = (2i, 2i + 1) */
+    int32_t max_position;  /* rows of cos_sin */
+    int64_t in_stride, out_stride; /* elements from one token to the next, multiples of 8; heads are contiguous */
+    int64_t w_stride;      /* elements from one head's 128 x 512 matrix to the next, a multiple of 8 */
+} pa_mla_project_shapes;
+
+/*
+ * pa_mla_query -- queries into the latent space, their rotary part turned:
+ *   q_out[t, h, 0:512]   = sum_i q[t, h, i] w_uk[h, i, 0:512]      (i < 128)
+ *   q_out[t, h, 512:576] = q[t, h, 128:192] turned by the token's angles (see
+ *                          pa_qk_norm_rope for the rotation and cos_sin)
+ * with fp32 sums, rounded once.
+ *   q          [T, H, 192], token stride in_stride
+ *   w_uk       [H, 128, 512], head stride w_stride (a slice of a packed weight will do)
+ *   positions  int32 [T]; a negative one marks a padding token, whose output is left
+ *              as it was
+ *   cos_sin    fp32 [max_position, 64], or NULL: the rotary part is copied, and
+ *              positions is not read
+ *   q_out      [T, H, 576], token stride out_stride
+ *   workspace  >= PA_STATUS_BYTES (status word), zero-filled once
+ * A position at or past max_position is recorded as PA_ERR_DEVICE_BOUNDS and its
+ * token left as it was.
+ */
+pa_status pa_mla_query(const pa_mla_project_shapes* shapes, const void* q, const void* w_uk, const int32_t* positions,
+                       const float* cos_sin, void* q_out, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+
+/*
+ * pa_mla_output -- attended latent vectors to the heads' values:
+ *   out[t, h, i] = sum_k w_uv[h, i, k] o[t, h, k]                  (i < 128, k < 512)
+ * with fp32 sums, rounded once.
+ *   o          [T, H, 512], token stride in_stride
+ *   w_uv       [H, 128, 512], head stride w_stride
+ *   out        [T, H, 128], token stride out_stride
+ *   workspace  >= PA_STATUS_BYTES (status word), zero-filled once
+ */
+pa_status pa_mla_output(const pa_mla_project_shapes* shapes, const void* o, const void* w_uv, void* out,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+typedef struct {
+    int32_t batch;             /* B sequences */
+    int32_t latent_dim;        /* 512 */
+    int32_t rope_dim;          /* 64 */
+    int32_t page_size;         /* must be 64 */
+    int32_t max_pages_per_seq; /* block_table row stride */
+    int32_t num_pool_pages;
+    int32_t total_new;         /* rows of kv_new or of the outputs, padding included */
+    int32_t dtype;             /* PA_KV_BF16 or PA_KV_FP16 */
+    int32_t norm;              /* append: 1 = RMS norm of the latent part first, 0 = none */
+    int32_t interleaved;       /* append: pairs of the rotation, 0 = (i, i + 32), 1 = (2i, 2i + 1) */
+    int32_t max_position;      /* append: rows of cos_sin */
+    float eps;                 /* append: of the norm */
+    int64_t kv_stride;         /* append: elements from one row of kv_new to the next, a multiple of 8 */
+} pa_mla_cache_shapes;
+
+/*
+ * pa_mla_append_kv -- new tokens' rows into their pages.  Row i of sequence b
+ * goes to position start_pos[b] + i (see pa_append_kv), its latent part as
+ *   c = x / sqrt(mean(x^2) + eps) * weight        over the 512 elements (norm 1; else copied)
+ * and its rotary part turned; fp32 inside, rounded once.
+ *   kv_new     [total_new, 576], row stride kv_stride (a slice of a projection will do)
+ *   weight     [512], or NULL for ones
+ *   positions  int32 [total_new], or NULL: the position in the cache.  A negative one
+ *              marks a padding token.  Not read where cos_sin is NULL
+ *   cos_sin    fp32 [max_position, 64], or NULL: the rotary part is copied
+ *   cu_seqlens_new, start_pos, block_table   as for pa_append_kv
+ *   workspace  >= PA_STATUS_BYTES (status word), zero-filled once
+ * Rows past cu_seqlens_new[B] (or before cu_seqlens_new[0]) are padding; nothing of
+ * a padding token is written, whatever it holds.  A token whose place in the cache
+ * or position in cos_sin is out of range is skipped and recorded as
+ * PA_ERR_DEVICE_BOUNDS.
+ */
+pa_status pa_mla_append_kv(const pa_mla_cache_shapes* shapes, const void* kv_new, const void* weight,
+                           const int32_t* positions, const float* cos_sin, const int32_t* cu_seqlens_new,
+                           const int32_t* start_pos, const int32_t* block_table, void* pool, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * pa_mla_gather_kv -- rows of a latent cache back, bit for bit, as the ragged
+ * tensors that a prefill over expanded keys and values starts from (the latent
+ * rows times the up-projections give its k and v, the rotary rows are its
+ * k_rope).  Row i of sequence b is position start_pos[b] + i.
+ *   latent_out  [total_new, 512];  rope_out  [total_new, 1, 64]
+ *   cu_seqlens, start_pos, block_table, workspace, rows outside [cu_seqlens[0],
+ *   cu_seqlens[B]) and positions out of range as for pa_gather_kv
+ */
+pa_status pa_mla_gather_kv(const pa_mla_cache_shapes* shapes, const void* pool, const int32_t* cu_seqlens,
+                           const int32_t* start_pos, const int32_t* block_table, void* latent_out, void* rope_out,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+typedef struct {
+    int32_t batch;             /* B */
+    int32_t num_q_heads;       /* H */
+    int32_t q_len;             /* tokens per sequence, the last of its keys among them (1; more to verify drafts) */
+    int32_t latent_dim;        /* 512 */
+    int32_t rope_dim;          /* 64 */
+    int32_t page_size;         /* must be 64 */
+    int32_t max_pages_per_seq; /* block_table row stride */
+    int32_t num_pool_pages;
+    int32_t num_sms;           /* SMs of the device (cudaDevAttrMultiProcessorCount) */
+    int32_t dtype;             /* PA_KV_BF16 or PA_KV_FP16 */
+} pa_mla_decode_shapes;
+
+/*
+ * pa_mla_decode -- attention of the last q_len tokens of every sequence over its
+ * latent rows, long sequences split over the SMs and joined by a log-sum-exp
+ * merge:
+ *   s_j = scale <q[b q_len + i, h], row_j>   (576 elements),  j < seq_lens[b] - (q_len - 1 - i)
+ *   out = sum_j softmax_j(s) row_j[0:512],   lse = ln sum_j exp(s_j)
+ * A token that sees no key has out = 0 and lse = -inf.
+ *   q          [B q_len, H, 576]    (pa_mla_query's output)
+ *   pool       [num_pool_pages, 64, 576]; rows at or past seq_lens[b] and table entries
+ *              past ceil(seq_lens[b] / 64) are never used, whatever they hold
+ *   seq_lens   int32 [B], keys per sequence, the q_len new ones included
+ *   scale      softmax scale (that of the expanded form, e.g. 1 / sqrt(192))
+ *   out        [B q_len, H, 512];  lse  fp32 [B q_len, H] or NULL
+ *   workspace  >= pa_mla_decode_workspace_size(shapes), the status word zero-filled
+ *              once; not used by two calls that may overlap
+ * There is no plan: lengths are read on the device only, where the work is dealt
+ * to the SMs, so a captured call replays with new lengths, tables and queries.
+ * A length below 0 counts as 0, one past max_pages_per_seq * 64 as that many keys,
+ * a page id outside the pool as page 0; each is recorded as PA_ERR_DEVICE_BOUNDS.
+ * With fp16 and bf16 rows alike the softmax weights are rounded to the rows' type
+ * before they are multiplied; sums are fp32.
+ */
+pa_status pa_mla_decode(const pa_mla_decode_shapes* shapes, const void* q, const void* pool, const int32_t* block_table,
+                        const int32_t* seq_lens, float scale, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of pa_mla_decode; they depend on num_sms alone. */
+size_t pa_mla_decode_workspace_size(const pa_mla_decode_shapes* shapes);
+
 /* ----------------------------------------------------------------- status */
 
 /*

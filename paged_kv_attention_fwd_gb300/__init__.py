@@ -17,6 +17,8 @@ from .binding import (  # noqa: F401  (the C-ABI calls, constants and structs)
     pa_prefill, pa_prefill_workspace_size, pa_prefill_mla_fp8, pa_prefill_mla_rope_fp8,
     pa_prefill_mla_rope_fp8_workspace_size, pa_get_mixed_plan, pa_mixed, pa_append_kv,
     pa_page_slab_bytes, pa_gather_kv, pa_rope_shapes, pa_qk_norm_rope, pa_norm_rope_append_kv,
+    pa_mla_project_shapes, pa_mla_cache_shapes, pa_mla_decode_shapes, pa_mla_query, pa_mla_output, pa_mla_append_kv,
+    pa_mla_gather_kv, pa_mla_decode, pa_mla_decode_workspace_size,
 )
 
 __version__ = "0.1.0"

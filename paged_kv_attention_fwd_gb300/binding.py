@@ -75,6 +75,25 @@ class pa_rope_shapes(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride", "k_out_stride")])
 
 
+class pa_mla_project_shapes(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("total_tokens", "num_heads", "head_dim", "latent_dim", "rope_dim", "dtype",
+                                               "interleaved", "max_position")]
+                + [(n, ctypes.c_int64) for n in ("in_stride", "out_stride", "w_stride")])
+
+
+class pa_mla_cache_shapes(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "latent_dim", "rope_dim", "page_size", "max_pages_per_seq",
+                                               "num_pool_pages", "total_new", "dtype", "norm", "interleaved",
+                                               "max_position")]
+                + [("eps", ctypes.c_float), ("kv_stride", ctypes.c_int64)])
+
+
+class pa_mla_decode_shapes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_q_heads", "q_len", "latent_dim", "rope_dim", "page_size", "max_pages_per_seq", "num_pool_pages",
+        "num_sms", "dtype")]
+
+
 _lib = None
 _P = ctypes.c_void_p
 
@@ -132,6 +151,15 @@ def lib() -> ctypes.CDLL:
         L.pa_norm_rope_append_kv.argtypes = [ctypes.POINTER(pa_rope_shapes), ctypes.POINTER(pa_append_shapes), _P, _P,
                                              _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]
         L.pa_norm_rope_append_kv.restype = ctypes.c_int
+        L.pa_mla_query.argtypes = [ctypes.POINTER(pa_mla_project_shapes), _P, _P, _P, _P, _P, _P, sz, _P]
+        L.pa_mla_output.argtypes = [ctypes.POINTER(pa_mla_project_shapes), _P, _P, _P, _P, sz, _P]
+        L.pa_mla_append_kv.argtypes = [ctypes.POINTER(pa_mla_cache_shapes), _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]
+        L.pa_mla_gather_kv.argtypes = [ctypes.POINTER(pa_mla_cache_shapes), _P, _P, _P, _P, _P, _P, _P, sz, _P]
+        L.pa_mla_decode.argtypes = [ctypes.POINTER(pa_mla_decode_shapes), _P, _P, _P, _P, f32, _P, _P, _P, sz, _P]
+        L.pa_mla_decode_workspace_size.argtypes = [ctypes.POINTER(pa_mla_decode_shapes)]
+        L.pa_mla_decode_workspace_size.restype = sz
+        for f in ("pa_mla_query", "pa_mla_output", "pa_mla_append_kv", "pa_mla_gather_kv", "pa_mla_decode"):
+            getattr(L, f).restype = ctypes.c_int
         L.pa_prefill_workspace_size.argtypes = [ctypes.POINTER(pa_prefill_shapes)]
         L.pa_prefill_workspace_size.restype = ctypes.c_size_t
         L.pa_check_status.argtypes = [_P, _P]
@@ -390,6 +418,53 @@ def pa_norm_rope_append_kv(rope_shapes: pa_rope_shapes, append_shapes: pa_append
                                         _ptr(cu_seqlens_new), _ptr(start_pos), _ptr(block_table), _ptr(q_out),
                                         _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(workspace),
                                         int(workspace_bytes), _stream(stream)))
+
+
+def pa_mla_query(shapes: pa_mla_project_shapes, q, w_uk, positions, cos_sin, q_out, workspace,
+                 workspace_bytes: Optional[int] = None, stream=None) -> None:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_mla_query(ctypes.byref(shapes), _ptr(q), _ptr(w_uk), _ptr(positions), _ptr(cos_sin), _ptr(q_out),
+                              _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def pa_mla_output(shapes: pa_mla_project_shapes, o, w_uv, out, workspace, workspace_bytes: Optional[int] = None,
+                  stream=None) -> None:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_mla_output(ctypes.byref(shapes), _ptr(o), _ptr(w_uv), _ptr(out), _ptr(workspace),
+                               int(workspace_bytes), _stream(stream)))
+
+
+def pa_mla_append_kv(shapes: pa_mla_cache_shapes, kv_new, weight, positions, cos_sin, cu_seqlens_new, start_pos,
+                     block_table, pool, workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_mla_append_kv(ctypes.byref(shapes), _ptr(kv_new), _ptr(weight), _ptr(positions), _ptr(cos_sin),
+                                  _ptr(cu_seqlens_new), _ptr(start_pos), _ptr(block_table), _ptr(pool), _ptr(workspace),
+                                  int(workspace_bytes), _stream(stream)))
+
+
+def pa_mla_gather_kv(shapes: pa_mla_cache_shapes, pool, cu_seqlens, start_pos, block_table, latent_out, rope_out,
+                     workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_mla_gather_kv(ctypes.byref(shapes), _ptr(pool), _ptr(cu_seqlens), _ptr(start_pos), _ptr(block_table),
+                                  _ptr(latent_out), _ptr(rope_out), _ptr(workspace), int(workspace_bytes),
+                                  _stream(stream)))
+
+
+def pa_mla_decode(shapes: pa_mla_decode_shapes, q, pool, block_table, seq_lens, scale: float, out, lse, workspace,
+                  workspace_bytes: Optional[int] = None, stream=None) -> None:
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().pa_mla_decode(ctypes.byref(shapes), _ptr(q), _ptr(pool), _ptr(block_table), _ptr(seq_lens),
+                               float(scale), _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes),
+                               _stream(stream)))
+
+
+def pa_mla_decode_workspace_size(shapes: pa_mla_decode_shapes) -> int:
+    return int(lib().pa_mla_decode_workspace_size(ctypes.byref(shapes)))
 
 
 def pa_prefill_workspace_size(shapes: pa_prefill_shapes) -> int:

@@ -17,9 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 SOURCES = ["pa_api.cu", "decode.cu", "prefill.cu", "prefill_pair.cu", "append.cu", "schedule.cu",
-           "cache4.cu", "norm_rope.cu", "decode_fp4.cu"]
+           "cache4.cu", "norm_rope.cu", "decode_fp4.cu", "mla_api.cu", "mla_cache.cu", "mla_project.cu", "mla_decode.cu"]
 HEADERS = ["pa_ptx.cuh", "pa_internal.h", "pa_launch.h", "prefill_common.cuh", "pa_step.h", "f32x2.cuh", "fp4.cuh",
-           "cache4.cuh", "token_place.cuh"]
+           "cache4.cuh", "token_place.cuh", "pa_mla.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

@@ -13,6 +13,7 @@
 #include <string>
 #include <vector>
 
+#include "pa_mla.h"
 #include "pa_step.h"
 
 namespace {
@@ -188,6 +189,23 @@ int one_wave_slack(const pa_decode_shapes* sh) {
 
 namespace pa {
 void set_last_error(const char* msg) { g_last_error = msg; }
+
+pa_status host_fail(pa_status st, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return st;
+}
+
+pa_status host_map_16(bool f16, CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides_bytes, const uint32_t* box) {
+    return make_map_16(f16, map, base, rank, dims, strides_bytes, box);
+}
+
+uint64_t host_wait_limit_ns() { return g_wait_limit_ns.load(); }
 }  // namespace pa
 
 extern "C" {

@@ -361,3 +361,80 @@ def norm_rope_append_kv(sh: B.pa_rope_shapes, append: B.pa_append_shapes, q, k, 
     B.pa_norm_rope_append_kv(sh, append, q, k, v, q_weight, k_weight, positions, cos_sin, cu_seqlens_new, start_pos,
                              block_table, q_out, k_pool, v_pool, k_scale, v_scale, workspace, stream=stream)
     return q_out, workspace
+
+
+# ------------------------------------------------------------- latent cache
+
+MLA_HEAD, MLA_LATENT, MLA_ROPE = 128, 512, 64
+MLA_ROW = MLA_LATENT + MLA_ROPE
+_MLA_DTYPES = {torch.bfloat16: B.PA_KV_BF16, torch.float16: B.PA_KV_FP16}
+
+
+def mla_pool(num_pages: int, dtype: str = "bf16", device="cuda") -> torch.Tensor:
+    """A zero-filled pool of latent pages: [num_pages, 64, 576]."""
+    return torch.zeros((num_pages, 64, MLA_ROW), dtype=_POOL_TORCH[dtype], device=device)
+
+
+def _check_heads(name: str, x, shape, like):
+    """[T, H, D] with contiguous heads, of `like`'s type and device."""
+    t, h, d = shape
+    if (x.dim() != 3 or tuple(x.shape) != shape or x.dtype != like.dtype or x.device != like.device
+            or (d > 1 and x.stride(2) != 1) or (h > 1 and x.stride(1) != d)):
+        _refuse(name, x, f"[{t}, {h}, {d}] of {like.dtype} on {like.device}, heads contiguous")
+
+
+def _check_head_matrices(name: str, w, heads: int, like):
+    if (w.dim() != 3 or tuple(w.shape) != (heads, MLA_HEAD, MLA_LATENT) or w.dtype != like.dtype
+            or w.device != like.device or w.stride(2) != 1 or w.stride(1) != MLA_LATENT):
+        _refuse(name, w, f"[{heads}, {MLA_HEAD}, {MLA_LATENT}] of {like.dtype} on {like.device}, matrices contiguous")
+
+
+def _mla_project_shapes(x, w, in_row: int, out_row: int, out, **more) -> B.pa_mla_project_shapes:
+    if x.dtype not in _MLA_DTYPES:
+        _refuse("input", x, "bf16 or fp16")
+    if x.dim() != 3:
+        _refuse("input", x, f"[tokens, heads, {in_row}]")
+    t, h, _ = x.shape
+    _check_heads("input", x, (t, h, in_row), x)
+    _check_head_matrices("weights", w, h, x)
+    if out is not None:
+        _check_heads("output", out, (t, h, out_row), x)
+
+    def step(y, row):  # a single token's stride is never used
+        return h * row if y is None or t <= 1 else y.stride(0)
+
+    return B.pa_mla_project_shapes(total_tokens=t, num_heads=h, head_dim=MLA_HEAD, latent_dim=MLA_LATENT,
+                                   rope_dim=MLA_ROPE, dtype=_MLA_DTYPES[x.dtype], in_stride=step(x, in_row),
+                                   out_stride=step(out, out_row),
+                                   w_stride=w.stride(0) if h > 1 else MLA_HEAD * MLA_LATENT, **more)
+
+
+def mla_query_shapes(q, w_uk, max_position: int = 0, interleaved: bool = False, out=None) -> B.pa_mla_project_shapes:
+    """Shapes of pa_mla_query for q [T, H, 192] and w_uk [H, 128, 512] (slices
+    of packed tensors keep their strides); an output not given is contiguous."""
+    return _mla_project_shapes(q, w_uk, MLA_HEAD + MLA_ROPE, MLA_ROW, out, max_position=max_position,
+                               interleaved=int(interleaved))
+
+
+def mla_output_shapes(o, w_uv, out=None) -> B.pa_mla_project_shapes:
+    """Shapes of pa_mla_output for o [T, H, 512] and w_uv [H, 128, 512]."""
+    return _mla_project_shapes(o, w_uv, MLA_LATENT, MLA_HEAD, out)
+
+
+def mla_cache_shapes(batch: int, max_pages: int, num_pool_pages: int, total_new: int, dtype: str = "bf16", kv=None,
+                     max_position: int = 0, interleaved: bool = False, norm: bool = True,
+                     eps: float = 1e-6) -> B.pa_mla_cache_shapes:
+    """Shapes of pa_mla_append_kv (rows of `kv`, whose stride they take) and pa_mla_gather_kv."""
+    stride = MLA_ROW if kv is None or kv.shape[0] <= 1 else kv.stride(0)
+    return B.pa_mla_cache_shapes(batch=batch, latent_dim=MLA_LATENT, rope_dim=MLA_ROPE, page_size=64,
+                                 max_pages_per_seq=max_pages, num_pool_pages=num_pool_pages, total_new=total_new,
+                                 dtype=KV_DTYPES[dtype], norm=int(norm), interleaved=int(interleaved),
+                                 max_position=max_position, eps=eps, kv_stride=stride)
+
+
+def mla_decode_shapes(batch: int, num_q_heads: int, max_pages: int, num_pool_pages: int, q_len: int = 1,
+                      dtype: str = "bf16", device="cuda", sms: Optional[int] = None) -> B.pa_mla_decode_shapes:
+    return B.pa_mla_decode_shapes(batch=batch, num_q_heads=num_q_heads, q_len=q_len, latent_dim=MLA_LATENT,
+                                  rope_dim=MLA_ROPE, page_size=64, max_pages_per_seq=max_pages,
+                                  num_pool_pages=num_pool_pages, num_sms=sms if sms is not None else num_sms(device),
+                                  dtype=KV_DTYPES[dtype])
