@@ -468,29 +468,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint8_t* p_row = sm + kPOff + kh * kChunkBytes + row * 128;
                     uint64_t acc[2] = {f2_pack(0u, 0u), f2_pack(0u, 0u)};
                     float rsum = 0.f;
-                    const uint64_t sc2 = f2_pack(__float_as_uint(sl2), __float_as_uint(sl2));
-                    const uint64_t nm2 = f2_pack(__float_as_uint(-m_run), __float_as_uint(-m_run));
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        uint32_t pw[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int e = u * 8 + 2 * k;
-                            float p0, p1;
-                            if (fast) {
-                                float x0, x1;
-                                f2_unpack(f2_fma(f2_pack(r[e], r[e + 1]), sc2, nm2), x0, x1);
-                                p0 = ex2(x0);
-                                p1 = ex2(x1);
-                                acc[k & 1] = f2_add(acc[k & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
-                            } else {
-                                p0 = none || e >= vis ? 0.f : ex2(__uint_as_float(r[e]) * sl2 - m_run);
-                                p1 = none || e + 1 >= vis ? 0.f : ex2(__uint_as_float(r[e + 1]) * sl2 - m_run);
-                                rsum += p0 + p1;
-                            }
-                            pw[k] = pack16x2(p0, p1, kF16);
-                        }
+                    auto store8 = [&](int u, const uint32_t (&pw)[4]) {
                         *reinterpret_cast<uint4*>(p_row + ((u ^ (row & 7)) << 4)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+                    };
+                    if (fast) {
+                        const uint64_t sc2 = f2_pack(__float_as_uint(sl2), __float_as_uint(sl2));
+                        const uint64_t nm2 = f2_pack(__float_as_uint(-m_run), __float_as_uint(-m_run));
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            uint32_t pw[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float x0, x1;
+                                f2_unpack(f2_fma(f2_pack(r[u * 8 + 2 * k], r[u * 8 + 2 * k + 1]), sc2, nm2), x0, x1);
+                                const float p0 = ex2(x0), p1 = ex2(x1);
+                                acc[k & 1] = f2_add(acc[k & 1], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+                                pw[k] = pack16x2(p0, p1, kF16);
+                            }
+                            store8(u, pw);
+                        }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            uint32_t pw[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int e = u * 8 + 2 * k;
+                                const float p0 = none || e >= vis ? 0.f : ex2(__uint_as_float(r[e]) * sl2 - m_run);
+                                const float p1 = none || e + 1 >= vis ? 0.f : ex2(__uint_as_float(r[e + 1]) * sl2 - m_run);
+                                rsum += p0 + p1;
+                                pw[k] = pack16x2(p0, p1, kF16);
+                            }
+                            store8(u, pw);
+                        }
                     }
                     float a0, a1, b0, b1;
                     f2_unpack(acc[0], a0, a1);
@@ -516,10 +526,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             }
                     }
                 }
-                fence_proxy_async_cluster();
+                // P lies in this CTA's shared memory and is read there by its own half of the pair's MMA: once the proxy
+                // fence is through, the arrival itself has nothing left to order (a release at cluster scope takes 700
+                // cycles, and the fence over the cluster 900).  Rows zeroed in the peer are released as a whole.
+                const bool zeroed = leader && live_keys < 128;
+                if (zeroed) fence_proxy_async_cluster();
+                else fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cl(lead(B_PF));
+                if (lane == 0) {
+                    if (zeroed) mbar_arrive_cl(lead(B_PF));
+                    else mbar_signal_cl(lead(B_PF));
+                }
             }
             if (bad) break;
             // ---- output of the piece
