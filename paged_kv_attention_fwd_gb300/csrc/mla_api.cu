@@ -51,12 +51,13 @@ pa_status check_stride(int64_t stride, int64_t least, const char* name) {
 
 // ------------------------------------------------------------ attention
 
-// Pairs of CTAs that a device of num_sms can hold, and so the ranges of work.
-int decode_pairs(const pa_mla_decode_shapes* sh) { return std::max(sh->num_sms / 2, 1); }
+// CTAs of a launch that may leave parts of items: the SMs' (a launch of more has one range a block, and no parts).
+int decode_ctas(const pa_mla_decode_shapes* sh) { return sh->num_sms; }
 
 size_t merges_offset() { return PA_STATUS_BYTES; }
-size_t lse_offset(int pairs) { return merges_offset() + up256((size_t)pairs * sizeof(pa::MlaMerge)); }
-size_t part_offset(int pairs) { return lse_offset(pairs) + (size_t)2 * pairs * pa::kMlaBlockRows * 4; }
+size_t ref_offset(int ctas) { return merges_offset() + up256((size_t)ctas * sizeof(pa::MlaMerge)); }
+size_t sum_offset(int ctas) { return ref_offset(ctas) + (size_t)2 * ctas * pa::kMlaBlockRows * 4; }
+size_t part_offset(int ctas) { return sum_offset(ctas) + (size_t)2 * ctas * 4 * pa::kMlaBlockRows * 4; }
 
 pa_status check_decode_shapes(const pa_mla_decode_shapes* sh) {
     if (!sh) return host_fail(PA_ERR_INVALID_ARG, "shapes must not be NULL");
@@ -161,8 +162,8 @@ extern "C" {
 
 size_t pa_mla_decode_workspace_size(const pa_mla_decode_shapes* sh) {
     if (!sh || sh->num_sms <= 0) return PA_STATUS_BYTES;
-    const int pairs = decode_pairs(sh);
-    return part_offset(pairs) + (size_t)2 * pairs * pa::kMlaBlockRows * pa::kMlaLatent * 4;
+    const int ctas = decode_ctas(sh);
+    return part_offset(ctas) + (size_t)2 * ctas * pa::kMlaBlockRows * pa::kMlaLatent * 4;
 }
 
 pa_status pa_mla_decode(const pa_mla_decode_shapes* sh, const void* q, const void* pool, const int32_t* block_table,
@@ -180,14 +181,15 @@ pa_status pa_mla_decode(const pa_mla_decode_shapes* sh, const void* q, const voi
     pa::MlaDecodeArgs a;
     std::memset(&a, 0, sizeof a);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int pairs = decode_pairs(sh);
+    const int ctas = decode_ctas(sh);
     a.block_table = block_table;
     a.seq_lens = seq_lens;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
     a.merges = reinterpret_cast<pa::MlaMerge*>(ws + merges_offset());
-    a.lse_part = reinterpret_cast<float*>(ws + lse_offset(pairs));
-    a.o_part = reinterpret_cast<float*>(ws + part_offset(pairs));
+    a.ref_part = reinterpret_cast<float*>(ws + ref_offset(ctas));
+    a.sum_part = reinterpret_cast<float*>(ws + sum_offset(ctas));
+    a.o_part = reinterpret_cast<float*>(ws + part_offset(ctas));
     a.status = static_cast<int*>(workspace);
     a.batch = sh->batch;
     a.q_len = sh->q_len;
@@ -202,11 +204,11 @@ pa_status pa_mla_decode(const pa_mla_decode_shapes* sh, const void* q, const voi
     const uint64_t stride[1] = {pa::kMlaRow * 2};
     const uint64_t qd[2] = {pa::kMlaRow, (uint64_t)sh->batch * a.rows};
     const uint64_t kd[2] = {pa::kMlaRow, (uint64_t)sh->num_pool_pages * pa::kPage};
-    const uint32_t box[2] = {64, 64};
-    st = pa::host_map_16(a.f16, &mq, q, 2, qd, stride, box);
-    if (st == PA_OK) st = pa::host_map_16(a.f16, &mkv, pool, 2, kd, stride, box);
+    const uint32_t qbox[2] = {64, (uint32_t)pa::mla_block_rows(a.rows)}, kbox[2] = {64, pa::kPage};
+    st = pa::host_map_16(a.f16, &mq, q, 2, qd, stride, qbox);
+    if (st == PA_OK) st = pa::host_map_16(a.f16, &mkv, pool, 2, kd, stride, kbox);
     if (st != PA_OK) return st;
-    return launched(pa::launch_mla_decode(a, pairs, &mq, &mkv, stream), "latent decode launch");
+    return launched(pa::launch_mla_decode(a, sh->num_sms, &mq, &mkv, stream), "latent decode launch");
 }
 
 pa_status pa_mla_append_kv(const pa_mla_cache_shapes* sh, const void* kv_new, const void* weight,

@@ -17,27 +17,29 @@ pa_status host_map_16(bool f16, CUtensorMap* map, const void* base, int rank, co
 uint64_t host_wait_limit_ns();
 
 // Attention over latent pages (mla_decode.cu)
-constexpr int kMlaBlockRows = 128;  // query rows (token, head) of a work item: 64 in each CTA of a pair
+constexpr int kMlaBlockRows = 64;  // query rows (token, head) of a block at most, and those of a sequence's blocks
+constexpr int mla_block_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : kMlaBlockRows; }
 struct MlaMerge {
-    int32_t b, blk, pieces, first;  // pieces of a split item, the first of them in the pair `first` (0: none)
+    int32_t b, blk, pieces, first;  // pieces of a split item, the first of them in range `first` (0: none)
 };
 struct MlaDecodeArgs {
     const int32_t* block_table;
     const int32_t* seq_lens;
     uint16_t* out;     // [batch * rows, 512]
     float* lse;        // [batch * rows] or nullptr
-    float* o_part;     // fp32 [2 * pairs, 128, 512]
-    float* lse_part;   // fp32 [2 * pairs, 128]
-    MlaMerge* merges;  // [pairs]
+    float* o_part;     // fp32 [2 * ranges * blocks, 64, 512]
+    float* ref_part;   // fp32 [2 * ranges * blocks, 64]
+    float* sum_part;   // fp32 [2 * ranges * blocks, 4, 64]
+    MlaMerge* merges;  // [ranges * blocks]
     int* status;
     int32_t batch, rows, q_len, num_heads, max_pages, num_pool_pages;
     int32_t f16;
-    int32_t pairs;  // set by the launch
+    int32_t ranges;  // set by the launch
     float scale_log2;
     uint64_t wait_ns;
 };
-// map_q: [batch * rows, 576], map_kv: [pages * 64, 576], boxes of 64 rows x 64 elements
-cudaError_t launch_mla_decode(MlaDecodeArgs a, int max_pairs, const CUtensorMap* map_q, const CUtensorMap* map_kv,
+// map_q: [batch * rows, 576], boxes of 64 elements of mla_block_rows rows; map_kv: [pages * 64, 576], of 64 rows
+cudaError_t launch_mla_decode(MlaDecodeArgs a, int sms, const CUtensorMap* map_q, const CUtensorMap* map_kv,
                               cudaStream_t stream);
 
 // Rows into and out of latent pages (mla_cache.cu)
