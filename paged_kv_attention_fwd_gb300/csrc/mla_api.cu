@@ -72,6 +72,8 @@ pa_status check_decode_shapes(const pa_mla_decode_shapes* sh) {
         return host_fail(PA_ERR_INVALID_ARG, "num_sms must be in [1, 4096] (got %d)", sh->num_sms);
     pa_status st = check_row(sh->latent_dim, sh->rope_dim, sh->dtype);
     if (st == PA_OK) st = check_pages(sh->page_size, sh->max_pages_per_seq, sh->num_pool_pages);
+    if (st == PA_OK && (int64_t)sh->batch * ((int64_t)sh->max_pages_per_seq + 16) >= ((int64_t)1 << 31))
+        return host_fail(PA_ERR_UNSUPPORTED, "batch * (max_pages_per_seq + 16) must be below 2^31");
     if (st == PA_OK && (int64_t)sh->num_pool_pages * pa::kPage >= ((int64_t)1 << 31))
         return host_fail(PA_ERR_UNSUPPORTED, "pool rows (pages * 64) must be below 2^31");
     return st;
@@ -182,6 +184,7 @@ pa_status pa_mla_decode(const pa_mla_decode_shapes* sh, const void* q, const voi
     std::memset(&a, 0, sizeof a);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int ctas = decode_ctas(sh);
+    a.pool = static_cast<const uint8_t*>(pool);
     a.block_table = block_table;
     a.seq_lens = seq_lens;
     a.out = static_cast<uint16_t*>(out);
@@ -200,15 +203,17 @@ pa_status pa_mla_decode(const pa_mla_decode_shapes* sh, const void* q, const voi
     a.f16 = sh->dtype == PA_KV_FP16;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.wait_ns = pa::host_wait_limit_ns();
-    CUtensorMap mq, mkv;
-    const uint64_t stride[1] = {pa::kMlaRow * 2};
-    const uint64_t qd[2] = {pa::kMlaRow, (uint64_t)sh->batch * a.rows};
-    const uint64_t kd[2] = {pa::kMlaRow, (uint64_t)sh->num_pool_pages * pa::kPage};
-    const uint32_t qbox[2] = {64, (uint32_t)pa::mla_block_rows(a.rows)}, kbox[2] = {64, pa::kPage};
-    st = pa::host_map_16(a.f16, &mq, q, 2, qd, stride, qbox);
-    if (st == PA_OK) st = pa::host_map_16(a.f16, &mkv, pool, 2, kd, stride, kbox);
+    CUtensorMap maps[3];
+    const uint64_t strides[2] = {pa::kMlaRow * 2, 128};
+    const uint64_t qd[3] = {64, (uint64_t)sh->batch * a.rows, pa::kMlaRow / 64};
+    const uint64_t kd[3] = {64, (uint64_t)sh->num_pool_pages * pa::kPage, pa::kMlaRow / 64};
+    const uint32_t qbox[3] = {64, (uint32_t)pa::mla_block_rows(a.rows), pa::kMlaRow / 64};
+    const uint32_t latent[3] = {64, pa::kPage, 2}, rope[3] = {64, pa::kPage, 1};
+    st = pa::host_map_16(a.f16, &maps[0], q, 3, qd, strides, qbox);
+    if (st == PA_OK) st = pa::host_map_16(a.f16, &maps[1], pool, 3, kd, strides, latent);
+    if (st == PA_OK) st = pa::host_map_16(a.f16, &maps[2], pool, 3, kd, strides, rope);
     if (st != PA_OK) return st;
-    return launched(pa::launch_mla_decode(a, sh->num_sms, &mq, &mkv, stream), "latent decode launch");
+    return launched(pa::launch_mla_decode(a, sh->num_sms, maps, stream), "latent decode launch");
 }
 
 pa_status pa_mla_append_kv(const pa_mla_cache_shapes* sh, const void* kv_new, const void* weight,

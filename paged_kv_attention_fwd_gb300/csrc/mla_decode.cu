@@ -22,8 +22,9 @@
 //   warp 0     producer: queries, and pages through a ring (128 latent elements
 //              of a page a stage, the 64 rotary ones in a ring of their own)
 //   warp 1     the MMAs of S          warp 10   the MMAs of O
-//   warps 2-9  softmax: a key a thread (16 of a warp's lanes: the layout of M =
-//              64), half of the columns; P to shared memory
+//   warps 2-9  softmax: 16 keys a warp (M = 64 fills as many lanes of four
+//              groups of 32), half of the columns, a quarter a lane; P to shared
+//              memory
 //
 // The softmax's reference is not each key's running maximum but one value a
 // column, which changes only when a score exceeds it by more than 2^8.  Whether
@@ -49,13 +50,15 @@ constexpr int kBox = 64 * 128;         // a chunk of a page's rows
 constexpr int kPageStages = 4;         // latent stages of a page, two chunks each
 constexpr int kRopeStages = 2, kMaxStages = 11;
 constexpr int kSoftmaxWarps = 8;
+constexpr int kListed = 16;  // sequences of a CTA's range whose pieces are found at its start
 constexpr int kThreads = 96 + 32 * kSoftmaxWarps;
-constexpr long long kFixed = 4;     // what an item costs besides its pages, in pages
-constexpr long long kMinShare = 6;  // a range is at least this long
+constexpr int kFixed = 4;     // what an item costs besides its pages, in pages
+constexpr int kMinShare = 6;  // a range is at least this long
 
 template <int N>
 struct Layout {
     static constexpr int kHalf = N / 2;           // columns of a softmax warp
+    static constexpr int kQuarter = N / 4;        // and of a lane
     static constexpr int kQChunk = N * 128;       // 64 elements of the queries
     static constexpr int kPBuffers = N > 32 ? 1 : 2;  // side by side in the 128-byte rows of P, a key each
     static constexpr int kStages = N > 32 ? 8 : N > 16 ? 10 : 11;  // latent stages that shared memory has room for
@@ -85,7 +88,7 @@ enum : int {
 // A stretch of pages [lo, hi) of sequence b that a CTA takes.
 struct Piece {
     int b, lo, hi, pages, len;
-    long long at;  // where the item's cost starts
+    int at;  // where the item's cost starts
 };
 
 __device__ __forceinline__ int clamped_len(const MlaDecodeArgs& a, int b, bool report) {
@@ -96,23 +99,24 @@ __device__ __forceinline__ int clamped_len(const MlaDecodeArgs& a, int b, bool r
     return len < 0 ? 0 : (int)most;
 }
 
+// The pieces of a range [from, to) of costs, from sequence b on, whose cost starts at `at`.
 struct Walk {
-    long long from, to, at;
+    int from, to, at;
     int b;
+    __device__ __forceinline__ bool take(const MlaDecodeArgs& a, int len, Piece& p) {
+        p.b = b++;
+        p.at = at;
+        p.len = len;
+        p.pages = (len + kPage - 1) / kPage;
+        const int t0 = at + kFixed;
+        p.lo = min(p.pages, max(0, from - t0));
+        p.hi = min(p.pages, max(0, to - t0));
+        at = t0 + p.pages;
+        return p.pages == 0 ? p.at >= from : p.hi > p.lo;
+    }
     __device__ __noinline__ bool next(const MlaDecodeArgs& a, Piece& p) {
-        while (b < a.batch && at < to) {
-            p.b = b;
-            p.at = at;
-            p.len = clamped_len(a, b, false);
-            p.pages = (p.len + kPage - 1) / kPage;
-            const long long t0 = at + kFixed;
-            p.lo = (int)min((long long)p.pages, max(0ll, from - t0));
-            p.hi = (int)min((long long)p.pages, max(0ll, to - t0));
-            const bool mine = p.pages == 0 ? at >= from : p.hi > p.lo;
-            at = t0 + p.pages;
-            ++b;
-            if (mine) return true;
-        }
+        while (b < a.batch && at < to)
+            if (take(a, clamped_len(a, b, false), p)) return true;
         return false;
     }
 };
@@ -143,41 +147,42 @@ __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t nthreads, bool p) {
     return r != 0;
 }
 
-// Joins every column's values over lanes 0-15 of the warp, n columns (8, 16 or 32): at each step a lane hands over the
-// columns that its partner keeps.  In the end v[0] (and v[16] of 32) is that of column lane % 16 (+ 16), of 8 columns
-// lane % 8.  The other lanes do the same with what they hold.
+// Joins every column's values over 16 lanes, n columns (4, 8 or 16): at each step a lane hands over the columns that its
+// partner keeps.  In the end v[0] is that of column lane % n.
 template <int n, typename Op>
 __device__ __forceinline__ void join_columns(float (&v)[n], Op op) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = n < 16 ? n / 2 : 8; o >= 1; o >>= 1) {
+    for (int o = n / 2; o >= 1; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
-        for (int c = 0; c < n; ++c)
-            if ((c & 15) < o) {
-                const float give = up ? v[c] : v[c + o], keep = up ? v[c + o] : v[c];
-                v[c] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
-            }
+        for (int c = 0; c < o; ++c) {
+            const float give = up ? v[c] : v[c + o], keep = up ? v[c + o] : v[c];
+            v[c] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+        }
     }
-    if (n < 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 8));
+#pragma unroll
+    for (int o = n; o < 16; o <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
 }
 
 template <int N, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_decode_kernel(const __grid_constant__ MlaDecodeArgs a, const __grid_constant__ CUtensorMap map_q,
-                      const __grid_constant__ CUtensorMap map_kv) {
+                      const __grid_constant__ CUtensorMap map_latent, const __grid_constant__ CUtensorMap map_rope) {
     using L = Layout<N>;
-    constexpr int kHalf = L::kHalf, kStages = L::kStages;
+    constexpr int kHalf = L::kHalf, kQuarter = L::kQuarter, kStages = L::kStages;
     struct Small {
         uint64_t bars[B_COUNT];
-        Walk start;
-        long long sums[kThreads / 32];
+        Walk start;            // where the walk goes on behind the pieces listed here
+        Piece pieces[kListed];
+        int count, share;
+        int sums[kThreads / 32];
         uint32_t tmem_base;
         int abort;
-        float part[4][N];      // the 4 parts of a column's reduction
-        float minus_ref[N];    // -reference (0 while it is -inf)
-        float factor[N];       // of the last change, or of the output
-        int sees[N];           // keys that the column's token sees
+        alignas(16) float part[4][N];  // the 4 parts of a column's reduction
+        alignas(16) float minus_ref[N];  // read by four: -reference (0 while it is -inf)
+        alignas(16) float factor[N];  // of the last change, or of the output
+        alignas(16) int sees[N];  // read by four: keys that the column's token sees
     };
     static_assert(L::kEnd + sizeof(Small) <= 232448, "shared memory of a CTA");
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -208,9 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         *abort_sh = 0;
         sh.start.b = a.batch;
+        sh.start.at = sh.start.from = sh.start.to = 0;
         fence_barrier_init();
         tma_prefetch_map(&map_q);
-        tma_prefetch_map(&map_kv);
+        tma_prefetch_map(&map_latent);
+        tma_prefetch_map(&map_rope);
     }
     grid_dependency_wait();
     if (warp == 1) {
@@ -221,37 +228,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
         const int per = (a.batch + kThreads - 1) / kThreads;
         const int b0 = min((int)threadIdx.x * per, a.batch), b1 = min(b0 + per, a.batch);
-        long long mine = 0;
+        int mine = 0;
         for (int b = b0; b < b1; ++b) mine += kFixed + (clamped_len(a, b, blockIdx.x == 0) + kPage - 1) / kPage;
-        long long incl = mine;
+        int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
         if (lane == 31) sh.sums[warp] = incl;
         __syncthreads();
-        long long before = incl - mine, total = 0;
+        int before = incl - mine, total = 0;
+#pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sh.sums[w];
-            total += sh.sums[w];
+            const int sum = sh.sums[w];
+            if (w < warp) before += sum;
+            total += sum;
         }
-        // (as many ranges as are at least that long, and all alike)
-        const long long ranges = max(1ll, min((long long)a.ranges, total / kMinShare));
-        const long long share = (total + ranges - 1) / ranges;
-        const long long from = range * share;
+        // (as many ranges as are at least that long, and all alike; the launch sees to sums below 2^31)
+        const int ranges = max(1, min(a.ranges, total / kMinShare));
+        const int share = (total + ranges - 1) / ranges;
+        const int from = range < ranges ? range * share : total;
         if (from >= before && from < before + mine) {
             Walk w;
             w.from = from;
-            w.to = from + share;
+            w.to = min(from + share, total);
             w.at = before;
             w.b = b0;
             for (;;) {
-                const long long cost = kFixed + (clamped_len(a, w.b, false) + kPage - 1) / kPage;
+                const int cost = kFixed + (clamped_len(a, w.b, false) + kPage - 1) / kPage;
                 if (from < w.at + cost) break;
                 w.at += cost;
                 ++w.b;
             }
+            sh.start = w;
+            sh.share = share;
+        }
+    }
+    __syncthreads();
+    if (warp == 2) {
+        // the pieces among the next kListed sequences, their lengths fetched at once: a role that asked for one at an item's
+        // end would wait for the load behind all the stores of the output
+        Walk w = sh.start;
+        const int b = w.b + lane;
+        const bool in = lane < kListed && b < a.batch;
+        const int len = in ? clamped_len(a, b, false) : 0;
+        const int cost = in ? kFixed + (len + kPage - 1) / kPage : 0;
+        int incl = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        Walk mine = w;
+        mine.b = b;
+        mine.at = w.at + incl - cost;
+        Piece p;
+        const bool take = in && mine.at < w.to && mine.take(a, len, p);
+        const unsigned taken = __ballot_sync(0xffffffffu, take);
+        if (take) sh.pieces[__popc(taken & ((1u << lane) - 1))] = p;
+        if (lane == 31) {
+            sh.count = __popc(taken);
+            w.b = min(w.b + kListed, a.batch);
+            w.at += incl;
             sh.start = w;
         }
     }
@@ -261,6 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tbase = sh.tmem_base;
     Walk walk = sh.start;
     Piece pc;
+    int listed = 0;
+    auto next_piece = [&]() {
+        if (listed < sh.count) {
+            pc = sh.pieces[listed++];
+            return true;
+        }
+        return walk.next(a, pc);
+    };
     const Waiter wait{abort_sh, a.wait_ns};
     bool ok = true;
 
@@ -269,42 +316,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             uint32_t items = 0, pages = 0;  // pieces with pages, pages issued
             uint32_t slot = 0, phase = 1;   // of the ring's next stage
-            while (ok && walk.next(a, pc)) {
+            while (ok && next_piece()) {
                 if (pc.hi == pc.lo) continue;
                 if (items > 0) ok = wait(&bars[B_QE], (items - 1) & 1);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&bars[B_QF], kChunks * L::kQChunk);
-                const int row = pc.b * a.rows + blk * N;
-#pragma unroll 1
-                for (int c = 0; c < kChunks; ++c)
-                    tma_load_2d(sm + L::kQOff + c * L::kQChunk, &map_q, &bars[B_QF], c * 64, row);
+                tma_load_3d(sm + L::kQOff, &map_q, &bars[B_QF], 0, pc.b * a.rows + blk * N, 0);
                 ++items;
                 const int32_t* table = a.block_table + (long long)pc.b * a.max_pages;
-                int next = __ldg(&table[pc.lo]);
+                auto row_of = [&](int p) {  // first row of page p (past the last one: that one's)
+                    const int id = __ldg(&table[min(p, pc.hi - 1)]);
+                    const bool in = (unsigned)id < (unsigned)a.num_pool_pages;
+                    if (!in) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
+                    return in ? id * kPage : 0;
+                };
+                int y = row_of(pc.lo), next = row_of(pc.lo + 1);
 #pragma unroll 1
                 for (int p = pc.lo; p < pc.hi && ok; ++p, ++pages) {
-                    const bool in = (unsigned)next < (unsigned)a.num_pool_pages;
-                    if (!in) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
-                    const int y = in ? next * kPage : 0;
-                    next = __ldg(&table[min(p + 1, pc.hi - 1)]);
+                    // the page behind is asked for in L2: with two pages in shared memory its loads are issued too late to
+                    // hide the memory's latency (64 sequences, 128 heads: 79 us a call without, 72 with, 73 two pages ahead)
+                    if (blk == 0 && p + 1 < pc.hi) prefetch_l2(a.pool + (long long)next * (kMlaRow * 2), kPage * kMlaRow * 2);
                     const uint32_t r = pages % kRopeStages;
                     ok = wait(&bars[B_RE + r], ((pages / kRopeStages) & 1) ^ 1);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&bars[B_RF + r], kBox);
-                    tma_load_2d(sm + L::kRopeOff + r * kBox, &map_kv, &bars[B_RF + r], kMlaLatent, y);
+                    tma_load_3d(sm + L::kRopeOff + r * kBox, &map_rope, &bars[B_RF + r], 0, y, kChunks - 1);
 #pragma unroll 1
                     for (int i = 0; i < kPageStages; ++i) {
                         ok = wait(&bars[B_LE + slot], phase);
                         if (!ok) break;
                         uint8_t* at = sm + L::kRingOff + slot * (2 * kBox);
                         mbar_arrive_expect_tx(&bars[B_LF + slot], 2 * kBox);
-                        tma_load_2d(at, &map_kv, &bars[B_LF + slot], i * 128, y);
-                        tma_load_2d(at + kBox, &map_kv, &bars[B_LF + slot], i * 128 + 64, y);
+                        tma_load_3d(at, &map_latent, &bars[B_LF + slot], 0, y, 2 * i);
                         if (++slot == kStages) {
                             slot = 0;
                             phase ^= 1;
                         }
                     }
+                    y = next;
+                    next = row_of(p + 2);
                 }
             }
             // every copy issued lands before the CTA may exit (after a timeout the last page may be short of some)
@@ -325,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t rd = sdesc_sw128(smem_u32(sm + L::kRopeOff), 16, 1024), kd = sdesc_sw128(smem_u32(sm + L::kRingOff), 16, 1024);
             const uint32_t q_lo = (uint32_t)qd, r_lo = (uint32_t)rd, k_lo = (uint32_t)kd, hi = (uint32_t)(qd >> 32);
             uint32_t items = 0, g = 0, slot = 0, phase = 0;  // pieces, pages, the ring's next stage
-            while (ok && walk.next(a, pc)) {
+            while (ok && next_piece()) {
                 if (pc.hi == pc.lo) continue;
                 ok = wait(&bars[B_QF], items & 1);
                 ++items;
@@ -374,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t p_lo = (uint32_t)pd, v_lo = (uint32_t)vd, p_hi = (uint32_t)(pd >> 32), v_hi = (uint32_t)(vd >> 32);
             auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
             uint32_t g = 0, slot = 0;
-            while (ok && walk.next(a, pc)) {
+            while (ok && next_piece()) {
 #pragma unroll 1
                 for (int p = pc.lo; p < pc.hi; ++p, ++g) {
                     ok = wait(&bars[B_PF + (g & 1)], (g >> 1) & 1);  // (its S was made of the page: that has landed)
@@ -404,21 +454,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = (warp - 2) >> 2;                 // of the columns
         const int tid = ((int)threadIdx.x - 64) & 127;    // of the half's threads: column half * kHalf + tid is its to keep
         const int key = q4 * 16 + (lane & 15);            // of the page
-        const bool has_key = lane < 16;
+        const int first = half * kHalf + (lane >> 4) * kQuarter;  // of this lane's columns
+        const int joined = half * kHalf + (lane >> 4) * kQuarter + lane % kQuarter;  // the one it has of joined columns
         const uint32_t bar_id = 1 + half, lane_addr = (uint32_t)(q4 * 32) << 16;
         const float sl2 = a.scale_log2;
         const int block_rows = min(N, a.rows - blk * N);
         const int columns = max(0, min(kHalf, block_rows - half * kHalf));  // of this half that are used
         const int column = half * kHalf + tid;
-        const float4* ref4 = reinterpret_cast<const float4*>(&sh.minus_ref[half * kHalf]);
-        const int4* sees4 = reinterpret_cast<const int4*>(&sh.sees[half * kHalf]);
+        const float4* ref4 = reinterpret_cast<const float4*>(&sh.minus_ref[first]);
+        const int4* sees4 = reinterpret_cast<const int4*>(&sh.sees[first]);
         uint32_t g = 0;       // pages done
         bool bad = false;     // a wait ran out: the half's threads leave together at their next barrier
         MlaMerge merge{0, 0, 0, 0};
-        uint64_t l2[kHalf / 2];  // the key's sums of weights, of two columns each
-        float s[kHalf];          // and its scores, in units of ln 2
+        uint64_t l2[kQuarter / 2];  // the key's sums of weights, of two columns each
+        float s[kQuarter];          // and its scores, in units of ln 2
 
-        while (walk.next(a, pc)) {
+        while (next_piece()) {
             const int n = pc.hi - pc.lo;
             float ref = -INFINITY;  // of the column to keep
             if (n > 0) {
@@ -431,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int all_see = pc.len - (a.q_len - 1);
 #pragma unroll
-            for (int c = 0; c < kHalf / 2; ++c) l2[c] = f2_pack(0u, 0u);
+            for (int c = 0; c < kQuarter / 2; ++c) l2[c] = f2_pack(0u, 0u);
 #pragma unroll 1
             for (int p = pc.lo; p < pc.hi; ++p, ++g) {
                 const int k0 = p * kPage + key;  // the key
@@ -440,15 +491,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float top = -INFINITY;
                 if (columns > 0 && __all_sync(0xffffffffu, !bad)) {
                     tc_fence_after();
-                    uint32_t (&r)[kHalf] = reinterpret_cast<uint32_t (&)[kHalf]>(s);
-                    tmem_ld_cols<kHalf>(tbase + lane_addr + (g & 1) * N + half * kHalf, r);
+                    uint32_t (&r)[kQuarter] = reinterpret_cast<uint32_t (&)[kQuarter]>(s);
+                    tmem_ld_halves<kQuarter, kQuarter>(tbase + lane_addr + (g & 1) * N + half * kHalf, r);
                     tmem_ld_wait();
                     reg_fence(r);
 #pragma unroll
-                    for (int c = 0; c < kHalf; ++c) s[c] = has_key ? s[c] * sl2 : -INFINITY;
+                    for (int c = 0; c < kQuarter; ++c) s[c] *= sl2;
                     if (edge) {
 #pragma unroll
-                        for (int c = 0; c < kHalf; c += 4) {
+                        for (int c = 0; c < kQuarter; c += 4) {
                             const int4 see = sees4[c / 4];
                             s[c] = k0 < see.x ? s[c] : -INFINITY;
                             s[c + 1] = k0 < see.y ? s[c + 1] : -INFINITY;
@@ -458,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (p > pc.lo) {
 #pragma unroll
-                        for (int c = 0; c < kHalf; c += 4) {
+                        for (int c = 0; c < kQuarter; c += 4) {
                             const float4 m = ref4[c / 4];
                             top = fmax3(fmax3(top, s[c] + m.x, s[c + 1] + m.y), s[c + 2] + m.z, s[c + 3] + m.w);
                         }
@@ -470,14 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (change) {
                     // the columns' maxima over the page
                     if (columns > 0) {
-                        float v[kHalf];
+                        float v[kQuarter];
 #pragma unroll
-                        for (int c = 0; c < kHalf; ++c) v[c] = s[c];
+                        for (int c = 0; c < kQuarter; ++c) v[c] = s[c];
                         join_columns(v, [](float x, float y) { return fmaxf(x, y); });
-                        if (lane < (kHalf < 16 ? kHalf : 16)) {
-                            sh.part[q4][half * kHalf + lane] = v[0];
-                            if (kHalf > 16) sh.part[q4][half * kHalf + 16 + lane] = v[kHalf > 16 ? 16 : 0];
-                        }
+                        sh.part[q4][joined] = v[0];  // (lanes of the same column have the same value)
                     }
                     bad = bar_or(bar_id, 128, bad);
                     if (bad) break;
@@ -502,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (rescale) {
                         tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < kHalf / 2; ++c) {
-                            const float2 f = *reinterpret_cast<const float2*>(&sh.factor[half * kHalf + 2 * c]);
+                        for (int c = 0; c < kQuarter / 2; ++c) {
+                            const float2 f = *reinterpret_cast<const float2*>(&sh.factor[first + 2 * c]);
                             float x, y;
                             f2_unpack(l2[c], x, y);
                             l2[c] = f2_pack(__float_as_uint(x * f.x), __float_as_uint(y * f.y));
@@ -522,23 +570,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st_wait();
                     }
                     uint8_t* const p_row = sm + L::kPOff + key * 128;
-                    const int chunk0 = (int)(g % L::kPBuffers) * (N / 8) + half * (kHalf / 8);
+                    uint32_t w[kQuarter / 2];
 #pragma unroll
-                    for (int u = 0; u < kHalf / 8; ++u) {
-                        uint32_t w[4];
+                    for (int c = 0; c < kQuarter; c += 4) {
+                        const float4 m = ref4[c / 4];
+                        const float x0 = ex2(s[c] + m.x), x1 = ex2(s[c + 1] + m.y);
+                        const float x2 = ex2(s[c + 2] + m.z), x3 = ex2(s[c + 3] + m.w);
+                        l2[c / 2] = f2_add(l2[c / 2], f2_pack(__float_as_uint(x0), __float_as_uint(x1)));
+                        l2[c / 2 + 1] = f2_add(l2[c / 2 + 1], f2_pack(__float_as_uint(x2), __float_as_uint(x3)));
+                        w[c / 2] = pack16x2(x0, x1, kF16);
+                        w[c / 2 + 1] = pack16x2(x2, x3, kF16);
+                    }
+                    const int at = (int)(g % L::kPBuffers) * (N * 2) + first * 2;  // byte of the row, 16-byte groups swizzled
+                    if constexpr (kQuarter == 4) {
+                        *reinterpret_cast<uint2*>(p_row + ((((at >> 4) ^ (key & 7)) << 4) | (at & 15))) = make_uint2(w[0], w[1]);
+                    } else {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int c = 8 * u + 4 * h;
-                            const float4 m = ref4[c / 4];
-                            const float x0 = ex2(s[c] + m.x), x1 = ex2(s[c + 1] + m.y);
-                            const float x2 = ex2(s[c + 2] + m.z), x3 = ex2(s[c + 3] + m.w);
-                            l2[c / 2] = f2_add(l2[c / 2], f2_pack(__float_as_uint(x0), __float_as_uint(x1)));
-                            l2[c / 2 + 1] = f2_add(l2[c / 2 + 1], f2_pack(__float_as_uint(x2), __float_as_uint(x3)));
-                            w[2 * h] = pack16x2(x0, x1, kF16);
-                            w[2 * h + 1] = pack16x2(x2, x3, kF16);
-                        }
-                        if (has_key)
-                            *reinterpret_cast<uint4*>(p_row + (((chunk0 + u) ^ (key & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int u = 0; u < kQuarter / 8; ++u)
+                            *reinterpret_cast<uint4*>(p_row + ((((at >> 4) + u) ^ (key & 7)) << 4)) =
+                                make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
                     }
                 }
                 const int live = pc.len - p * kPage;
@@ -564,16 +614,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long slot = (long long)(2 * range + (pc.lo == 0)) * blocks + blk;
             const long long row0 = (long long)pc.b * a.rows + blk * N;  // of the block's first column
             if (n > 0) {
-                float v[kHalf];
+                float v[kQuarter];
 #pragma unroll
-                for (int c = 0; c < kHalf / 2; ++c) f2_unpack(l2[c], v[2 * c], v[2 * c + 1]);
+                for (int c = 0; c < kQuarter / 2; ++c) f2_unpack(l2[c], v[2 * c], v[2 * c + 1]);
                 join_columns(v, [](float x, float y) { return x + y; });
-                const bool keeps = lane < (kHalf < 16 ? kHalf : 16);
                 if (whole) {
-                    if (keeps) {
-                        sh.part[q4][half * kHalf + lane] = v[0];
-                        if (kHalf > 16) sh.part[q4][half * kHalf + 16 + lane] = v[kHalf > 16 ? 16 : 0];
-                    }
+                    sh.part[q4][joined] = v[0];
                     bar_or(bar_id, 128, false);
                     if (tid < kHalf) {
                         const float l = (sh.part[0][column] + sh.part[1][column]) + (sh.part[2][column] + sh.part[3][column]);
@@ -582,9 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     bar_or(bar_id, 128, false);
                 } else {
-                    float* l = a.sum_part + (slot * 4 + q4) * kMlaBlockRows + half * kHalf + lane;
-                    if (keeps) l[0] = v[0];
-                    if (kHalf > 16 && keeps) l[16] = v[kHalf > 16 ? 16 : 0];
+                    if ((lane & 15) < kQuarter) a.sum_part[(slot * 4 + q4) * kMlaBlockRows + joined] = v[0];
                     if (tid < kHalf) a.ref_part[slot * kMlaBlockRows + column] = ref;
                 }
                 bad = !wait(&bars[B_OD + ((g - 1) & 1)], ((g - 1) >> 1) & 1);
@@ -619,8 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!whole && pc.lo == 0) {
-                const long long share = walk.to - walk.from;
-                merge = MlaMerge{pc.b, blk, (int)((pc.at + kFixed + pc.pages - 1) / share) - range + 1, range};
+                merge = MlaMerge{pc.b, blk, (pc.at + kFixed + pc.pages - 1) / sh.share - range + 1, range};
             }
             tc_fence_before();
         }
@@ -642,39 +685,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merge of split items: with a piece's references r_s, sums l_s and accumulators o_s (in units of 2^r_s),
 //   out = sum_s 2^(r_s - m) o_s / sum_s 2^(r_s - m) l_s,  lse = m ln 2 + ln of that sum,  m = max_s r_s.
-// A warp takes a row; where the pieces are many (few rows then), a quarter of it.
-constexpr int kMergeRows = 8, kMergeMany = 8;
-template <int N, bool kF16>
+// A warp takes a row, or where sequences are few and their pieces many a quarter of it (gridDim.z 4).
+constexpr int kMergeRows = 8;
+template <int N, bool kF16, int kColumns>
 __global__ void __launch_bounds__(kMergeRows * 32) mla_merge_kernel(const __grid_constant__ MlaDecodeArgs a) {
     grid_dependency_wait();
-    const int blocks = (a.rows + N - 1) / N;
     const MlaMerge m = a.merges[blockIdx.y];
-    const int quarter = blockIdx.x & 3;
-    const bool many = m.pieces > kMergeMany;
-    if (m.pieces == 0 || (!many && quarter != 0)) return;
+    if (m.pieces == 0) return;
+    constexpr int kVecs = kColumns / 128, kAhead = 2;
+    const int blocks = (a.rows + N - 1) / N;
     const int lane = threadIdx.x & 31;
-    const int in_block = (int)(blockIdx.x >> 2) * kMergeRows + (int)(threadIdx.x >> 5);
+    const int in_block = (int)blockIdx.x * kMergeRows + (int)(threadIdx.x >> 5);
     const int in_seq = m.blk * N + in_block;
     if (in_block >= N || in_seq >= a.rows) return;
     auto slot = [&](int s) { return (long long)(2 * (m.first + s) + (s == 0)) * blocks + m.blk; };  // of the s-th piece
     auto ref_of = [&](int s) { return a.ref_part[slot(s) * kMlaBlockRows + in_block]; };
+    const int column = lane * 4 + (int)blockIdx.z * kColumns;
+    const float* part = a.o_part + (long long)in_block * kMlaLatent + column;
+    // the first pieces' accumulators on their way while their weights are found
+    float4 v[kAhead][kVecs];
+    auto load = [&](float4 (&to)[kVecs], int s) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            to[i] = *reinterpret_cast<const float4*>(part + slot(s) * (kMlaBlockRows * kMlaLatent) + i * 128);
+    };
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) load(v[s], min(s, m.pieces - 1));
     float top = -INFINITY;
     for (int s = lane; s < m.pieces; s += 32) top = fmaxf(top, ref_of(s));
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float minus_top = top == -INFINITY ? 0.f : -top;
     float sum = 0.f;
-    float4 acc[4];
+    float4 acc[kVecs];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* part = a.o_part + (long long)in_block * kMlaLatent + lane * 4 + (many ? quarter * 128 : 0);
-    auto add = [&](float4& to, float w, const float* from) {
-        const float4 v = *reinterpret_cast<const float4*>(from);
-        to.x = fmaf(w, v.x, to.x);
-        to.y = fmaf(w, v.y, to.y);
-        to.z = fmaf(w, v.z, to.z);
-        to.w = fmaf(w, v.w, to.w);
-    };
+    for (int i = 0; i < kVecs; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < m.pieces; s0 += 32) {
         float weight = 0.f;  // of piece s0 + lane
         if (s0 + lane < m.pieces) {
@@ -685,17 +730,19 @@ __global__ void __launch_bounds__(kMergeRows * 32) mla_merge_kernel(const __grid
             sum = fmaf(weight, l, sum);
         }
         const int count = min(32, m.pieces - s0);
-        if (many) {
-#pragma unroll 4
-            for (int s = 0; s < count; ++s)
-                add(acc[0], __shfl_sync(0xffffffffu, weight, s), part + slot(s0 + s) * (kMlaBlockRows * kMlaLatent));
-        } else {
-#pragma unroll 2
-            for (int s = 0; s < count; ++s) {
-                const float w = __shfl_sync(0xffffffffu, weight, s);
-                const float* from = part + slot(s0 + s) * (kMlaBlockRows * kMlaLatent);
+        for (int s = 0; s < count; s += kAhead) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) add(acc[i], w, from + i * 128);
+            for (int j = 0; j < kAhead; ++j) {
+                if (s + j >= count) break;
+                const float w = __shfl_sync(0xffffffffu, weight, s + j);
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    acc[i].x = fmaf(w, v[j][i].x, acc[i].x);
+                    acc[i].y = fmaf(w, v[j][i].y, acc[i].y);
+                    acc[i].z = fmaf(w, v[j][i].z, acc[i].z);
+                    acc[i].w = fmaf(w, v[j][i].w, acc[i].w);
+                }
+                if (s0 + s + j + kAhead < m.pieces) load(v[j], s0 + s + j + kAhead);
             }
         }
     }
@@ -703,22 +750,17 @@ __global__ void __launch_bounds__(kMergeRows * 32) mla_merge_kernel(const __grid
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const long long orow = (long long)m.b * a.rows + in_seq;
-    uint16_t* out = a.out + orow * kMlaLatent + lane * 4;
-    auto put = [&](uint16_t* to, const float4& v) {
-        *reinterpret_cast<uint2*>(to) = sum > 0.f ? make_uint2(pack16x2(v.x * inv, v.y * inv, kF16), pack16x2(v.z * inv, v.w * inv, kF16))
-                                                  : make_uint2(0u, 0u);
-    };
-    if (many) {
-        put(out + quarter * 128, acc[0]);
-    } else {
+    uint16_t* out = a.out + orow * kMlaLatent + column;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) put(out + i * 128, acc[i]);
-    }
-    if (a.lse && quarter == 0 && lane == 0) a.lse[orow] = sum > 0.f ? (top + __log2f(sum)) * kLn2f : -INFINITY;
+    for (int i = 0; i < kVecs; ++i)
+        *reinterpret_cast<uint2*>(out + i * 128) =
+            sum > 0.f ? make_uint2(pack16x2(acc[i].x * inv, acc[i].y * inv, kF16), pack16x2(acc[i].z * inv, acc[i].w * inv, kF16))
+                      : make_uint2(0u, 0u);
+    if (a.lse && blockIdx.z == 0 && lane == 0) a.lse[orow] = sum > 0.f ? (top + __log2f(sum)) * kLn2f : -INFINITY;
 }
 
 template <int N, bool kF16>
-cudaError_t launch(MlaDecodeArgs& a, int sms, const CUtensorMap* mq, const CUtensorMap* mkv, cudaStream_t stream) {
+cudaError_t launch(MlaDecodeArgs& a, int sms, const CUtensorMap* maps, cudaStream_t stream) {
     auto kernel = mla_decode_kernel<N, kF16>;
     constexpr int smem = 232448;  // all of an SM's: one CTA each
     static std::atomic<uint64_t> configured{0};
@@ -729,26 +771,29 @@ cudaError_t launch(MlaDecodeArgs& a, int sms, const CUtensorMap* mq, const CUten
     const long long most = ((long long)a.batch * (kFixed + a.max_pages) + kMinShare - 1) / kMinShare;
     a.ranges = (int)max(1ll, min((long long)sms / blocks, most));
     const unsigned ctas = (unsigned)(a.ranges * blocks);
-    e = launch_overlapped(kernel, dim3(ctas), dim3(kThreads), smem, stream, a, *mq, *mkv);
+    e = launch_overlapped(kernel, dim3(ctas), dim3(kThreads), smem, stream, a, maps[0], maps[1], maps[2]);
     if (e != cudaSuccess || a.ranges == 1) return e;
-    const int rows = min(a.rows, N);
-    return launch_overlapped(mla_merge_kernel<N, kF16>, dim3(4 * ((rows + kMergeRows - 1) / kMergeRows), ctas),
-                             dim3(kMergeRows * 32), 0, stream, a);
+    const unsigned groups = (unsigned)((min(a.rows, N) + kMergeRows - 1) / kMergeRows);
+    const dim3 block(kMergeRows * 32);
+    // an item has many pieces where it is one of few: rows of which a warp would read 150 pieces alone
+    if (8 * a.batch <= a.ranges)
+        return launch_overlapped(mla_merge_kernel<N, kF16, 128>, dim3(groups, ctas, 4), block, 0, stream, a);
+    return launch_overlapped(mla_merge_kernel<N, kF16, 512>, dim3(groups, ctas), block, 0, stream, a);
 }
 
 template <bool kF16>
-cudaError_t launch_block(MlaDecodeArgs& a, int sms, const CUtensorMap* mq, const CUtensorMap* mkv, cudaStream_t stream) {
+cudaError_t launch_block(MlaDecodeArgs& a, int sms, const CUtensorMap* maps, cudaStream_t stream) {
     switch (mla_block_rows(a.rows)) {
-        case 16: return launch<16, kF16>(a, sms, mq, mkv, stream);
-        case 32: return launch<32, kF16>(a, sms, mq, mkv, stream);
-        default: return launch<64, kF16>(a, sms, mq, mkv, stream);
+        case 16: return launch<16, kF16>(a, sms, maps, stream);
+        case 32: return launch<32, kF16>(a, sms, maps, stream);
+        default: return launch<64, kF16>(a, sms, maps, stream);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_mla_decode(MlaDecodeArgs a, int sms, const CUtensorMap* mq, const CUtensorMap* mkv, cudaStream_t stream) {
-    return a.f16 ? launch_block<true>(a, sms, mq, mkv, stream) : launch_block<false>(a, sms, mq, mkv, stream);
+cudaError_t launch_mla_decode(MlaDecodeArgs a, int sms, const CUtensorMap* maps, cudaStream_t stream) {
+    return a.f16 ? launch_block<true>(a, sms, maps, stream) : launch_block<false>(a, sms, maps, stream);
 }
 
 }  // namespace pa

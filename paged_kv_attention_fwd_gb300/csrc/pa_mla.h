@@ -23,6 +23,7 @@ struct MlaMerge {
     int32_t b, blk, pieces, first;  // pieces of a split item, the first of them in range `first` (0: none)
 };
 struct MlaDecodeArgs {
+    const uint8_t* pool;
     const int32_t* block_table;
     const int32_t* seq_lens;
     uint16_t* out;     // [batch * rows, 512]
@@ -38,9 +39,9 @@ struct MlaDecodeArgs {
     float scale_log2;
     uint64_t wait_ns;
 };
-// map_q: [batch * rows, 576], boxes of 64 elements of mla_block_rows rows; map_kv: [pages * 64, 576], of 64 rows
-cudaError_t launch_mla_decode(MlaDecodeArgs a, int sms, const CUtensorMap* map_q, const CUtensorMap* map_kv,
-                              cudaStream_t stream);
+// maps: rows of 576 elements as [9 chunks, rows, 64], so that a box's chunks lie one behind the other: the queries'
+// (boxes of all chunks of mla_block_rows rows), the pool's (two chunks of a page, one chunk of a page)
+cudaError_t launch_mla_decode(MlaDecodeArgs a, int sms, const CUtensorMap* maps, cudaStream_t stream);
 
 // Rows into and out of latent pages (mla_cache.cu)
 struct MlaCacheArgs {

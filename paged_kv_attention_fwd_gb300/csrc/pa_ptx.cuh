@@ -155,6 +155,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
         : "memory");
 }
 
+// `bytes` (a multiple of 16) of global memory into L2
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // ------------------------------------------------------------------ tcgen05
 
 // Whole warp: allocate `ncols` (power of two >= 32) TMEM columns; the base
@@ -293,6 +298,27 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
     else if constexpr (N == 8) tmem_ld_x8(taddr, r);
     else if constexpr (N == 16) tmem_ld_x16(taddr, r);
     else tmem_ld_x32(taddr, r);
+}
+
+// N consecutive columns of lanes 0-15 of the warp's 32 for threads 0-15, and the
+// kStep columns further ones of the same lanes for threads 16-31 (N in {4, 8, 16})
+template <int N, int kStep>
+__device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0, %1, %2, %3}, [%4], %5;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr), "n"(kStep));
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], %9;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr), "n"(kStep));
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], %17;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr), "n"(kStep));
 }
 
 // Wait for this thread's outstanding TMEM loads.  Registers filled by the
