@@ -269,14 +269,14 @@ pa_status pa_mla_query(const pa_mla_project_shapes* sh, const void* q, const voi
     if (!sh) return host_fail(PA_ERR_INVALID_ARG, "shapes must not be NULL");
     if (sh->total_tokens < 0) return host_fail(PA_ERR_INVALID_ARG, "total_tokens must be >= 0");
     if (sh->total_tokens == 0) return PA_OK;
+    if (cos_sin && !positions) return host_fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (cos_sin && sh->max_position <= 0) return host_fail(PA_ERR_INVALID_ARG, "max_position must be positive");
+    if (!aligned16(cos_sin)) return host_fail(PA_ERR_INVALID_ARG, "cos_sin must be 16-byte aligned");
     pa::MlaProjectArgs a;
     CUtensorMap map_in, map_w;
     pa_status st = fill_project(sh, pa::kMlaNope + pa::kMlaRope, pa::kMlaRow, 64, q, w_uk, q_out, workspace,
                                 workspace_bytes, &a, &map_in, &map_w);
     if (st != PA_OK) return st;
-    if (cos_sin && !positions) return host_fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
-    if (cos_sin && sh->max_position <= 0) return host_fail(PA_ERR_INVALID_ARG, "max_position must be positive");
-    if (!aligned16(cos_sin)) return host_fail(PA_ERR_INVALID_ARG, "cos_sin must be 16-byte aligned");
     a.positions = positions;
     a.cos_sin = cos_sin;
     return launched(pa::launch_mla_query(a, &map_in, &map_w, stream), "latent query launch");

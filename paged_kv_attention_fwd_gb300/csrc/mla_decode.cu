@@ -623,8 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bar_or(bar_id, 128, false);
                     if (tid < kHalf) {
                         const float l = (sh.part[0][column] + sh.part[1][column]) + (sh.part[2][column] + sh.part[3][column]);
-                        sh.factor[column] = l > 0.f ? 1.f / l : 0.f;
-                        if (tid < columns && a.lse) a.lse[row0 + column] = l > 0.f ? (ref + __log2f(l)) * kLn2f : -INFINITY;
+                        sh.factor[column] = l == 0.f ? 0.f : 1.f / l;  // (a NaN stays one)
+                        if (tid < columns && a.lse) a.lse[row0 + column] = l == 0.f ? -INFINITY : (ref + __log2f(l)) * kLn2f;
                     }
                     bar_or(bar_id, 128, false);
                 } else {
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < kHalf; ++c) {
                             const float f = n > 0 ? sh.factor[half * kHalf + c] : 0.f;
-                            const float y = f > 0.f ? __uint_as_float(o[c]) * f : 0.f;
+                            const float y = f == 0.f ? 0.f : __uint_as_float(o[c]) * f;
                             if (c < columns) out[c * kMlaLatent + i * 128] = (uint16_t)pack16x2(y, 0.f, kF16);
                         }
                     } else {
@@ -748,15 +748,15 @@ __global__ void __launch_bounds__(kMergeRows * 32) mla_merge_kernel(const __grid
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long orow = (long long)m.b * a.rows + in_seq;
     uint16_t* out = a.out + orow * kMlaLatent + column;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
         *reinterpret_cast<uint2*>(out + i * 128) =
-            sum > 0.f ? make_uint2(pack16x2(acc[i].x * inv, acc[i].y * inv, kF16), pack16x2(acc[i].z * inv, acc[i].w * inv, kF16))
-                      : make_uint2(0u, 0u);
-    if (a.lse && blockIdx.z == 0 && lane == 0) a.lse[orow] = sum > 0.f ? (top + __log2f(sum)) * kLn2f : -INFINITY;
+            sum == 0.f ? make_uint2(0u, 0u) : make_uint2(pack16x2(acc[i].x * inv, acc[i].y * inv, kF16),
+                                                         pack16x2(acc[i].z * inv, acc[i].w * inv, kF16));
+    if (a.lse && blockIdx.z == 0 && lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2f;
 }
 
 template <int N, bool kF16>

@@ -438,3 +438,139 @@ def mla_decode_shapes(batch: int, num_q_heads: int, max_pages: int, num_pool_pag
                                   rope_dim=MLA_ROPE, page_size=64, max_pages_per_seq=max_pages,
                                   num_pool_pages=num_pool_pages, num_sms=sms if sms is not None else num_sms(device),
                                   dtype=KV_DTYPES[dtype])
+
+
+def _check_mla_table(sh, batch: int, device, cu_seqlens, start_pos, block_table):
+    if cu_seqlens is not None:
+        _check_flat("cu_seqlens", cu_seqlens, torch.int32, batch + 1, device, f"[{batch + 1}]")
+        _check_flat("start_pos", start_pos, torch.int32, batch, device, f"[{batch}]")
+    t = block_table
+    if (t.dtype != torch.int32 or t.device != device or t.dim() != 2 or t.shape[0] < batch
+            or (t.shape[1] > 1 and t.stride(1) != 1) or (batch > 1 and t.stride(0) != sh.max_pages_per_seq)
+            or (batch == 1 and t.shape[1] < sh.max_pages_per_seq)):
+        _refuse("block_table", t, f"{batch} rows of {sh.max_pages_per_seq} int32, one behind the other, on {device}")
+
+
+def _mla_dtype(sh):
+    return torch.float16 if sh.dtype == B.PA_KV_FP16 else torch.bfloat16
+
+
+def _check_mla_pool(sh, pool):
+    if (pool.dtype != _mla_dtype(sh) or not pool.is_contiguous()
+            or pool.numel() < sh.num_pool_pages * 64 * MLA_ROW):
+        _refuse("pool", pool, f"contiguous [{sh.num_pool_pages}, 64, {MLA_ROW}] of {_mla_dtype(sh)}")
+
+
+def _check_turn(sh, cos_sin, positions, count: int, device):
+    if cos_sin is None:
+        return
+    _check_flat("cos_sin", cos_sin, torch.float32, sh.max_position * MLA_ROPE, device, f"[{sh.max_position}, {MLA_ROPE}]")
+    if cos_sin.shape[-1] != MLA_ROPE:
+        _refuse("cos_sin", cos_sin, f"[{sh.max_position}, {MLA_ROPE}]")
+    if positions is not None:
+        _check_flat("positions", positions, torch.int32, count, device, f"[{count}]")
+
+
+def _check_workspace(workspace, device):
+    if workspace is not None:
+        _check_flat("workspace", workspace, workspace.dtype, 0, device, "bytes")
+
+
+def mla_query(q, w_uk, positions=None, cos_sin=None, interleaved: bool = False, q_out=None, workspace=None, stream=None):
+    """Queries q [T, H, 192] into the latent space: their first 128 elements
+    times w_uk [H, 128, 512], the last 64 turned by the angles of `positions`
+    in cos_sin (rope_table(.., 64)).  Returns (q_out [T, H, 576], workspace)."""
+    sh = mla_query_shapes(q, w_uk, 0 if cos_sin is None else cos_sin.shape[0], interleaved, q_out)
+    t, h, _ = q.shape
+    _check_turn(sh, cos_sin, positions, t, q.device)
+    _check_workspace(workspace, q.device)
+    q_out = _output(q_out, (t, h, MLA_ROW), q.dtype, q.device, stream)
+    workspace = _status(workspace, q.device, stream)
+    B.pa_mla_query(sh, q, w_uk, positions, cos_sin, q_out, workspace, stream=stream)
+    return q_out, workspace
+
+
+def mla_output(o, w_uv, out=None, workspace=None, stream=None):
+    """Attended latent vectors o [T, H, 512] to the heads' values: w_uv
+    [H, 128, 512] times each.  Returns (out [T, H, 128], workspace)."""
+    sh = mla_output_shapes(o, w_uv, out)
+    _check_workspace(workspace, o.device)
+    out = _output(out, (*o.shape[:2], MLA_HEAD), o.dtype, o.device, stream)
+    workspace = _status(workspace, o.device, stream)
+    B.pa_mla_output(sh, o, w_uv, out, workspace, stream=stream)
+    return out, workspace
+
+
+def mla_append_kv(sh: B.pa_mla_cache_shapes, kv_new, cu_seqlens_new, start_pos, block_table, pool, weight=None,
+                  positions=None, cos_sin=None, workspace=None, stream=None):
+    """New tokens' rows kv_new [total_new, 576] (latent part first) into their
+    pages, normed and turned.  Returns the workspace."""
+    dev = kv_new.device
+    if sh.batch > 0 and sh.total_new > 0:
+        if (kv_new.dim() != 2 or kv_new.shape[0] < sh.total_new or kv_new.shape[1] != MLA_ROW
+                or kv_new.dtype != _mla_dtype(sh) or kv_new.stride(1) != 1
+                or (sh.total_new > 1 and kv_new.stride(0) != sh.kv_stride)):
+            _refuse("kv_new", kv_new, f"[{sh.total_new}, {MLA_ROW}] of {_mla_dtype(sh)}, rows {sh.kv_stride} elements apart")
+        if pool.device != dev:
+            _refuse("pool", pool, f"a pool on {dev}")
+        _check_mla_pool(sh, pool)
+        _check_mla_table(sh, sh.batch, dev, cu_seqlens_new, start_pos, block_table)
+        if sh.norm and weight is not None:
+            _check_flat("weight", weight, kv_new.dtype, MLA_LATENT, dev, f"[{MLA_LATENT}]")
+        _check_turn(sh, cos_sin, positions, sh.total_new, dev)
+        _check_workspace(workspace, dev)
+    workspace = _status(workspace, dev, stream)
+    B.pa_mla_append_kv(sh, kv_new, weight, positions, cos_sin, cu_seqlens_new, start_pos, block_table, pool, workspace,
+                       stream=stream)
+    return workspace
+
+
+def mla_gather_kv(sh: B.pa_mla_cache_shapes, pool, cu_seqlens, start_pos, block_table, latent_out=None, rope_out=None,
+                  workspace=None, stream=None):
+    """Rows of a latent cache back: latent [total_new, 512] and rotary
+    [total_new, 1, 64] (the k_rope of a prefill over the expanded keys).
+    Returns (latent_out, rope_out, workspace)."""
+    dev, dt = pool.device, _mla_dtype(sh)
+    shapes = {"latent_out": (sh.total_new, MLA_LATENT), "rope_out": (sh.total_new, 1, MLA_ROPE)}
+    if sh.batch > 0 and sh.total_new > 0:
+        _check_mla_pool(sh, pool)
+        _check_mla_table(sh, sh.batch, dev, cu_seqlens, start_pos, block_table)
+        for name, x in (("latent_out", latent_out), ("rope_out", rope_out)):
+            if x is not None:
+                _check_flat(name, x, dt, int(np.prod(shapes[name])), dev, f"{list(shapes[name])}")
+        _check_workspace(workspace, dev)
+    latent_out = _output(latent_out, shapes["latent_out"], dt, dev, stream)
+    rope_out = _output(rope_out, shapes["rope_out"], dt, dev, stream)
+    workspace = _status(workspace, dev, stream)
+    B.pa_mla_gather_kv(sh, pool, cu_seqlens, start_pos, block_table, latent_out, rope_out, workspace, stream=stream)
+    return latent_out, rope_out, workspace
+
+
+def mla_decode(sh: B.pa_mla_decode_shapes, q, pool, block_table, seq_lens, scale: float, out=None, lse=None,
+               workspace=None, stream=None):
+    """Attention of the last q_len tokens of every sequence, q [B * q_len, H,
+    576] (mla_query's output), over its latent rows.  Returns (out
+    [B * q_len, H, 512], lse [B * q_len, H], workspace)."""
+    dev, dt = q.device, _mla_dtype(sh)
+    rows, h = sh.batch * sh.q_len, sh.num_q_heads
+    if sh.batch > 0:
+        if tuple(q.shape) != (rows, h, MLA_ROW) or q.dtype != dt or not q.is_contiguous():
+            _refuse("q", q, f"contiguous [{rows}, {h}, {MLA_ROW}] of {dt}")
+        if pool.device != dev:
+            _refuse("pool", pool, f"a pool on {dev}")
+        _check_mla_pool(sh, pool)
+        _check_mla_table(sh, sh.batch, dev, None, None, block_table)
+        _check_flat("seq_lens", seq_lens, torch.int32, sh.batch, dev, f"[{sh.batch}]")
+        if out is not None:
+            _check_flat("out", out, dt, rows * h * MLA_LATENT, dev, f"[{rows}, {h}, {MLA_LATENT}]")
+        if lse is not None:
+            _check_flat("lse", lse, torch.float32, rows * h, dev, f"[{rows}, {h}]")
+        _check_workspace(workspace, dev)
+    out = _output(out, (rows, h, MLA_LATENT), dt, dev, stream)
+    lse = _output(lse, (rows, h), torch.float32, dev, stream)
+    if workspace is None:
+        with _on(stream):
+            workspace = torch.empty(B.pa_mla_decode_workspace_size(sh), dtype=torch.uint8, device=dev)
+            workspace[:B.PA_STATUS_BYTES].zero_()
+    B.pa_mla_decode(sh, q, pool, block_table, seq_lens, scale, out, lse, workspace, stream=stream)
+    return out, lse, workspace
