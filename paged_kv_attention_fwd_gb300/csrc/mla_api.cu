@@ -114,16 +114,17 @@ pa_status check_cache_sizes(const pa_mla_cache_shapes* sh) {
 
 // ------------------------------------------------------------ products
 
-// Checks of both products; fills `a` and the two maps.  in_row, out_row: a
-// head's elements of the input and the output; sum: those that are multiplied.
-pa_status fill_project(const pa_mla_project_shapes* sh, int in_row, int out_row, int w_box_rows, const void* in,
-                       const void* w, void* out, void* workspace, size_t workspace_bytes, pa::MlaProjectArgs* a,
-                       CUtensorMap* map_in, CUtensorMap* map_w) {
+// Checks of both products; fills `a` and the three maps.  in_row, out_row: a
+// head's elements of the input and the output.
+pa_status fill_project(const pa_mla_project_shapes* sh, int in_row, int out_row, const void* in, const void* w, void* out,
+                       void* workspace, size_t workspace_bytes, pa::MlaProjectArgs* a, CUtensorMap* maps) {
     pa_status st = check_row(sh->latent_dim, sh->rope_dim, sh->dtype);
     if (st != PA_OK) return st;
     if (sh->head_dim != pa::kMlaNope) return host_fail(PA_ERR_UNSUPPORTED, "head_dim must be 128 (got %d)", sh->head_dim);
     if (sh->num_heads <= 0 || sh->num_heads > 65535)
         return host_fail(PA_ERR_INVALID_ARG, "num_heads must be in [1, 65535] (got %d)", sh->num_heads);
+    if ((int64_t)sh->num_heads * (((int64_t)sh->total_tokens + 127) / 128) >= ((int64_t)1 << 28))
+        return host_fail(PA_ERR_UNSUPPORTED, "num_heads * total_tokens / 128 must be below 2^28");
     if (sh->total_tokens > 65535 * 128) return host_fail(PA_ERR_UNSUPPORTED, "total_tokens above 65535 * 128");
     st = check_stride(sh->in_stride, (int64_t)sh->num_heads * in_row, "in_stride");
     if (st == PA_OK) st = check_stride(sh->out_stride, (int64_t)sh->num_heads * out_row, "out_stride");
@@ -152,9 +153,12 @@ pa_status fill_project(const pa_mla_project_shapes* sh, int in_row, int out_row,
     const uint32_t ib[3] = {64, 1, 128};
     const uint64_t wd[3] = {(uint64_t)pa::kMlaLatent, 128, heads};
     const uint64_t ws[2] = {(uint64_t)pa::kMlaLatent * 2, (uint64_t)sh->w_stride * 2};
-    const uint32_t wb[3] = {64, (uint32_t)w_box_rows, 1};
-    st = pa::host_map_16(a->f16, map_in, in, 3, id, is, ib);
-    if (st == PA_OK) st = pa::host_map_16(a->f16, map_w, w, 3, wd, ws, wb);
+    const uint32_t wb[3] = {64, 128, 1};
+    const uint64_t od[3] = {(uint64_t)out_row, heads, (uint64_t)sh->total_tokens};
+    const uint64_t os[2] = {(uint64_t)out_row * 2, (uint64_t)sh->out_stride * 2};
+    st = pa::host_map_16(a->f16, &maps[0], in, 3, id, is, ib);
+    if (st == PA_OK) st = pa::host_map_16(a->f16, &maps[1], w, 3, wd, ws, wb);
+    if (st == PA_OK) st = pa::host_map_16(a->f16, &maps[2], out, 3, od, os, ib);
     return st;
 }
 
@@ -273,13 +277,13 @@ pa_status pa_mla_query(const pa_mla_project_shapes* sh, const void* q, const voi
     if (cos_sin && sh->max_position <= 0) return host_fail(PA_ERR_INVALID_ARG, "max_position must be positive");
     if (!aligned16(cos_sin)) return host_fail(PA_ERR_INVALID_ARG, "cos_sin must be 16-byte aligned");
     pa::MlaProjectArgs a;
-    CUtensorMap map_in, map_w;
-    pa_status st = fill_project(sh, pa::kMlaNope + pa::kMlaRope, pa::kMlaRow, 64, q, w_uk, q_out, workspace,
-                                workspace_bytes, &a, &map_in, &map_w);
+    CUtensorMap maps[3];
+    pa_status st = fill_project(sh, pa::kMlaNope + pa::kMlaRope, pa::kMlaRow, q, w_uk, q_out, workspace, workspace_bytes, &a,
+                                maps);
     if (st != PA_OK) return st;
     a.positions = positions;
     a.cos_sin = cos_sin;
-    return launched(pa::launch_mla_query(a, &map_in, &map_w, stream), "latent query launch");
+    return launched(pa::launch_mla_query(a, maps, stream), "latent query launch");
 }
 
 pa_status pa_mla_output(const pa_mla_project_shapes* sh, const void* o, const void* w_uv, void* out, void* workspace,
@@ -289,11 +293,10 @@ pa_status pa_mla_output(const pa_mla_project_shapes* sh, const void* o, const vo
     if (sh->total_tokens < 0) return host_fail(PA_ERR_INVALID_ARG, "total_tokens must be >= 0");
     if (sh->total_tokens == 0) return PA_OK;
     pa::MlaProjectArgs a;
-    CUtensorMap map_in, map_w;
-    pa_status st = fill_project(sh, pa::kMlaLatent, pa::kMlaValue, 128, o, w_uv, out, workspace, workspace_bytes, &a,
-                                &map_in, &map_w);
+    CUtensorMap maps[3];
+    pa_status st = fill_project(sh, pa::kMlaLatent, pa::kMlaValue, o, w_uv, out, workspace, workspace_bytes, &a, maps);
     if (st != PA_OK) return st;
-    return launched(pa::launch_mla_output(a, &map_in, &map_w, stream), "latent output launch");
+    return launched(pa::launch_mla_output(a, maps, stream), "latent output launch");
 }
 
 }  // extern "C"

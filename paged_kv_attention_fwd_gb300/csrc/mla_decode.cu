@@ -136,17 +136,6 @@ struct Waiter {
     }
 };
 
-__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t nthreads, bool p) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)p), "r"(id), "r"(nthreads)
-        : "memory");
-    return r != 0;
-}
-
 // Joins every column's values over 16 lanes, n columns (4, 8 or 16): at each step a lane hands over the columns that its
 // partner keeps.  In the end v[0] is that of column lane % n.
 template <int n, typename Op>

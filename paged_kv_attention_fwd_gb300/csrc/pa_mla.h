@@ -74,11 +74,9 @@ struct MlaProjectArgs {
     int32_t total, heads, interleaved, max_position, f16;
     uint64_t wait_ns;
 };
-// map_in: the input as [tokens, heads, elements], boxes of 64 elements of 128 tokens
-// map_w: the weights as [heads, 128, 512], boxes of 64 elements of 128 rows
-cudaError_t launch_mla_query(const MlaProjectArgs& a, const CUtensorMap* map_in, const CUtensorMap* map_w,
-                             cudaStream_t stream);
-cudaError_t launch_mla_output(const MlaProjectArgs& a, const CUtensorMap* map_in, const CUtensorMap* map_w,
-                              cudaStream_t stream);
+// maps: the input as [tokens, heads, elements] in boxes of 64 elements of 128 tokens, the weights as [heads, 128, 512] in
+// boxes of 64 elements of 128 rows, the output like the input
+cudaError_t launch_mla_query(const MlaProjectArgs& a, const CUtensorMap* maps, cudaStream_t stream);
+cudaError_t launch_mla_output(const MlaProjectArgs& a, const CUtensorMap* maps, cudaStream_t stream);
 
 }  // namespace pa
