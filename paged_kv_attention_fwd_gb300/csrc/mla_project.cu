@@ -21,58 +21,74 @@ namespace {
 constexpr int kTokens = 128;
 constexpr int kTokenBytes = kTokens * 128;  // 64 elements of 128 tokens
 
-// A query's rotary part of one token, in whole sectors where the addresses allow it.
+// The rotary parts of 32 tokens of a head, a warp's: 4 lanes a token, 8 pairs each, so that a load or store touches whole
+// sectors of 8 tokens.  All of the warp's loads are in flight before the first angle is asked for.
 template <bool kF16, bool kInterleaved>
-__device__ __forceinline__ void turn_row(const uint16_t* src, uint16_t* dst, const float* cs, bool wide_in, bool wide_out) {
-    Sector in[4];
+__device__ __forceinline__ void turn_rows(const MlaProjectArgs& a, int h, int tok0, int lane) {
+    const int rj = lane & 3;
+    const int ra = kInterleaved ? 16 * rj : 8 * rj, rb = kInterleaved ? 16 * rj + 8 : 32 + 8 * rj;
+    uint4 lo[4], hi[4];
+    int at[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[i] = load_sector(src + 16 * i, wide_in);
+    for (int i = 0; i < 4; ++i) {
+        const int tok = tok0 + 8 * i + (lane >> 2);
+        at[i] = -1;
+        if (tok >= a.total) continue;
+        at[i] = a.cos_sin != nullptr ? __ldg(&a.positions[tok]) : 0;
+        const uint16_t* src = a.in + (long long)tok * a.in_stride + (long long)h * (kMlaNope + kMlaRope) + kMlaNope;
+        lo[i] = __ldg(reinterpret_cast<const uint4*>(src + ra));
+        hi[i] = __ldg(reinterpret_cast<const uint4*>(src + rb));
+    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // 16 pairs: sectors 2i, 2i + 1 or i, i + 2
-        Sector& lo = in[kInterleaved ? 2 * i : i];
-        Sector& hi = in[kInterleaved ? 2 * i + 1 : i + 2];
-        if (cs != nullptr) {
-            uint32_t u[16] = {lo.lo.x, lo.lo.y, lo.lo.z, lo.lo.w, lo.hi.x, lo.hi.y, lo.hi.z, lo.hi.w,
-                              hi.lo.x, hi.lo.y, hi.lo.z, hi.lo.w, hi.hi.x, hi.hi.y, hi.hi.z, hi.hi.w};
-            float v[32], c[16], s[16];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                *reinterpret_cast<float4*>(&c[4 * k]) = __ldg(reinterpret_cast<const float4*>(cs + 16 * i) + k);
-                *reinterpret_cast<float4*>(&s[4 * k]) = __ldg(reinterpret_cast<const float4*>(cs + 32 + 16 * i) + k);
+    for (int i = 0; i < 4; ++i) {
+        if (at[i] < 0) continue;
+        if (a.cos_sin != nullptr) {
+            if (at[i] >= a.max_position) {
+                atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
+                continue;
             }
+            float c[8], s[8], v[16];
+            const float4* t = reinterpret_cast<const float4*>(a.cos_sin + (long long)at[i] * kMlaRope + 8 * rj);
+            *reinterpret_cast<float4*>(&c[0]) = __ldg(t);
+            *reinterpret_cast<float4*>(&c[4]) = __ldg(t + 1);
+            *reinterpret_cast<float4*>(&s[0]) = __ldg(t + 8);
+            *reinterpret_cast<float4*>(&s[4]) = __ldg(t + 9);
+            uint32_t u[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
 #pragma unroll
-            for (int k = 0; k < 16; ++k) unpack16x2(u[k], kF16, v[2 * k], v[2 * k + 1]);
+            for (int k = 0; k < 8; ++k) unpack16x2(u[k], kF16, v[2 * k], v[2 * k + 1]);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int f = kInterleaved ? 2 * k : k, g = kInterleaved ? 2 * k + 1 : 16 + k;
+            for (int k = 0; k < 8; ++k) {
+                const int f = kInterleaved ? 2 * k : k, g = kInterleaved ? 2 * k + 1 : 8 + k;
                 const float y = v[f] * c[k] - v[g] * s[k], z = v[g] * c[k] + v[f] * s[k];
                 v[f] = y;
                 v[g] = z;
             }
 #pragma unroll
-            for (int k = 0; k < 16; ++k) u[k] = pack16x2(v[2 * k], v[2 * k + 1], kF16);
-            lo = Sector{make_uint4(u[0], u[1], u[2], u[3]), make_uint4(u[4], u[5], u[6], u[7])};
-            hi = Sector{make_uint4(u[8], u[9], u[10], u[11]), make_uint4(u[12], u[13], u[14], u[15])};
+            for (int k = 0; k < 8; ++k) u[k] = pack16x2(v[2 * k], v[2 * k + 1], kF16);
+            lo[i] = make_uint4(u[0], u[1], u[2], u[3]);
+            hi[i] = make_uint4(u[4], u[5], u[6], u[7]);
         }
+        uint16_t* dst = a.out + (long long)(tok0 + 8 * i + (lane >> 2)) * a.out_stride + (long long)h * kMlaRow + kMlaLatent;
+        *reinterpret_cast<uint4*>(dst + ra) = lo[i];
+        *reinterpret_cast<uint4*>(dst + rb) = hi[i];
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) store_sector(dst + 16 * i, in[i], wide_out);
 }
 
 // ----------------------------------------------------------------- query
 
 // kLarge: a CTA an SM takes a run of (head, 128 tokens), all 512 columns of a head's weights in shared memory until the
-// head changes; tokens come two tiles ahead.  Otherwise two CTAs an SM take 256 columns of one tile each.  Results leave
-// by TMA from 64-column buffers; a token's rotary part is turned by warps of its own meanwhile.
+// head changes; 64 elements of the next tile come while one is multiplied.  Otherwise two CTAs an SM take 256 columns of
+// one tile each.  Results leave by TMA from 64-column buffers, which groups of 4 warps fill in turn; the rotary parts are
+// turned by warps of their own meanwhile.
 template <bool kLarge>
 struct Query {
     static constexpr int kCols = kLarge ? kMlaLatent : 256, kParts = kMlaLatent / kCols;
-    static constexpr int kStages = kLarge ? 2 : 1, kBuffers = kLarge ? 2 : 1;
+    static constexpr int kStages = kLarge ? 3 : 2, kBuffers = kLarge ? 3 : 1;
     static constexpr int kWBytes = kCols * kMlaNope * 2;
-    static constexpr int kABytes = 2 * kTokenBytes;
-    static constexpr int kAOff = kWBytes, kOutOff = kAOff + kStages * kABytes;
+    static constexpr int kAOff = kWBytes, kOutOff = kAOff + kStages * kTokenBytes;
     static constexpr int kEnd = kOutOff + kBuffers * kTokenBytes;
-    static constexpr int kSlots = kCols / 128;  // of tensor memory, 128 columns each
+    static constexpr int kPer = kLarge ? 4 : 2, kSlots = kCols / 64 / kPer;  // tensor memory: slots of kPer x 64 columns
+    static_assert(kBuffers <= kPer, "every group has a part of every slot");
     struct Small {
         uint64_t w_full[kSlots], w_empty, a_full[kStages], a_empty[kStages], d_full[kSlots], d_empty[kSlots];
         uint32_t tmem_base;
@@ -107,7 +123,7 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
         }
         for (int s = 0; s < L::kSlots; ++s) {
             mbar_init(&sh.d_full[s], 1);
-            mbar_init(&sh.d_empty[s], 8);
+            mbar_init(&sh.d_empty[s], 4 * L::kBuffers);
         }
         *abort_sh = 0;
         fence_barrier_init();
@@ -130,37 +146,38 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
     if (warp == 0) {
         if (elect_one()) {  // ---- loads
             int unit = -1;
-            uint32_t n = 0, units = 0;
-            for (int i = first; i < last && ok; ++i, ++n) {
+            uint32_t m = 0, units = 0;
+            for (int i = first; i < last && ok; ++i) {
                 const int u = i / tiles, h = u / L::kParts, part = u % L::kParts, tok0 = (i - u * tiles) * kTokens;
                 if (u != unit) {
                     if (units > 0) ok = mbar_wait(&sh.w_empty, (units - 1) & 1, abort_sh, a.wait_ns);
                     if (!ok) break;
 #pragma unroll 1
                     for (int q = 0; q < L::kSlots; ++q) {
-                        mbar_arrive_expect_tx(&sh.w_full[q], 2 * kTokenBytes);
-                        for (int c = 2 * q; c < 2 * q + 2; ++c)
+                        mbar_arrive_expect_tx(&sh.w_full[q], L::kPer * kTokenBytes);
+                        for (int c = L::kPer * q; c < L::kPer * (q + 1); ++c)
                             tma_load_3d(sm + c * kTokenBytes, &map_w, &sh.w_full[q], part * L::kCols + c * 64, 0, h);
                     }
                     unit = u;
                     ++units;
                 }
-                const uint32_t s = n % L::kStages;
-                ok = mbar_wait(&sh.a_empty[s], ((n / L::kStages) & 1) ^ 1, abort_sh, a.wait_ns);
-                if (!ok) break;
-                mbar_arrive_expect_tx(&sh.a_full[s], L::kABytes);
-                tma_load_3d(sm + L::kAOff + s * L::kABytes, &map_in, &sh.a_full[s], 0, h, tok0);
-                tma_load_3d(sm + L::kAOff + s * L::kABytes + kTokenBytes, &map_in, &sh.a_full[s], 64, h, tok0);
+                for (int k = 0; k < 2 && ok; ++k, ++m) {
+                    const uint32_t s = m % L::kStages;
+                    ok = mbar_wait(&sh.a_empty[s], ((m / L::kStages) & 1) ^ 1, abort_sh, a.wait_ns);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&sh.a_full[s], kTokenBytes);
+                    tma_load_3d(sm + L::kAOff + s * kTokenBytes, &map_in, &sh.a_full[s], 64 * k, h, tok0);
+                }
             }
             // every copy issued lands before the CTA may exit
             if (units > 0)
                 for (int q = 0; q < L::kSlots; ++q) mbar_wait(&sh.w_full[q], (units - 1) & 1, nullptr, a.wait_ns);
-            for (uint32_t s = 0; s < (uint32_t)L::kStages && s < n; ++s)
-                mbar_wait(&sh.a_full[s], ((n - 1 - (n - 1 - s) % L::kStages) / L::kStages) & 1, nullptr, a.wait_ns);
+            for (uint32_t s = 0; s < (uint32_t)L::kStages && s < m; ++s)
+                mbar_wait(&sh.a_full[s], ((m - 1 - (m - 1 - s) % L::kStages) / L::kStages) & 1, nullptr, a.wait_ns);
         }
     } else if (warp == 1) {
         if (elect_one()) {  // ---- MMAs
-            constexpr uint32_t idesc = idesc_f16(kTokens, 128, !kF16, false, true);
+            constexpr uint32_t idesc = idesc_f16(kTokens, 64 * L::kPer, !kF16, false, true);
             const uint64_t ad = sdesc_sw128(smem_u32(sm + L::kAOff), 16, 1024), wd = sdesc_sw128(smem_u32(sm), kTokenBytes, 1024);
             const uint32_t a_lo = (uint32_t)ad, w_lo = (uint32_t)wd, a_hi = (uint32_t)(ad >> 32), w_hi = (uint32_t)(wd >> 32);
             int unit = -1;
@@ -172,38 +189,42 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
                     unit = u;
                     ++units;
                 }
-                const uint32_t s = n % L::kStages;
-                ok = mbar_wait(&sh.a_full[s], (n / L::kStages) & 1, abort_sh, a.wait_ns);
+                uint32_t a0[2];
+                for (uint32_t k = 0; k < 2; ++k) {
+                    const uint32_t m = 2 * n + k, s = m % L::kStages;
+                    if (ok) ok = mbar_wait(&sh.a_full[s], (m / L::kStages) & 1, abort_sh, a.wait_ns);
+                    a0[k] = a_lo + s * (kTokenBytes >> 4);
+                }
                 if (!ok) break;
-                const uint32_t a0 = a_lo + s * (L::kABytes >> 4);
 #pragma unroll 1
-                for (int q = 0; q < L::kSlots; ++q, ++steps) {  // slot q: columns 128 q of the part
+                for (int q = 0; q < L::kSlots; ++q, ++steps) {
                     if (fresh) ok = mbar_wait(&sh.w_full[q], (units - 1) & 1, abort_sh, a.wait_ns);
                     if (ok) ok = mbar_wait(&sh.d_empty[q], (n & 1) ^ 1, abort_sh, a.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t w0 = w_lo + (uint32_t)(q * 2) * (kTokenBytes >> 4), dt = tbase + q * 128;
-                    mma_ss_w<0>(dt, a0, a_hi, w0, w_hi, idesc);
+                    const uint32_t w0 = w_lo + (uint32_t)(q * L::kPer) * (kTokenBytes >> 4), dt = tbase + q * 64 * L::kPer;
+                    mma_ss_w<0>(dt, a0[0], a_hi, w0, w_hi, idesc);
 #pragma unroll
                     for (int k = 1; k < 8; ++k)
-                        mma_ss_w<1>(dt, a0 + (uint32_t)((k / 4 * kTokenBytes) >> 4) + (k & 3) * 2, a_hi, w0 + k * 128, w_hi, idesc);
+                        mma_ss_w<1>(dt, a0[k / 4] + (k & 3) * 2, a_hi, w0 + k * 128, w_hi, idesc);
                     mma_commit(&sh.d_full[q]);
                 }
                 if (!ok) break;
-                mma_commit(&sh.a_empty[s]);
+                for (uint32_t k = 0; k < 2; ++k) mma_commit(&sh.a_empty[(2 * n + k) % L::kStages]);
                 if (i + 1 == last || (i + 1) / tiles != u) mma_commit(&sh.w_empty);
             }
             // (MMAs in flight end before the results are read, or after a timeout with their barriers)
-            if (!ok && n > 0) mbar_wait(&sh.a_empty[(n - 1) % L::kStages], ((n - 1) / L::kStages) & 1, nullptr, a.wait_ns);
+            if (!ok && n > 0) mbar_wait(&sh.a_empty[(2 * n - 1) % L::kStages], ((2 * n - 1) / L::kStages) & 1, nullptr, a.wait_ns);
         }
     } else if (warp < 2 + 4 * L::kBuffers) {
         // ---- the result, a token a thread; each group of 4 warps has a buffer and every kBuffers-th 64 columns
-        const int group = (warp - 2) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
+        const uint32_t group = (warp - 2) >> 2;
+        const int q4 = warp & 3, row = q4 * 32 + lane;
         const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16, bar_id = 1 + group;
         const bool issuer = threadIdx.x == 64 + 128 * group;
         const bool wide = aligned32(a.out) && a.out_stride % 16 == 0;
         uint8_t* const buffer = sm + L::kOutOff + group * kTokenBytes;
-        bool bad = false;
+        bool late = false, bad = false;  // this thread's wait ended at its limit, one of the group's
         uint32_t n = 0;
         for (int i = first; i < last && !bad; ++i, ++n) {
             const int u = i / tiles, h = u / L::kParts, part = u % L::kParts, tok0 = (i - u * tiles) * kTokens, tok = tok0 + row;
@@ -216,11 +237,13 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
             const bool by_rows = bar_or(bar_id, 128, !write && tok < a.total) || a.total - tok0 < 16;
             uint16_t* const dst = a.out + (long long)(write ? tok : 0) * a.out_stride + (long long)h * kMlaRow + part * L::kCols;
 #pragma unroll 1
-            for (int c = group; c < L::kCols / 64; c += L::kBuffers) {  // 64 columns
-                const int q = c / 2;
-                bad = !mbar_wait(&sh.d_full[q], n & 1, abort_sh, a.wait_ns);
+            for (int c = 0; c < L::kCols / 64; ++c) {  // 64 columns
+                const int q = c / L::kPer;
+                // (each waits for every slot of every tile, its first chunk or not: no slot runs two ahead of it)
+                if (c % L::kPer == 0) late |= !mbar_wait(&sh.d_full[q], n & 1, abort_sh, a.wait_ns);
+                if ((n * (L::kCols / 64) + c) % L::kBuffers != group) continue;
                 if (issuer) bulk_wait_read<0>();
-                bad = bar_or(bar_id, 128, bad);  // the buffer is free
+                bad = bar_or(bar_id, 128, late);  // the buffer is free
                 if (bad) break;
                 tc_fence_after();
                 uint32_t o[64];
@@ -233,7 +256,7 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
                 reg_fence(o1);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.d_empty[q]);  // (both halves of its 128 columns do)
+                if (lane == 0 && c % L::kPer + L::kBuffers >= L::kPer) mbar_arrive(&sh.d_empty[q]);  // the group's last of the slot
                 uint32_t w[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) w[k] = pack16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]), kF16);
@@ -259,23 +282,13 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
             }
         }
         if (issuer) bulk_wait_read<0>();  // (the buffer is not read any more; what was written is there when the grid ends)
-        ok = !bad;
+        ok = !bad && !late;
     } else {
-        // ---- the rotary part, a token a thread
-        const int row = (warp - 2 - 4 * L::kBuffers) * 32 + lane;
-        const bool wide_in = aligned32(a.in) && a.in_stride % 16 == 0, wide_out = aligned32(a.out) && a.out_stride % 16 == 0;
+        // ---- the rotary part, 32 tokens a warp
+        const int w = warp - 2 - 4 * L::kBuffers;
         for (int i = first; i < last; ++i) {
-            const int u = i / tiles, h = u / L::kParts, tok = (i - u * tiles) * kTokens + row;
-            if (u % L::kParts != L::kParts - 1 || tok >= a.total) continue;
-            const float* cs = nullptr;
-            if (a.cos_sin != nullptr) {
-                const int pos = __ldg(&a.positions[tok]);
-                if (pos >= a.max_position) atomicCAS(a.status, 0, PA_ERR_DEVICE_BOUNDS);
-                if (pos < 0 || pos >= a.max_position) continue;
-                cs = a.cos_sin + (long long)pos * kMlaRope;
-            }
-            turn_row<kF16, kInterleaved>(a.in + (long long)tok * a.in_stride + (long long)h * (kMlaNope + kMlaRope) + kMlaNope,
-                                         a.out + (long long)tok * a.out_stride + (long long)h * kMlaRow + kMlaLatent, cs, wide_in, wide_out);
+            const int u = i / tiles;
+            if (u % L::kParts == L::kParts - 1) turn_rows<kF16, kInterleaved>(a, u / L::kParts, (i - u * tiles) * kTokens + 32 * w, lane);
         }
     }
     if (!ok) {

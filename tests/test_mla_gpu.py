@@ -85,6 +85,12 @@ def test_query_against_fp64(t, h, dtype, inter):
     assert (room[t] == 7).all() and (room[:, h * 576:] == 7).all()
 
 
+@pytest.mark.parametrize("t,h,dtype,inter", [(2100, 64, "f16", True), (40, 304, "bf16", False), (200, 300, "bf16", True)])
+def test_query_many_tiles_a_head_and_many_heads(t, h, dtype, inter):
+    """Enough heads and tokens that an SM goes through several tiles of a head, or through several heads."""
+    test_query_against_fp64(t, h, dtype, inter)
+
+
 def test_query_padding_bad_positions_and_no_rotation():
     t, h = 140, 2
     q, w, table = normal((t, h, 192), 1), normal((h, 128, 512), 2) * 0.05, ops.rope_table(50, 64)
