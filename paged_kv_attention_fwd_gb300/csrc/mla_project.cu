@@ -9,6 +9,8 @@
 // products themselves stay far below the tensor cores' rate.  128 tokens are the
 // rows of an MMA.  W_uk lies with its columns contiguous (an MN-major operand),
 // W_uv with the summed dimension contiguous, so both are read as they are loaded.
+#include <algorithm>
+
 #include "cache4.cuh"
 #include "pa_launch.h"
 #include "pa_mla.h"
@@ -305,29 +307,67 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
 
 // ----------------------------------------------------------------- output
 
-// A CTA takes 128 tokens of a head; warp 0 loads and multiplies, one thread, warps 1-4 write, a token a thread.
-constexpr int kOutStages = 3, kOutStageBytes = 2 * kTokenBytes;  // 64 elements of 128 tokens, and of 128 rows of weights
-constexpr int kOutSteps = kMlaLatent / 64, kOutSmem = kOutStages * kOutStageBytes + 1024;
-constexpr int kOutThreads = 160;
+// A CTA an SM takes a run of groups of 32 tokens, head by head, with a head's 128 KB of weights in shared memory, the
+// run in tiles of up to 128 tokens whose 64-element pieces pass through a ring.  32 tokens are the unit so that SMs get
+// equal shares: only the groups of a tile that are the CTA's own are loaded, and written a token a thread.  (Rows of a
+// tile that were not loaded hold what was there; a row of a product depends on its own row alone.)
+struct Output {
+    static constexpr int kGroup = kMlaOutputGroup, kSteps = kMlaLatent / 64, kStages = 5;
+    static constexpr int kWBytes = kSteps * kTokenBytes;  // 64 elements of a head's 128 rows, eight times
+    static constexpr int kAOff = kWBytes, kEnd = kAOff + kStages * kTokenBytes;
+    struct Small {
+        uint64_t w_full[kSteps], w_empty[kSteps], a_full[kStages], a_empty[kStages], d_full[2], d_empty[2];
+        uint32_t tmem_base;
+        int abort;
+    };
+    static constexpr int kSmem = kEnd + (int)sizeof(Small);
+    static constexpr int kThreads = 192;  // loads, MMAs, 4 warps for the results
+};
+static_assert(Output::kSmem <= 232448, "a CTA an SM");
+
+// The tiles of a CTA's run of groups, in order.
+struct OutputRun {
+    int at, end, per_head, total;
+    int h, tok0, rows;  // the tile: its head, first token, and how many tokens are loaded
+    __device__ __forceinline__ OutputRun(const MlaProjectArgs& a)
+        : per_head((a.total + Output::kGroup - 1) / Output::kGroup), total(a.total), h(0), tok0(0), rows(0) {
+        const long long groups = (long long)a.heads * per_head;
+        at = (int)(groups * blockIdx.x / gridDim.x);
+        end = (int)(groups * (blockIdx.x + 1) / gridDim.x);
+    }
+    __device__ __forceinline__ bool next() {
+        if (at >= end) return false;
+        h = at / per_head;
+        const int first = at - h * per_head, n = min(min(kTokens / Output::kGroup, per_head - first), end - at);
+        tok0 = first * Output::kGroup;
+        rows = n * Output::kGroup;
+        at += n;
+        return true;
+    }
+};
 
 template <bool kF16>
-__global__ void __launch_bounds__(kOutThreads) mla_output_kernel(const __grid_constant__ MlaProjectArgs a,
-                                                                 const __grid_constant__ CUtensorMap map_in,
-                                                                 const __grid_constant__ CUtensorMap map_w) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full[kOutStages], empty[kOutStages], done;
-    __shared__ uint32_t tmem_base_sh;
-    __shared__ int abort_store;
-    volatile int* abort_sh = &abort_store;
+__global__ void __launch_bounds__(Output::kThreads, 1) mla_output_kernel(const __grid_constant__ MlaProjectArgs a,
+                                                                         const __grid_constant__ CUtensorMap map_in,
+                                                                         const __grid_constant__ CUtensorMap map_w) {
+    using L = Output;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    L::Small& sh = *reinterpret_cast<L::Small*>(sm + L::kEnd);
+    volatile int* const abort_sh = &sh.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = (int)blockIdx.x, tok0 = (int)blockIdx.y * kTokens;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kOutStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+        for (int s = 0; s < L::kSteps; ++s) {
+            mbar_init(&sh.w_full[s], 1);
+            mbar_init(&sh.w_empty[s], 1);
         }
-        mbar_init(&done, 1);
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(&sh.a_full[s], 1);
+            mbar_init(&sh.a_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh.d_full[s], 1);
+            mbar_init(&sh.d_empty[s], 4);
+        }
         *abort_sh = 0;
         fence_barrier_init();
         tma_prefetch_map(&map_in);
@@ -335,91 +375,141 @@ __global__ void __launch_bounds__(kOutThreads) mla_output_kernel(const __grid_co
     }
     grid_dependency_wait();
     allow_dependents_launch();
-    if (warp == 0) {
-        tmem_alloc(&tmem_base_sh, kMlaValue);
+    if (warp == 1) {
+        tmem_alloc(&sh.tmem_base, 2 * kMlaValue);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = tmem_base_sh;
+    const uint32_t tbase = sh.tmem_base;
+    bool ok = true;
 
+    OutputRun run(a);
     if (warp == 0) {
-        if (lane == 0) {
-            auto load = [&](int step) {
-                const int slot = step % kOutStages;
-                uint8_t* at = sm + slot * kOutStageBytes;
-                mbar_arrive_expect_tx(&full[slot], kOutStageBytes);
-                tma_load_3d(at + kTokenBytes, &map_w, &full[slot], step * 64, 0, h);
-                tma_load_3d(at, &map_in, &full[slot], step * 64, h, tok0);
-            };
-            for (int step = 0; step < kOutStages; ++step) load(step);
+        if (elect_one()) {  // ---- loads
+            int head = -1;
+            uint32_t m = 0, heads = 0;
+            uint32_t last_w = 0;  // how many of the newest head's pieces were asked for
+            while (ok && run.next()) {
+                const bool fresh = run.h != head;
+                if (fresh) {
+                    head = run.h;
+                    ++heads;
+                    last_w = 0;
+                }
+#pragma unroll 1
+                for (int k = 0; k < L::kSteps; ++k, ++m) {
+                    if (fresh) {
+                        if (heads > 1) ok = mbar_wait(&sh.w_empty[k], heads & 1, abort_sh, a.wait_ns);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&sh.w_full[k], kTokenBytes);
+                        tma_load_3d(sm + k * kTokenBytes, &map_w, &sh.w_full[k], 64 * k, 0, head);
+                        last_w = (uint32_t)k + 1;
+                    }
+                    const uint32_t s = m % L::kStages;
+                    ok = mbar_wait(&sh.a_empty[s], ((m / L::kStages) & 1) ^ 1, abort_sh, a.wait_ns);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&sh.a_full[s], run.rows * 128);
+                    for (int r = 0; r < run.rows; r += L::kGroup)
+                        tma_load_3d(sm + L::kAOff + s * kTokenBytes + r * 128, &map_in, &sh.a_full[s], 64 * k, head, run.tok0 + r);
+                }
+            }
+            // every copy issued lands before the CTA may exit
+            for (uint32_t k = 0; k < (uint32_t)L::kSteps && heads > 0; ++k)
+                if (k < last_w || heads > 1) mbar_wait(&sh.w_full[k], (k < last_w ? heads - 1 : heads) & 1, nullptr, a.wait_ns);
+            for (uint32_t s = 0; s < (uint32_t)L::kStages && s < m; ++s)
+                mbar_wait(&sh.a_full[s], ((m - 1 - (m - 1 - s) % L::kStages) / L::kStages) & 1, nullptr, a.wait_ns);
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {  // ---- MMAs
             constexpr uint32_t idesc = idesc_f16(kTokens, kMlaValue, !kF16, false, false);
-            bool ok = true;
-            int loaded = kOutStages;
-            for (int step = 0; step < kOutSteps && ok; ++step) {
-                const int slot = step % kOutStages;
-                ok = mbar_wait(&full[slot], (step / kOutStages) & 1, abort_sh, a.wait_ns);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t at = smem_u32(sm + slot * kOutStageBytes);
-                const uint64_t ad = sdesc_sw128(at, 16, 1024), bd = sdesc_sw128(at + kTokenBytes, 16, 1024);
+            const uint64_t ad = sdesc_sw128(smem_u32(sm + L::kAOff), 16, 1024), wd = sdesc_sw128(smem_u32(sm), 16, 1024);
+            const uint32_t a_lo = (uint32_t)ad, w_lo = (uint32_t)wd, a_hi = (uint32_t)(ad >> 32), w_hi = (uint32_t)(wd >> 32);
+            int head = -1;
+            uint32_t n = 0, m = 0, heads = 0;
+            for (bool more = run.next(); more && ok; ++n) {
+                const bool fresh = run.h != head;
+                if (fresh) {
+                    head = run.h;
+                    ++heads;
+                }
+                more = run.next();  // (the one after this one)
+                const bool leaves = !more || run.h != head;
+                const uint32_t slot = n & 1, dt = tbase + slot * kMlaValue;
+                ok = mbar_wait(&sh.d_empty[slot], ((n >> 1) & 1) ^ 1, abort_sh, a.wait_ns);
+#pragma unroll 1
+                for (int k = 0; k < L::kSteps && ok; ++k, ++m) {
+                    const uint32_t s = m % L::kStages;
+                    if (fresh) ok = mbar_wait(&sh.w_full[k], (heads - 1) & 1, abort_sh, a.wait_ns);
+                    if (ok) ok = mbar_wait(&sh.a_full[s], (m / L::kStages) & 1, abort_sh, a.wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a0 = a_lo + s * (kTokenBytes >> 4), w0 = w_lo + k * (kTokenBytes >> 4);
+                    if (k == 0)
+                        mma_ss_w<0>(dt, a0, a_hi, w0, w_hi, idesc);
+                    else
+                        mma_ss_w<1>(dt, a0, a_hi, w0, w_hi, idesc);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ss(tbase, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc, step > 0 || kk > 0);
-                if (step + 1 == kOutSteps) {
-                    mma_commit(&done);
-                } else if (loaded < kOutSteps) {
-                    mma_commit(&empty[slot]);
-                    ok = mbar_wait(&empty[slot], (step / kOutStages) & 1, abort_sh, a.wait_ns);
-                    if (ok) load(loaded++);
+                    for (int i = 1; i < 4; ++i) mma_ss_w<1>(dt, a0 + i * 2, a_hi, w0 + i * 2, w_hi, idesc);
+                    mma_commit(&sh.a_empty[s]);
+                    if (leaves) mma_commit(&sh.w_empty[k]);
                 }
+                if (ok) mma_commit(&sh.d_full[slot]);
             }
-            if (!ok) {
-                *abort_sh = 1;
-                atomicCAS(a.status, 0, PA_ERR_TIMEOUT);
-                // copies and MMAs in flight end before the CTA does
-                for (int s = 0; s < kOutStages; ++s) {
-                    const int last = loaded - 1 - (loaded - 1 - s) % kOutStages;
-                    mbar_wait(&full[s], (last / kOutStages) & 1, nullptr, a.wait_ns);
-                }
-                mma_commit(&done);
-                mbar_wait(&done, 0, nullptr, a.wait_ns);
-            }
+            // MMAs in flight end before the CTA does
+            if (!ok && m > 0) mbar_wait(&sh.a_empty[(m - 1) % L::kStages], ((m - 1) / L::kStages) & 1, nullptr, a.wait_ns);
         }
     } else {
-        const int q4 = warp & 3, row = q4 * 32 + lane, tok = tok0 + row;
-        const bool write = tok < a.total;
-        uint16_t* const dst = a.out + (long long)(write ? tok : 0) * a.out_stride + (long long)h * kMlaValue;
+        // ---- the result, a token a thread
+        const int q4 = warp & 3, row = q4 * 32 + lane;
         const bool wide = aligned32(a.out) && a.out_stride % 16 == 0;
-        const bool ok = mbar_wait(&done, 0, abort_sh, a.wait_ns);
-        if (__all_sync(0xffffffffu, ok) && __any_sync(0xffffffffu, write)) {
+        for (uint32_t n = 0; ok && run.next(); ++n) {
+            const int tok = run.tok0 + row;
+            const bool write = row < run.rows && tok < a.total;
+            uint16_t* const dst = a.out + (long long)(write ? tok : 0) * a.out_stride + (long long)run.h * kMlaValue;
+            const uint32_t slot = n & 1;
+            ok = mbar_wait(&sh.d_full[slot], (n >> 1) & 1, abort_sh, a.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             tc_fence_after();
-#pragma unroll 2
-            for (int c = 0; c < kMlaValue / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld_x32(tbase + ((uint32_t)(q4 * 32) << 16) + c * 32, o);
+#pragma unroll
+            for (int c = 0; c < kMlaValue / 64; ++c) {
+                uint32_t o[64];
+                uint32_t (&o0)[32] = *reinterpret_cast<uint32_t (*)[32]>(&o[0]);
+                uint32_t (&o1)[32] = *reinterpret_cast<uint32_t (*)[32]>(&o[32]);
+                const uint32_t at = tbase + ((uint32_t)(q4 * 32) << 16) + slot * kMlaValue + c * 64;
+                tmem_ld_x32(at, o0);
+                tmem_ld_x32(at + 32, o1);
                 tmem_ld_wait();
-                reg_fence(o);
-                if (write) {
+                reg_fence(o0);
+                reg_fence(o1);
+                if (c + 1 == kMlaValue / 64) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.d_empty[slot]);
+                }
+                if (!write) continue;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t w[8];
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            w[i] = pack16x2(__uint_as_float(o[16 * k + 2 * i]), __uint_as_float(o[16 * k + 2 * i + 1]), kF16);
-                        store_sector(dst + c * 32 + 16 * k,
-                                     Sector{make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])}, wide);
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        w[i] = pack16x2(__uint_as_float(o[16 * k + 2 * i]), __uint_as_float(o[16 * k + 2 * i + 1]), kF16);
+                    store_sector(dst + c * 64 + 16 * k, Sector{make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])}, wide);
                 }
             }
         }
     }
+    if (!ok) {
+        *abort_sh = 1;
+        atomicCAS(a.status, 0, PA_ERR_TIMEOUT);
+    }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tbase, kMlaValue);
+        tmem_dealloc(tbase, 2 * kMlaValue);
     }
 }
 
@@ -444,14 +534,28 @@ cudaError_t launch_query_size(const MlaProjectArgs& a, const CUtensorMap* maps, 
     return launch_query<false, kF16, kInterleaved>(a, items * Query<false>::kParts, maps, stream);
 }
 
+// How many CTAs: parts of one head each, so that none loads two heads' weights, or all SMs with equal shares, where the
+// longest share is then shorter by more than those weights, as long as 4 groups.  Measured at 32 heads of 1499 tokens
+// (12 groups against 10): 13.4 us and 13.7 us.
+int output_ctas(int heads, int total, int sms) {
+    const long long per_head = (total + Output::kGroup - 1) / Output::kGroup;
+    const long long groups = heads * per_head, equal = (groups + sms - 1) / sms;
+    if (heads >= sms) return sms;
+    const long long parts = std::min<long long>(sms / heads, per_head), whole = (per_head + parts - 1) / parts;
+    return (int)(whole <= equal + 4 ? heads * parts : std::min<long long>(sms, groups));
+}
+
 template <bool kF16>
 cudaError_t launch_output(const MlaProjectArgs& a, const CUtensorMap* maps, cudaStream_t stream) {
     auto kernel = mla_output_kernel<kF16>;
     static std::atomic<uint64_t> configured{0};
-    cudaError_t e = ensure_dynamic_smem(kernel, kOutSmem, configured);
+    cudaError_t e = ensure_dynamic_smem(kernel, Output::kSmem, configured);
+    int dev = 0, sms = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)a.heads, (unsigned)((a.total + kTokens - 1) / kTokens));
-    return launch_overlapped(kernel, grid, dim3(kOutThreads), kOutSmem, stream, a, maps[0], maps[1]);
+    return launch_overlapped(kernel, dim3((unsigned)output_ctas(a.heads, a.total, sms)), dim3(Output::kThreads), Output::kSmem, stream, a,
+                             maps[0], maps[1]);
 }
 
 }  // namespace

@@ -7,6 +7,7 @@
 namespace pa {
 
 constexpr int kMlaLatent = 512, kMlaRope = 64, kMlaRow = kMlaLatent + kMlaRope;  // elements of a cached row
+constexpr int kMlaOutputGroup = 32;  // tokens that pa_mla_output loads by one copy
 constexpr int kMlaNope = 128, kMlaValue = 128;                                     // of a head, before absorption
 
 // Host helpers of pa_api.cu: a status with a message for pa_last_error(), a

@@ -127,6 +127,12 @@ def test_output_against_fp64(t, h, dtype):
     assert (room[t] == 7).all() and (room[:, h * 128:] == 7).all()
 
 
+@pytest.mark.parametrize("t,h,dtype", [(1500, 32, "f16"), (40, 304, "bf16"), (1000, 200, "bf16"), (20000, 1, "bf16"), (300, 100, "f16")])
+def test_output_many_tiles_a_head_and_many_heads(t, h, dtype):
+    """Shares of an SM that hold several tiles, parts of tiles, and several heads' weights."""
+    test_output_against_fp64(t, h, dtype)
+
+
 def test_products_keep_nan_to_its_token_and_head():
     q, o, w = normal((200, 3, 192), 1), normal((200, 3, 512), 2), normal((3, 128, 512), 3)
     a, b = ops.mla_query(q, w)[0], ops.mla_output(o, w)[0]
