@@ -52,8 +52,8 @@ constexpr int kRopeStages = 2, kMaxStages = 11;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kListed = 16;  // sequences of a CTA's range whose pieces are found at its start
 constexpr int kThreads = 96 + 32 * kSoftmaxWarps;
-constexpr int kFixed = 4;     // what an item costs besides its pages, in pages
-constexpr int kMinShare = 6;  // a range is at least this long
+constexpr int kFixed = 5;     // what an item costs besides its pages, in pages
+constexpr int kMinShare = 2;  // a range is at least this long
 
 template <int N>
 struct Layout {
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Merge of split items: with a piece's references r_s, sums l_s and accumulators o_s (in units of 2^r_s),
 //   out = sum_s 2^(r_s - m) o_s / sum_s 2^(r_s - m) l_s,  lse = m ln 2 + ln of that sum,  m = max_s r_s.
 // A warp takes a row, or where sequences are few and their pieces many a quarter of it (gridDim.z 4).
-constexpr int kMergeRows = 8;
+constexpr int kMergeRows = 4;
 template <int N, bool kF16, int kColumns>
 __global__ void __launch_bounds__(kMergeRows * 32) mla_merge_kernel(const __grid_constant__ MlaDecodeArgs a) {
     grid_dependency_wait();
