@@ -80,17 +80,24 @@ __device__ __forceinline__ void turn_rows(const MlaProjectArgs& a, int h, int to
 
 // kLarge: a CTA an SM takes a run of (head, 128 tokens), all 512 columns of a head's weights in shared memory until the
 // head changes; 64 elements of the next tile come while one is multiplied.  Otherwise two CTAs an SM take 256 columns of
-// one tile each.  Results leave by TMA from 64-column buffers, which groups of 4 warps fill in turn; the rotary parts are
-// turned by warps of their own meanwhile.
+// one tile each.  Results leave by TMA from 64-column buffers, which groups of 4 warps fill in turn: three of them, or two
+// in the place of the one tile's tokens, which are multiplied by then.  Rotary parts are turned meanwhile, by warps of
+// their own or by the first group before it has results to wait for.
+//
+// Bound by memory: 1 token x 128 heads is 17 MB of weights in 5.7 us (2.9 TB/s, of which the launch and the first
+// loads' latency are over half), 64 x 128 29 MB in 7.3 us (4.0 TB/s), 1999 x 64 205 MB in 42 us (4.9 TB/s, three
+// quarters of it written).  Tiles of 128 columns, three CTAs an SM, took 7.1 and 9.8 us for the first two; without the
+// stores the third took 25 us, with weights loaded for every tile and heads side by side in time 45.
 template <bool kLarge>
 struct Query {
     static constexpr int kCols = kLarge ? kMlaLatent : 256, kParts = kMlaLatent / kCols;
-    static constexpr int kStages = kLarge ? 3 : 2, kBuffers = kLarge ? 3 : 1;
+    static constexpr int kStages = kLarge ? 3 : 2, kGroups = kLarge ? 3 : 2, kRotaryWarps = kLarge ? 4 : 0;
     static constexpr int kWBytes = kCols * kMlaNope * 2;
-    static constexpr int kAOff = kWBytes, kOutOff = kAOff + kStages * kTokenBytes;
-    static constexpr int kEnd = kOutOff + kBuffers * kTokenBytes;
-    static constexpr int kPer = kLarge ? 4 : 2, kSlots = kCols / 64 / kPer;  // tensor memory: slots of kPer x 64 columns
-    static_assert(kBuffers <= kPer, "every group has a part of every slot");
+    static constexpr int kAOff = kWBytes, kOutOff = kAOff + (kLarge ? kStages * kTokenBytes : 0);
+    static constexpr int kEnd = kOutOff + kGroups * kTokenBytes;
+    static constexpr int kPer = 4, kSlots = kCols / 64 / kPer;  // tensor memory: slots of kPer x 64 columns
+    static_assert(kGroups <= kPer, "every group has a part of every slot");
+    static_assert(kLarge || (kSlots == 1 && kGroups <= kStages), "a result is there once all tokens are multiplied");
     struct Small {
         uint64_t w_full[kSlots], w_empty, a_full[kStages], a_empty[kStages], d_full[kSlots], d_empty[kSlots];
         uint32_t tmem_base;
@@ -98,9 +105,9 @@ struct Query {
     };
     static constexpr int kSmem = kEnd + (int)sizeof(Small);
 };
-// loads, MMAs, 4 warps for each buffer of results, 4 for the rotary part
+// loads, MMAs, 4 warps for each buffer of results, those for the rotary part
 template <bool kLarge>
-constexpr int kQueryThreads = 192 + 128 * Query<kLarge>::kBuffers;
+constexpr int kQueryThreads = 64 + 128 * Query<kLarge>::kGroups + 32 * Query<kLarge>::kRotaryWarps;
 static_assert(Query<true>::kSmem <= 232448 && Query<false>::kSmem <= 115712, "one CTA an SM, two");
 
 template <bool kLarge, bool kF16, bool kInterleaved>
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
         }
         for (int s = 0; s < L::kSlots; ++s) {
             mbar_init(&sh.d_full[s], 1);
-            mbar_init(&sh.d_empty[s], 4 * L::kBuffers);
+            mbar_init(&sh.d_empty[s], 4 * L::kGroups);
         }
         *abort_sh = 0;
         fence_barrier_init();
@@ -218,8 +225,8 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
             // (MMAs in flight end before the results are read, or after a timeout with their barriers)
             if (!ok && n > 0) mbar_wait(&sh.a_empty[(2 * n - 1) % L::kStages], ((2 * n - 1) / L::kStages) & 1, nullptr, a.wait_ns);
         }
-    } else if (warp < 2 + 4 * L::kBuffers) {
-        // ---- the result, a token a thread; each group of 4 warps has a buffer and every kBuffers-th 64 columns
+    } else if (warp < 2 + 4 * L::kGroups) {
+        // ---- the result, a token a thread; each group of 4 warps has a buffer and every kGroups-th 64 columns
         const uint32_t group = (warp - 2) >> 2;
         const int q4 = warp & 3, row = q4 * 32 + lane;
         const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16, bar_id = 1 + group;
@@ -230,6 +237,7 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
         uint32_t n = 0;
         for (int i = first; i < last && !bad; ++i, ++n) {
             const int u = i / tiles, h = u / L::kParts, part = u % L::kParts, tok0 = (i - u * tiles) * kTokens, tok = tok0 + row;
+            if (!kLarge && group == 0 && part == L::kParts - 1) turn_rows<kF16, kInterleaved>(a, h, tok0 + 32 * (warp - 2), lane);
             bool write = tok < a.total;
             if (a.cos_sin != nullptr && write) {
                 const int pos = __ldg(&a.positions[tok]);
@@ -243,7 +251,7 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
                 const int q = c / L::kPer;
                 // (each waits for every slot of every tile, its first chunk or not: no slot runs two ahead of it)
                 if (c % L::kPer == 0) late |= !mbar_wait(&sh.d_full[q], n & 1, abort_sh, a.wait_ns);
-                if ((n * (L::kCols / 64) + c) % L::kBuffers != group) continue;
+                if ((n * (L::kCols / 64) + c) % L::kGroups != group) continue;
                 if (issuer) bulk_wait_read<0>();
                 bad = bar_or(bar_id, 128, late);  // the buffer is free
                 if (bad) break;
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
                 reg_fence(o1);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && c % L::kPer + L::kBuffers >= L::kPer) mbar_arrive(&sh.d_empty[q]);  // the group's last of the slot
+                if (lane == 0 && c % L::kPer + L::kGroups >= L::kPer) mbar_arrive(&sh.d_empty[q]);  // the group's last of the slot
                 uint32_t w[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) w[k] = pack16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]), kF16);
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
         ok = !bad && !late;
     } else {
         // ---- the rotary part, 32 tokens a warp
-        const int w = warp - 2 - 4 * L::kBuffers;
+        const int w = warp - 2 - 4 * L::kGroups;
         for (int i = first; i < last; ++i) {
             const int u = i / tiles;
             if (u % L::kParts == L::kParts - 1) turn_rows<kF16, kInterleaved>(a, u / L::kParts, (i - u * tiles) * kTokens + 32 * w, lane);
@@ -311,6 +319,10 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
 // run in tiles of up to 128 tokens whose 64-element pieces pass through a ring.  32 tokens are the unit so that SMs get
 // equal shares: only the groups of a tile that are the CTA's own are loaded, and written a token a thread.  (Rows of a
 // tile that were not loaded hold what was there; a row of a product depends on its own row alone.)
+//
+// Bound by memory: 64 tokens x 128 heads are 27 MB in 5.4 us (5.1 TB/s), 1499 x 32 66 MB in 13.4 us (4.9 TB/s, 1.2 of
+// it because SMs are given 12 groups or none).  A CTA a tile, two an SM, its weights streamed along with the tokens,
+// took 6.1 and 16.8 us.
 struct Output {
     static constexpr int kGroup = kMlaOutputGroup, kSteps = kMlaLatent / 64, kStages = 5;
     static constexpr int kWBytes = kSteps * kTokenBytes;  // 64 elements of a head's 128 rows, eight times
