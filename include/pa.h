@@ -640,14 +640,14 @@ typedef struct {
  *   q_out[t, h, 0:512]   = sum_i q[t, h, i] w_uk[h, i, 0:512]      (i < 128)
  *   q_out[t, h, 512:576] = q[t, h, 128:192] turned by the token's angles (see
  *                          pa_qk_norm_rope for the rotation and cos_sin)
- * with fp32 sums, rounded once.
+ * with fp32 sums, rounded once.  T <= 65535 * 128, H * T / 128 < 2^28.
  *   q          [T, H, 192], token stride in_stride
  *   w_uk       [H, 128, 512], head stride w_stride (a slice of a packed weight will do)
  *   positions  int32 [T]; a negative one marks a padding token, whose output is left
  *              as it was
  *   cos_sin    fp32 [max_position, 64], or NULL: the rotary part is copied, and
  *              positions is not read
- *   q_out      [T, H, 576], token stride out_stride
+ *   q_out      [T, H, 576], token stride out_stride; shares no memory with q
  *   workspace  >= PA_STATUS_BYTES (status word), zero-filled once
  * A position at or past max_position is recorded as PA_ERR_DEVICE_BOUNDS and its
  * token left as it was.
@@ -659,10 +659,10 @@ pa_status pa_mla_query(const pa_mla_project_shapes* shapes, const void* q, const
 /*
  * pa_mla_output -- attended latent vectors to the heads' values:
  *   out[t, h, i] = sum_k w_uv[h, i, k] o[t, h, k]                  (i < 128, k < 512)
- * with fp32 sums, rounded once.
+ * with fp32 sums, rounded once.  Limits as above.
  *   o          [T, H, 512], token stride in_stride
  *   w_uv       [H, 128, 512], head stride w_stride
- *   out        [T, H, 128], token stride out_stride
+ *   out        [T, H, 128], token stride out_stride; shares no memory with o
  *   workspace  >= PA_STATUS_BYTES (status word), zero-filled once
  */
 pa_status pa_mla_output(const pa_mla_project_shapes* shapes, const void* o, const void* w_uv, void* out,
@@ -752,7 +752,10 @@ typedef struct {
  * A length below 0 counts as 0, one past max_pages_per_seq * 64 as that many keys,
  * a page id outside the pool as page 0; each is recorded as PA_ERR_DEVICE_BOUNDS.
  * With fp16 and bf16 rows alike the softmax weights are rounded to the rows' type
- * before they are multiplied; sums are fp32.
+ * before they are multiplied; sums are fp32.  A NaN or an infinity in a row that a
+ * sequence holds reaches the outputs of all its q_len tokens, of one that does not
+ * see the row yet too (weight 0 times it).  num_q_heads * q_len <= 65536 and
+ * batch * (max_pages_per_seq + 16) < 2^31.
  */
 pa_status pa_mla_decode(const pa_mla_decode_shapes* shapes, const void* q, const void* pool, const int32_t* block_table,
                         const int32_t* seq_lens, float scale, void* out, float* lse, void* workspace,

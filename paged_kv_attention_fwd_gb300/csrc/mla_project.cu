@@ -542,6 +542,8 @@ cudaError_t launch_query_size(const MlaProjectArgs& a, const CUtensorMap* maps, 
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const long long items = (long long)a.heads * ((a.total + kTokens - 1) / kTokens);
+    // (with 128 heads and one tile both take the same time, 5.8 us for 1 token and 7.3 for 64; from there on SMs keep
+    // weights, below it halves reach twice as many SMs)
     if (items >= 2 * sms) return launch_query<true, kF16, kInterleaved>(a, sms, maps, stream);
     return launch_query<false, kF16, kInterleaved>(a, items * Query<false>::kParts, maps, stream);
 }
