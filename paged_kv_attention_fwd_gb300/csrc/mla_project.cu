@@ -79,22 +79,22 @@ __device__ __forceinline__ void turn_rows(const MlaProjectArgs& a, int h, int to
 // ----------------------------------------------------------------- query
 
 // kLarge: a CTA an SM takes a run of (head, 128 tokens), all 512 columns of a head's weights in shared memory until the
-// head changes; 64 elements of the next tile come while one is multiplied.  Otherwise two CTAs an SM take 256 columns of
-// one tile each.  Results leave by TMA from 64-column buffers, which groups of 4 warps fill in turn: three of them, or two
-// in the place of the one tile's tokens, which are multiplied by then.  Rotary parts are turned meanwhile, by warps of
-// their own or by the first group before it has results to wait for.
+// head changes.  Otherwise two CTAs an SM take 256 columns of one tile each.  Results leave by TMA from 64-column buffers
+// of two groups of 4 warps: two buffers each, or one in the place of the one tile's tokens, which are multiplied by then.
+// Rotary parts are turned meanwhile, by warps of their own or by the first group before it has results to wait for.
 //
 // Bound by memory: 1 token x 128 heads is 17 MB of weights in 5.7 us (2.9 TB/s, of which the launch and the first
-// loads' latency are over half), 64 x 128 29 MB in 7.3 us (4.0 TB/s), 1999 x 64 205 MB in 42 us (4.9 TB/s, three
-// quarters of it written).  Tiles of 128 columns, three CTAs an SM, took 7.1 and 9.8 us for the first two; without the
-// stores the third took 25 us, with weights loaded for every tile and heads side by side in time 45.
+// loads' latency are over half), 64 x 128 29 MB in 7.3 us (4.0 TB/s), 1999 x 64 205 MB in 40.7 us, 147 MB of them
+// written: a plain fill of as many bytes takes 41 us, one of 1 GB runs at 4.0 TB/s.  Tiles of 128 columns, three CTAs an
+// SM, took 7.1 and 9.8 us for the first two; three groups of one buffer and a token tile ahead 42 us for the third,
+// weights loaded for every tile and heads side by side in time 45.
 template <bool kLarge>
 struct Query {
     static constexpr int kCols = kLarge ? kMlaLatent : 256, kParts = kMlaLatent / kCols;
-    static constexpr int kStages = kLarge ? 3 : 2, kGroups = kLarge ? 3 : 2, kRotaryWarps = kLarge ? 4 : 0;
+    static constexpr int kStages = 2, kGroups = 2, kDeep = kLarge ? 2 : 1, kRotaryWarps = kLarge ? 4 : 0;
     static constexpr int kWBytes = kCols * kMlaNope * 2;
     static constexpr int kAOff = kWBytes, kOutOff = kAOff + (kLarge ? kStages * kTokenBytes : 0);
-    static constexpr int kEnd = kOutOff + kGroups * kTokenBytes;
+    static constexpr int kEnd = kOutOff + kGroups * kDeep * kTokenBytes;
     static constexpr int kPer = 4, kSlots = kCols / 64 / kPer;  // tensor memory: slots of kPer x 64 columns
     static_assert(kGroups <= kPer, "every group has a part of every slot");
     static_assert(kLarge || (kSlots == 1 && kGroups <= kStages), "a result is there once all tokens are multiplied");
@@ -226,13 +226,13 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
             if (!ok && n > 0) mbar_wait(&sh.a_empty[(2 * n - 1) % L::kStages], ((2 * n - 1) / L::kStages) & 1, nullptr, a.wait_ns);
         }
     } else if (warp < 2 + 4 * L::kGroups) {
-        // ---- the result, a token a thread; each group of 4 warps has a buffer and every kGroups-th 64 columns
+        // ---- the result, a token a thread; each group of 4 warps has kDeep buffers and every kGroups-th 64 columns
         const uint32_t group = (warp - 2) >> 2;
         const int q4 = warp & 3, row = q4 * 32 + lane;
         const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16, bar_id = 1 + group;
         const bool issuer = threadIdx.x == 64 + 128 * group;
         const bool wide = aligned32(a.out) && a.out_stride % 16 == 0;
-        uint8_t* const buffer = sm + L::kOutOff + group * kTokenBytes;
+        uint8_t* buffer = sm + L::kOutOff + group * L::kDeep * kTokenBytes;
         bool late = false, bad = false;  // this thread's wait ended at its limit, one of the group's
         uint32_t n = 0;
         for (int i = first; i < last && !bad; ++i, ++n) {
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
                 // (each waits for every slot of every tile, its first chunk or not: no slot runs two ahead of it)
                 if (c % L::kPer == 0) late |= !mbar_wait(&sh.d_full[q], n & 1, abort_sh, a.wait_ns);
                 if ((n * (L::kCols / 64) + c) % L::kGroups != group) continue;
-                if (issuer) bulk_wait_read<0>();
+                if (issuer) bulk_wait_read<L::kDeep - 1>();
                 bad = bar_or(bar_id, 128, late);  // the buffer is free
                 if (bad) break;
                 tc_fence_after();
@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kQueryThreads<kLarge>, kLarge ? 1 : 2)
                         tma_store_3d(&map_out, buffer, part * L::kCols + c * 64, h, tok0);
                         bulk_commit();
                     }
+                    if (L::kDeep == 2) buffer = sm + L::kOutOff + ((buffer - (sm + L::kOutOff)) ^ kTokenBytes);
                 }
             }
         }
