@@ -27,10 +27,11 @@
 //              memory
 //
 // The softmax's reference is not each key's running maximum but one value a
-// column, which changes only when a score exceeds it by more than 2^8.  Whether
-// one does is agreed upon by the four warps of a column; if so, and in an item's
-// first page, the columns' maxima over the page are found and the accumulators
-// rescaled.
+// column, which changes only when a score exceeds it by more than 2^8.  P is
+// written with the references as they are, and then the four warps of a column
+// agree whether one was exceeded; if so, and in an item's first page, the columns'
+// maxima over the page are found, the accumulators rescaled and P written again
+// (with the vote before P a call took 61.2 us, with it after 60.0).
 //
 // The sequences' costs (pages and a constant) are laid end to end and cut into
 // equal ranges, as many as there are CTAs a block: a CTA takes what lies in its
@@ -45,8 +46,9 @@
 // heads more than the memory's rate asks of the tensor cores at N = 64, where an
 // MMA reads 6 KB of shared memory for 34 cycles of products (48 at 128 B a
 // cycle): 1920 cycles a page and block, against 1500 for the memory's share of an
-// SM.  Measured, 64 sequences of 1-4096 keys, 128 heads, bf16: 61.2 us, 6 of them
-// the merge, about 2400 cycles a page, 6 us the start (launch, dealing, first
+// SM.  Measured, 64 sequences of 1-4096 keys, 128 heads, bf16: 60.0 us, 6 of them
+// the merge, about 2400 cycles a page (shared memory has room for two: a page's
+// turn is its load, 1150 cycles, S, the softmax, 1000, and O, in 4800 for two), 6 us the start (launch, dealing, first
 // page) and 4700 cycles the output of a piece; 32 of 64-16384 keys, 16 heads, two
 // tokens each: 59.6 us (287 MB, 4.8 TB/s, 5.9 while pages stream).  One sequence
 // of 777 keys, 128 heads: 12.9 us.
@@ -491,40 +493,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int p = pc.lo; p < pc.hi; ++p, ++g) {
                 const int k0 = p * kPage + key;  // the key
                 const bool edge = (p + 1) * kPage > all_see;
+                const int live = pc.len - p * kPage;
                 if (!bad) bad = !wait(&bars[B_SF + (g & 1)], (g >> 1) & 1);
-                float top = -INFINITY;
-                if (columns > 0 && __all_sync(0xffffffffu, !bad)) {
+                if (live < kPage && (live & 15) != 0 && !bad) {
+                    // 0 * NaN would poison the product: in the last group of 16 keys the rows past the last key are zeroed
+                    // (the page has landed and S is made of it)
+                    for (int w = (int)threadIdx.x - 64; w < (16 - (live & 15)) * 64; w += 32 * kSoftmaxWarps) {
+                        const int box = (w >> 3) & 7, i = w & 7;  // 16 bytes of a row of a box
+                        const uint32_t stage = (g * kPageStages + box / 2) % kStages;
+                        *reinterpret_cast<uint4*>(sm + L::kRingOff + stage * (2 * kBox) + (box & 1) * kBox +
+                                                  (live + (w >> 6)) * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                auto load_scores = [&]() {
                     tc_fence_after();
                     uint32_t (&r)[kQuarter] = reinterpret_cast<uint32_t (&)[kQuarter]>(s);
                     tmem_ld_halves<kQuarter, kQuarter>(tbase + lane_addr + (g & 1) * N + half * kHalf, r);
                     tmem_ld_wait();
                     reg_fence(r);
+                };
+                auto mask = [&]() {
+                    if (!edge) return;
 #pragma unroll
-                    for (int c = 0; c < kQuarter; ++c) s[c] *= sl2;
-                    if (edge) {
-#pragma unroll
-                        for (int c = 0; c < kQuarter; c += 4) {
-                            const int4 see = sees4[c / 4];
-                            s[c] = k0 < see.x ? s[c] : -INFINITY;
-                            s[c + 1] = k0 < see.y ? s[c + 1] : -INFINITY;
-                            s[c + 2] = k0 < see.z ? s[c + 2] : -INFINITY;
-                            s[c + 3] = k0 < see.w ? s[c + 3] : -INFINITY;
-                        }
+                    for (int c = 0; c < kQuarter; c += 4) {
+                        const int4 see = sees4[c / 4];
+                        s[c] = k0 < see.x ? s[c] : -INFINITY;
+                        s[c + 1] = k0 < see.y ? s[c + 1] : -INFINITY;
+                        s[c + 2] = k0 < see.z ? s[c + 2] : -INFINITY;
+                        s[c + 3] = k0 < see.w ? s[c + 3] : -INFINITY;
                     }
-                    if (p > pc.lo) {
+                };
+                // P where the page that its buffer was used for has been through O's MMAs; s becomes the weights
+                auto write_p = [&]() {
+                    uint8_t* const p_row = sm + L::kPOff + key * 128;
+                    uint32_t w[kQuarter / 2];
+#pragma unroll
+                    for (int c = 0; c < kQuarter; ++c) s[c] = ex2(s[c]);
+#pragma unroll
+                    for (int c = 0; c < kQuarter / 2; ++c) w[c] = pack16x2(s[2 * c], s[2 * c + 1], kF16);
+                    const int at = (int)(g % L::kPBuffers) * (N * 2) + first * 2;  // byte of the row, 16-byte groups swizzled
+                    if constexpr (kQuarter == 4) {
+                        *reinterpret_cast<uint2*>(p_row + ((((at >> 4) ^ (key & 7)) << 4) | (at & 15))) = make_uint2(w[0], w[1]);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < kQuarter / 8; ++u)
+                            *reinterpret_cast<uint4*>(p_row + ((((at >> 4) + u) ^ (key & 7)) << 4)) =
+                                make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+                    }
+                };
+                auto passed = [&](uint32_t behind) {  // O's MMAs of the page that many before this one
+                    return g < behind || wait(&bars[B_OD + ((g - behind) & 1)], ((g - behind) >> 1) & 1);
+                };
+                // ---- P with the references as they are, and then: did a score exceed its own?
+                bool change = p == pc.lo;
+                if (!change) {
+                    float top = -INFINITY;
+                    if (columns > 0 && __all_sync(0xffffffffu, !bad)) {
+                        load_scores();
 #pragma unroll
                         for (int c = 0; c < kQuarter; c += 4) {
                             const float4 m = ref4[c / 4];
-                            top = fmax3(fmax3(top, s[c] + m.x, s[c + 1] + m.y), s[c + 2] + m.z, s[c + 3] + m.w);
+                            s[c] = fmaf(s[c], sl2, m.x);
+                            s[c + 1] = fmaf(s[c + 1], sl2, m.y);
+                            s[c + 2] = fmaf(s[c + 2], sl2, m.z);
+                            s[c + 3] = fmaf(s[c + 3], sl2, m.w);
                         }
+                        mask();
+#pragma unroll
+                        for (int c = 0; c < kQuarter; c += 2) top = fmax3(top, s[c], s[c + 1]);
                     }
+                    if (!bad) bad = !passed(L::kPBuffers);
+                    if (columns > 0 && __all_sync(0xffffffffu, !bad)) write_p();
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    change = bar_or(bar_id, 128, bad || top > kRescaleThreshold);
                 }
-                // ---- does a score exceed its reference?
-                bool change = p == pc.lo;
-                if (!change) change = bar_or(bar_id, 128, bad || top > kRescaleThreshold);
                 if (change) {
-                    // the columns' maxima over the page
-                    if (columns > 0) {
+                    // ---- the columns' maxima over the page, new references, O rescaled, P with those
+                    if (columns > 0 && __all_sync(0xffffffffu, !bad)) {
+                        load_scores();
+#pragma unroll
+                        for (int c = 0; c < kQuarter; ++c) s[c] *= sl2;
+                        mask();
                         float v[kQuarter];
 #pragma unroll
                         for (int c = 0; c < kQuarter; ++c) v[c] = s[c];
@@ -545,71 +595,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sh.factor[column] = factor;
                     }
                     bar_or(bar_id, 128, false);
-                }
-                // ---- P, where the page that its buffer was used for has been through O's MMAs
-                const bool rescale = change && p > pc.lo;
-                const uint32_t behind = rescale ? 1 : L::kPBuffers;
-                if (g >= behind) bad = !wait(&bars[B_OD + ((g - behind) & 1)], ((g - behind) >> 1) & 1);
-                if (columns > 0 && __all_sync(0xffffffffu, !bad)) {
-                    if (rescale) {
-                        tc_fence_after();
+                    const bool rescale = p > pc.lo;
+                    bad = !passed(rescale ? 1 : L::kPBuffers);
+                    if (columns > 0 && __all_sync(0xffffffffu, !bad)) {
+                        if (rescale) {
+                            tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < kQuarter / 2; ++c) {
-                            const float2 f = *reinterpret_cast<const float2*>(&sh.factor[first + 2 * c]);
-                            float x, y;
-                            f2_unpack(l2[c], x, y);
-                            l2[c] = f2_pack(__float_as_uint(x * f.x), __float_as_uint(y * f.y));
-                        }
+                            for (int c = 0; c < kQuarter / 2; ++c) {
+                                const float2 f = *reinterpret_cast<const float2*>(&sh.factor[first + 2 * c]);
+                                float x, y;
+                                f2_unpack(l2[c], x, y);
+                                l2[c] = f2_pack(__float_as_uint(x * f.x), __float_as_uint(y * f.y));
+                            }
 #pragma unroll 1
-                        for (int i = 0; i < kPageStages; ++i) {
-                            uint32_t o[kHalf];
-                            const uint32_t at = tbase + lane_addr + L::kOCol + i * N + half * kHalf;
-                            tmem_ld_cols<kHalf>(at, o);
-                            tmem_ld_wait();
-                            reg_fence(o);
+                            for (int i = 0; i < kPageStages; ++i) {
+                                uint32_t o[kHalf];
+                                const uint32_t at = tbase + lane_addr + L::kOCol + i * N + half * kHalf;
+                                tmem_ld_cols<kHalf>(at, o);
+                                tmem_ld_wait();
+                                reg_fence(o);
 #pragma unroll
-                            for (int c = 0; c < kHalf; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * sh.factor[half * kHalf + c]);
-                            tmem_st_cols<kHalf>(at, o);
+                                for (int c = 0; c < kHalf; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * sh.factor[half * kHalf + c]);
+                                tmem_st_cols<kHalf>(at, o);
+                            }
+                            tmem_st_wait();
                         }
-                        tmem_st_wait();
-                    }
-                    uint8_t* const p_row = sm + L::kPOff + key * 128;
-                    uint32_t w[kQuarter / 2];
 #pragma unroll
-                    for (int c = 0; c < kQuarter; c += 4) {
-                        const float4 m = ref4[c / 4];
-                        const float x0 = ex2(s[c] + m.x), x1 = ex2(s[c + 1] + m.y);
-                        const float x2 = ex2(s[c + 2] + m.z), x3 = ex2(s[c + 3] + m.w);
-                        l2[c / 2] = f2_add(l2[c / 2], f2_pack(__float_as_uint(x0), __float_as_uint(x1)));
-                        l2[c / 2 + 1] = f2_add(l2[c / 2 + 1], f2_pack(__float_as_uint(x2), __float_as_uint(x3)));
-                        w[c / 2] = pack16x2(x0, x1, kF16);
-                        w[c / 2 + 1] = pack16x2(x2, x3, kF16);
+                        for (int c = 0; c < kQuarter; c += 4) {
+                            const float4 m = ref4[c / 4];
+                            s[c] += m.x;
+                            s[c + 1] += m.y;
+                            s[c + 2] += m.z;
+                            s[c + 3] += m.w;
+                        }
+                        write_p();
                     }
-                    const int at = (int)(g % L::kPBuffers) * (N * 2) + first * 2;  // byte of the row, 16-byte groups swizzled
-                    if constexpr (kQuarter == 4) {
-                        *reinterpret_cast<uint2*>(p_row + ((((at >> 4) ^ (key & 7)) << 4) | (at & 15))) = make_uint2(w[0], w[1]);
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < kQuarter / 8; ++u)
-                            *reinterpret_cast<uint4*>(p_row + ((((at >> 4) + u) ^ (key & 7)) << 4)) =
-                                make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
                 }
-                const int live = pc.len - p * kPage;
-                if (live < kPage && (live & 15) != 0 && !bad) {
-                    // 0 * NaN would poison the product: in the last group of 16 keys the rows past the last key are zeroed
-                    // (the page has landed and S is made of it)
-                    for (int w = (int)threadIdx.x - 64; w < (16 - (live & 15)) * 64; w += 32 * kSoftmaxWarps) {
-                        const int box = (w >> 3) & 7, i = w & 7;  // 16 bytes of a row of a box
-                        const uint32_t stage = (g * kPageStages + box / 2) % kStages;
-                        *reinterpret_cast<uint4*>(sm + L::kRingOff + stage * (2 * kBox) + (box & 1) * kBox +
-                                                  (live + (w >> 6)) * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_PF + (g & 1)]);
+                // (the sums while O's MMAs run)
+                if (columns > 0)
+#pragma unroll
+                    for (int c = 0; c < kQuarter / 2; ++c)
+                        l2[c] = f2_add(l2[c], f2_pack(__float_as_uint(s[2 * c]), __float_as_uint(s[2 * c + 1])));
             }
             if (n > 0) bad = bar_or(bar_id, 128, bad);
             if (bad) break;
