@@ -46,12 +46,12 @@
 // heads more than the memory's rate asks of the tensor cores at N = 64, where an
 // MMA reads 6 KB of shared memory for 34 cycles of products (48 at 128 B a
 // cycle): 1920 cycles a page and block, against 1500 for the memory's share of an
-// SM.  Measured, 64 sequences of 1-4096 keys, 128 heads, bf16: 60.0 us, 6 of them
-// the merge, about 2400 cycles a page (shared memory has room for two: a page's
-// turn is its load, 1150 cycles, S, the softmax, 1000, and O, in 4800 for two), 6 us the start (launch, dealing, first
-// page) and 4700 cycles the output of a piece; 32 of 64-16384 keys, 16 heads, two
-// tokens each: 59.6 us (287 MB, 4.8 TB/s, 5.9 while pages stream).  One sequence
-// of 777 keys, 128 heads: 12.9 us.
+// SM.  Measured, 64 sequences of 1-4096 keys, 128 heads, bf16: 60 us, 6 of them
+// the merge, 6 the start (launch, dealing, first page), about 2400 cycles a page
+// (shared memory has room for two, and two take 4800: load 1150, S, softmax 1000,
+// O) and 4700 cycles the output of a piece.  32 sequences of 64-16384 keys, 16
+// heads, two tokens each: 59.1 us (287 MB, 4.8 TB/s; 6.6, the memory's copy rate,
+// while pages stream).  One sequence of 777 keys, 128 heads: 11.8 us.
 #include "pa_launch.h"
 #include "pa_mla.h"
 #include "pa_ptx.cuh"
@@ -696,12 +696,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!whole && pc.lo == 0) {
-                merge = MlaMerge{pc.b, blk, (pc.at + kFixed + pc.pages - 1) / sh.share - range + 1, range};
+            if (pc.lo == 0) {  // (at most one piece of a CTA is the first of several)
+                const MlaMerge m{pc.b, blk, whole ? 0 : (pc.at + kFixed + pc.pages - 1) / sh.share - range + 1, range};
+                if (a.few && threadIdx.x == 64) a.merges[pc.b * blocks + blk] = m;
+                if (!whole) merge = m;
             }
             tc_fence_before();
         }
-        if (threadIdx.x == 64 && a.ranges > 1) a.merges[blockIdx.x] = merge;
+        if (threadIdx.x == 64 && a.ranges > 1 && !a.few) a.merges[blockIdx.x] = merge;
         ok = !bad;
     }
     if (!ok) {
@@ -719,53 +721,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merge of split items: with a piece's references r_s, sums l_s and accumulators o_s (in units of 2^r_s),
 //   out = sum_s 2^(r_s - m) o_s / sum_s 2^(r_s - m) l_s,  lse = m ln 2 + ln of that sum,  m = max_s r_s.
-// A warp takes a row, or where sequences are few and their pieces many a quarter of it (gridDim.z 4).  Bound by the
-// partials, 2 KB a row and piece out of L2, and by its launch: 40 MB in 6 us for 64 sequences and 128 heads; 8 rows a
-// CTA took 0.3 us longer.
-constexpr int kMergeRows = 4;
-template <int N, bool kF16, int kColumns>
-__global__ void __launch_bounds__(kMergeRows * 32) mla_merge_kernel(const __grid_constant__ MlaDecodeArgs a) {
+// Bound by the partials, 2 KB a row and piece out of L2, and by its launch: 40 MB in 6 us for 64 sequences and 128 heads.
+// A warp takes a row, a CTA four; blockIdx.y is the attention kernel's CTA.  Where sequences are few (kFew) their pieces
+// are many: the CTA's warps share the pieces of a quarter of a row, and blockIdx.y is (sequence, block).  One sequence of
+// 131072 keys, 16 heads, is 152 pieces a row: a call takes 41 us, with a warp a quarter of a row 58.  64 sequences take
+// 65 us that way against 60, with four pieces ahead instead of two 60.8.
+constexpr int kMergeWarps = 4;
+template <int N, bool kF16, bool kFew>
+__global__ void __launch_bounds__(kMergeWarps * 32) mla_merge_kernel(const __grid_constant__ MlaDecodeArgs a) {
+    constexpr int kVecs = kFew ? 1 : kMlaLatent / 128;  // of 4 columns a lane
+    constexpr int kAhead = kFew ? 8 : N > 32 ? 2 : 4;  // pieces whose accumulators are on their way
+    __shared__ float top_sh[kMergeWarps], sum_sh[kMergeWarps];
+    __shared__ __align__(16) float acc_sh[kMergeWarps][128];
     grid_dependency_wait();
+    allow_dependents_launch();
     const MlaMerge m = a.merges[blockIdx.y];
-    if (m.pieces == 0) return;
-    constexpr int kVecs = kColumns / 128, kAhead = 2;
     const int blocks = (a.rows + N - 1) / N;
-    const int lane = threadIdx.x & 31;
-    const int in_block = (int)blockIdx.x * kMergeRows + (int)(threadIdx.x >> 5);
+    // (after a call that ended at its wait limit an entry may be another call's)
+    if (m.pieces <= 0 || m.first < 0 || m.pieces > a.ranges - m.first || (unsigned)m.blk >= (unsigned)blocks ||
+        (unsigned)m.b >= (unsigned)a.batch)
+        return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int in_block = kFew ? (int)blockIdx.x : (int)blockIdx.x * kMergeWarps + warp;
     const int in_seq = m.blk * N + in_block;
-    if (in_block >= N || in_seq >= a.rows) return;
+    if (in_block >= N || in_seq >= a.rows) return;  // (all of a CTA's warps, or with kFew 0 none that others wait for)
+    const int per = kFew ? (m.pieces + kMergeWarps - 1) / kMergeWarps : m.pieces;
+    const int from = kFew ? min(warp * per, m.pieces) : 0, to = min(from + per, m.pieces);
     auto slot = [&](int s) { return (long long)(2 * (m.first + s) + (s == 0)) * blocks + m.blk; };  // of the s-th piece
     auto ref_of = [&](int s) { return a.ref_part[slot(s) * kMlaBlockRows + in_block]; };
-    const int column = lane * 4 + (int)blockIdx.z * kColumns;
+    const int column = lane * 4 + (kFew ? (int)blockIdx.z * 128 : 0);
     const float* part = a.o_part + (long long)in_block * kMlaLatent + column;
     // the first pieces' accumulators on their way while their weights are found
     float4 v[kAhead][kVecs];
-    auto load = [&](float4 (&to)[kVecs], int s) {
+    auto load = [&](float4 (&to_v)[kVecs], int s) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
-            to[i] = *reinterpret_cast<const float4*>(part + slot(s) * (kMlaBlockRows * kMlaLatent) + i * 128);
+            to_v[i] = *reinterpret_cast<const float4*>(part + slot(s) * (kMlaBlockRows * kMlaLatent) + i * 128);
     };
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) load(v[s], min(s, m.pieces - 1));
+    for (int s = 0; s < kAhead; ++s)
+        if (from + s < to) load(v[s], from + s);
     float top = -INFINITY;
-    for (int s = lane; s < m.pieces; s += 32) top = fmaxf(top, ref_of(s));
+    for (int s = from + lane; s < to; s += 32) top = fmaxf(top, ref_of(s));
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if constexpr (kFew) {
+        if (lane == 0) top_sh[warp] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(top_sh[0], top_sh[1]), fmaxf(top_sh[2], top_sh[3]));
+    }
     const float minus_top = top == -INFINITY ? 0.f : -top;
     float sum = 0.f;
     float4 acc[kVecs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < m.pieces; s0 += 32) {
+    for (int s0 = from; s0 < to; s0 += 32) {
         float weight = 0.f;  // of piece s0 + lane
-        if (s0 + lane < m.pieces) {
+        if (s0 + lane < to) {
             weight = ex2(ref_of(s0 + lane) + minus_top);
             float l = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) l += a.sum_part[(slot(s0 + lane) * 4 + i) * kMlaBlockRows + in_block];
             sum = fmaf(weight, l, sum);
         }
-        const int count = min(32, m.pieces - s0);
+        const int count = min(32, to - s0);
         for (int s = 0; s < count; s += kAhead) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
@@ -778,14 +797,26 @@ __global__ void __launch_bounds__(kMergeRows * 32) mla_merge_kernel(const __grid
                     acc[i].z = fmaf(w, v[j][i].z, acc[i].z);
                     acc[i].w = fmaf(w, v[j][i].w, acc[i].w);
                 }
-                if (s0 + s + j + kAhead < m.pieces) load(v[j], s0 + s + j + kAhead);
+                if (s0 + s + j + kAhead < to) load(v[j], s0 + s + j + kAhead);
             }
         }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long orow = (long long)m.b * a.rows + in_seq;
+    if constexpr (kFew) {
+        if (lane == 0) sum_sh[warp] = sum;
+        *reinterpret_cast<float4*>(&acc_sh[warp][lane * 4]) = acc[0];
+        __syncthreads();
+        if (warp != 0) return;
+        sum = (sum_sh[0] + sum_sh[1]) + (sum_sh[2] + sum_sh[3]);
+#pragma unroll
+        for (int w = 1; w < kMergeWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(&acc_sh[w][lane * 4]);
+            acc[0] = make_float4(acc[0].x + x.x, acc[0].y + x.y, acc[0].z + x.z, acc[0].w + x.w);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint16_t* out = a.out + orow * kMlaLatent + column;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
@@ -806,15 +837,15 @@ cudaError_t launch(MlaDecodeArgs& a, int sms, const CUtensorMap* maps, cudaStrea
     // as many ranges as there are SMs for them, and no more than the longest lengths could give one each
     const long long most = ((long long)a.batch * (kFixed + a.max_pages) + kMinShare - 1) / kMinShare;
     a.ranges = (int)max(1ll, min((long long)sms / blocks, most));
+    a.few = 8ll * a.batch <= a.ranges;  // (an item may then have more than 8 pieces, and entries by sequence fit)
     const unsigned ctas = (unsigned)(a.ranges * blocks);
     e = launch_overlapped(kernel, dim3(ctas), dim3(kThreads), smem, stream, a, maps[0], maps[1], maps[2]);
     if (e != cudaSuccess || a.ranges == 1) return e;
-    const unsigned groups = (unsigned)((min(a.rows, N) + kMergeRows - 1) / kMergeRows);
-    const dim3 block(kMergeRows * 32);
-    // an item has many pieces where it is one of few: rows of which a warp would read 150 pieces alone
-    if (8 * a.batch <= a.ranges)
-        return launch_overlapped(mla_merge_kernel<N, kF16, 128>, dim3(groups, ctas, 4), block, 0, stream, a);
-    return launch_overlapped(mla_merge_kernel<N, kF16, 512>, dim3(groups, ctas), block, 0, stream, a);
+    const unsigned rows = (unsigned)min(a.rows, N);
+    const dim3 block(kMergeWarps * 32);
+    if (a.few)
+        return launch_overlapped(mla_merge_kernel<N, kF16, true>, dim3(rows, (unsigned)(a.batch * blocks), kMlaLatent / 128), block, 0, stream, a);
+    return launch_overlapped(mla_merge_kernel<N, kF16, false>, dim3((rows + kMergeWarps - 1) / kMergeWarps, ctas), block, 0, stream, a);
 }
 
 template <bool kF16>

@@ -32,11 +32,11 @@ struct MlaDecodeArgs {
     float* o_part;     // fp32 [2 * ranges * blocks, 64, 512]
     float* ref_part;   // fp32 [2 * ranges * blocks, 64]
     float* sum_part;   // fp32 [2 * ranges * blocks, 4, 64]
-    MlaMerge* merges;  // [ranges * blocks]
+    MlaMerge* merges;  // [ranges * blocks]: of the CTA's split item, or where few is set of (sequence, block)
     int* status;
     int32_t batch, rows, q_len, num_heads, max_pages, num_pool_pages;
     int32_t f16;
-    int32_t ranges;  // set by the launch
+    int32_t ranges, few;  // set by the launch
     float scale_log2;
     uint64_t wait_ns;
 };
