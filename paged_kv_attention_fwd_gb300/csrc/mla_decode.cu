@@ -46,10 +46,10 @@
 // heads more than the memory's rate asks of the tensor cores at N = 64, where an
 // MMA reads 6 KB of shared memory for 34 cycles of products (48 at 128 B a
 // cycle): 1920 cycles a page and block, against 1500 for the memory's share of an
-// SM.  Measured, 64 sequences of 1-4096 keys, 128 heads, bf16: 60 us, 6 of them
+// SM.  Measured, 64 sequences of 1-4096 keys, 128 heads, bf16: 58.7 us, 6 of them
 // the merge, 6 the start (launch, dealing, first page), about 2400 cycles a page
 // (shared memory has room for two, and two take 4800: load 1150, S, softmax 1000,
-// O) and 4700 cycles the output of a piece.  32 sequences of 64-16384 keys, 16
+// O) and the outputs of pieces.  32 sequences of 64-16384 keys, 16
 // heads, two tokens each: 59.1 us (287 MB, 4.8 TB/s; 6.6, the memory's copy rate,
 // while pages stream).  One sequence of 777 keys, 128 heads: 11.8 us.
 #include "pa_launch.h"
@@ -67,9 +67,10 @@ constexpr int kRopeStages = 2, kMaxStages = 11;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kListed = 16;  // sequences of a CTA's range whose pieces are found at its start
 constexpr int kThreads = 96 + 32 * kSoftmaxWarps;
-// What an item costs besides its pages, in pages (64 sequences of 1-4096 keys: 62.5 us a call with 4, 61.5 with 5, 63 with
-// 6), and the shortest range (one sequence of 777 keys: 17.1 us with 6, 14.0 with 3, 13.0 with 2, 13.3 with 1).
-constexpr int kFixed = 5;
+// What an item costs besides its pages, in pages (64 sequences of 1-4096 keys: 58.7 us a call with 3, 58.3 with 4, 59.5
+// with 5; one of 777: 11.8, 13.1 and 11.8), and the shortest range (one sequence of 777 keys: 17.1 us with 6, 14.0 with 3,
+// 13.0 with 2, 13.3 with 1, of which the output and the merge took one more than now).
+constexpr int kFixed = 3;
 constexpr int kMinShare = 2;
 
 template <int N>
@@ -674,25 +675,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int element = q4 * 32 + lane;
                 uint16_t* out = a.out + (row0 + half * kHalf) * kMlaLatent + element;
                 float* part = a.o_part + (slot * kMlaBlockRows + half * kHalf) * kMlaLatent + element;
-#pragma unroll 1
-                for (int i = 0; i < kPageStages; ++i) {
-                    uint32_t o[kHalf];
-                    if (n > 0) {
+                const float* by = &sh.factor[half * kHalf];
+                bool plain = n > 0 && columns == kHalf;
+                if (whole && plain) plain = __all_sync(0xffffffffu, lane >= kHalf || by[lane % kHalf] != 0.f);
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < kPageStages; ++i) {
+                        uint32_t o[kHalf];
                         tmem_ld_cols<kHalf>(tbase + lane_addr + L::kOCol + i * N + half * kHalf, o);
                         tmem_ld_wait();
                         reg_fence(o);
+                        if (whole) {
+#pragma unroll
+                            for (int c = 0; c < kHalf; ++c)
+                                out[c * kMlaLatent + i * 128] = (uint16_t)pack16x2(__uint_as_float(o[c]) * by[c], 0.f, kF16);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < kHalf; ++c) part[c * kMlaLatent + i * 128] = __uint_as_float(o[c]);
+                        }
                     }
-                    if (whole) {
+                } else {  // columns that are not there, or see nothing (whatever the rows hold)
+#pragma unroll 1
+                    for (int i = 0; i < kPageStages; ++i) {
+                        uint32_t o[kHalf];
+                        if (n > 0) {
+                            tmem_ld_cols<kHalf>(tbase + lane_addr + L::kOCol + i * N + half * kHalf, o);
+                            tmem_ld_wait();
+                            reg_fence(o);
+                        }
 #pragma unroll
                         for (int c = 0; c < kHalf; ++c) {
-                            const float f = n > 0 ? sh.factor[half * kHalf + c] : 0.f;
-                            const float y = f == 0.f ? 0.f : __uint_as_float(o[c]) * f;
-                            if (c < columns) out[c * kMlaLatent + i * 128] = (uint16_t)pack16x2(y, 0.f, kF16);
+                            if (c >= columns) continue;
+                            if (whole) {
+                                const float y = n == 0 || by[c] == 0.f ? 0.f : __uint_as_float(o[c]) * by[c];
+                                out[c * kMlaLatent + i * 128] = (uint16_t)pack16x2(y, 0.f, kF16);
+                            } else {
+                                part[c * kMlaLatent + i * 128] = __uint_as_float(o[c]);
+                            }
                         }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kHalf; ++c)
-                            if (c < columns) part[c * kMlaLatent + i * 128] = __uint_as_float(o[c]);
                     }
                 }
             }
