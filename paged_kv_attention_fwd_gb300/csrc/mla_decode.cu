@@ -49,9 +49,9 @@
 // SM.  Measured, 64 sequences of 1-4096 keys, 128 heads, bf16: 58.7 us, 6 of them
 // the merge, 6 the start (launch, dealing, first page), about 2400 cycles a page
 // (shared memory has room for two, and two take 4800: load 1150, S, softmax 1000,
-// O) and the outputs of pieces.  32 sequences of 64-16384 keys, 16
-// heads, two tokens each: 59.1 us (287 MB, 4.8 TB/s; 6.6, the memory's copy rate,
-// while pages stream).  One sequence of 777 keys, 128 heads: 11.8 us.
+// O) and the outputs of pieces.  32 sequences of 64-16384 keys, 16 heads, two
+// tokens each: 59 us (287 MB, 4.9 TB/s; 6.6, the memory's copy rate, while pages
+// stream).  One sequence of 777 keys, 128 heads: 11.8 us.
 #include "pa_launch.h"
 #include "pa_mla.h"
 #include "pa_ptx.cuh"
