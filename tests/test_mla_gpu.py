@@ -482,6 +482,18 @@ def test_captured_decode_follows_new_lengths_tables_and_queries():
         check_decode(c, q, SCALE, out, lse)
 
 
+def test_calls_of_other_shapes_share_a_dirty_workspace():
+    """One after the other: few long sequences, many short ones, none with a key, one block and several."""
+    cases = [([9000], 128), ([70, 0, 5000] + [3] * 60, 16), ([0, 0, 0], 40), ([4000, 1], 20), ([65] * 20, 128), ([9000], 128)]
+    caches = [Cache(lens, "bf16", seed=20 + i, width=150) for i, (lens, _) in enumerate(cases)]
+    need = max(B.pa_mla_decode_workspace_size(c.shapes(h)) for c, (_, h) in zip(caches, cases))
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    ws[:B.PA_STATUS_BYTES] = 0
+    for c, (lens, h) in zip(caches, cases):
+        q = normal((len(lens), h, 576), 1)
+        check_decode(c, q, SCALE, *decode(c, q, workspace=ws))
+
+
 def test_two_streams_with_their_own_workspaces():
     caches = [Cache([1500, 900, 30], seed=i) for i in (1, 2)]
     qs = [normal((3, 64, 576), i) for i in (3, 4)]
