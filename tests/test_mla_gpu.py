@@ -482,6 +482,28 @@ def test_captured_decode_follows_new_lengths_tables_and_queries():
         check_decode(c, q, SCALE, out, lse)
 
 
+def test_pages_past_two_to_the_31_elements():
+    """A 5 GB pool: rows appended behind 2^31 elements (2^32 bytes), attended over and read back."""
+    pages, n, heads = 70000, 200, 24
+    pool = torch.full((pages, 64, 576), float("nan"), dtype=torch.bfloat16, device=DEV)
+    table = ints([[pages - 1, 59000, 58500, pages - 7]])
+    kv = normal((n, 576), 1)
+    sh = ops.mla_cache_shapes(1, 4, pages, n, norm=False)
+    ok(ops.mla_append_kv(sh, kv, ints([0, n]), ints([0]), table, pool))
+    assert torch.equal(pool.view(-1, 576)[rows_at(table, 0, 0, n)], kv)
+    latent, rope, ws = ops.mla_gather_kv(sh, pool, ints([0, n]), ints([0]), table)
+    ok(ws)
+    assert torch.equal(latent, kv[:, :512]) and torch.equal(rope[:, 0], kv[:, 512:])
+    q = normal((1, heads, 576), 2)
+    out, lse, ws = ops.mla_decode(ops.mla_decode_shapes(1, heads, 4, pages), q, pool, table, ints([n]), SCALE)
+    ok(ws)
+    near_pages = Cache([n], "bf16")  # the same rows in pages at the front
+    near_pages.pool.view(-1, 576)[rows_at(near_pages.table, 0, 0, n)] = kv
+    want = decode(near_pages, q)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    check_decode(near_pages, q, SCALE, out, lse)
+
+
 def test_calls_of_other_shapes_share_a_dirty_workspace():
     """One after the other: few long sequences, many short ones, none with a key, one block and several."""
     cases = [([9000], 128), ([70, 0, 5000] + [3] * 60, 16), ([0, 0, 0], 40), ([4000, 1], 20), ([65] * 20, 128), ([9000], 128)]
