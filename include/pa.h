@@ -738,7 +738,7 @@ typedef struct {
  * merge:
  *   s_j = scale <q[b q_len + i, h], row_j>   (576 elements),  j < seq_lens[b] - (q_len - 1 - i)
  *   out = sum_j softmax_j(s) row_j[0:512],   lse = ln sum_j exp(s_j)
- * A token that sees no key has out = 0 and lse = -inf.
+ * A token that sees no key, or whose scores are all -inf, has out = 0 and lse = -inf.
  *   q          [B q_len, H, 576]    (pa_mla_query's output)
  *   pool       [num_pool_pages, 64, 576]; rows at or past seq_lens[b] and table entries
  *              past ceil(seq_lens[b] / 64) are never used, whatever they hold

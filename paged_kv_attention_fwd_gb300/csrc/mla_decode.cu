@@ -29,9 +29,10 @@
 // The softmax's reference is not each key's running maximum but one value a
 // column, which changes only when a score exceeds it by more than 2^8.  P is
 // written with the references as they are, and then the four warps of a column
-// agree whether one was exceeded; if so, and in an item's first page, the columns'
-// maxima over the page are found, the accumulators rescaled and P written again
-// (with the vote before P a call took 61.2 us, with it after 60.0).
+// agree whether one was exceeded; if so, in an item's first page, and as long as a
+// column has seen scores of -inf only, the columns' maxima over the page are found,
+// the accumulators rescaled and P written again (with the vote before P a call took
+// 61.2 us, with it after 60.0).
 //
 // The sequences' costs (pages and a constant) are laid end to end and cut into
 // equal ranges, as many as there are CTAs a block: a CTA takes what lies in its
@@ -479,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (next_piece()) {
             const int n = pc.hi - pc.lo;
             float ref = -INFINITY;  // of the column to keep
+            bool open = false;      // a column of the half has no reference yet: its scores so far were all -inf
             if (n > 0) {
                 if (tid < kHalf) {
                     const int tok = min(blk * N + column, a.rows - 1) / a.num_heads;
@@ -545,8 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto passed = [&](uint32_t behind) {  // O's MMAs of the page that many before this one
                     return g < behind || wait(&bars[B_OD + ((g - behind) & 1)], ((g - behind) >> 1) & 1);
                 };
-                // ---- P with the references as they are, and then: did a score exceed its own?
-                bool change = p == pc.lo;
+                // ---- P with the references as they are, and then: did a score exceed its own?  (With a column that has none,
+                // any score above -inf does: the page's maxima are looked at without asking.)
+                bool change = p == pc.lo || open;
                 if (!change) {
                     float top = -INFINITY;
                     if (columns > 0 && __all_sync(0xffffffffu, !bad)) {
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sh.minus_ref[column] = ref == -INFINITY ? 0.f : -ref;
                         sh.factor[column] = factor;
                     }
-                    bar_or(bar_id, 128, false);
+                    open = bar_or(bar_id, 128, tid < columns && ref == -INFINITY);
                     const bool rescale = p > pc.lo;
                     bad = !passed(rescale ? 1 : L::kPBuffers);
                     if (columns > 0 && __all_sync(0xffffffffu, !bad)) {

@@ -1,0 +1,129 @@
+"""Softmax weights of the latent decode where they can go wrong: keys whose
+scores are -inf, page after page and for some heads only; fp16 weights far
+below a dominant key's; long sequences whose every page shows in the output.
+All against fp64 on the GPU."""
+import math
+
+import pytest
+import torch
+
+from paged_kv_attention_fwd_gb300 import binding as B
+from paged_kv_attention_fwd_gb300 import ops
+
+from .test_mla_gpu import DEV, HALF, SCALE, T16, TINY, Cache, decode, gen, gpu, normal, rows_at  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# The least step of a weight, half of it, relative to the largest weight: fp16's 2^-25
+LEAST = {"bf16": 0.0, "f16": 2.0 ** -25}
+
+
+def check(c, q, scale, out, lse, seen, terms=576, depth=None):
+    """One token a sequence.  seen[b]: [heads, keys], which keys have a score above -inf; terms: products of a score that
+    are not zero; depth: additions that a key's share goes through (all keys of a sequence at most)."""
+    for b, n in enumerate(c.lens):
+        k, live = c.rows(b), seen[b]
+        k = torch.where(torch.isfinite(k), k, 0.0)
+        v = k[:, :512]
+        s = torch.where(live, q[b].double() @ k.T * scale, -math.inf)
+        none = ~live.any(-1)
+        assert (out[b, none] == 0).all() and (lse[b, none] == -math.inf).all(), b
+        reach = torch.where(live, q[b].double().abs() @ k.abs().T * abs(scale), 0.0).amax(-1)
+        want = torch.logsumexp(s, -1)
+        p = torch.exp(s - torch.where(none, 0.0, want)[:, None])
+        o, spread = p @ v, p @ v.abs()
+        # a score: its fp32 products and the steps up to the exponent (2^-23 of its reach each), the exponential 2^-21;
+        # fp32 sums of values and of weights, 2^-23 an addition (truncation included)
+        sums = min(n, depth or n) * 2.0 ** -23
+        logit = (terms + 4) * 2.0 ** -23 * reach + 2.0 ** -21
+        rounded = torch.maximum(HALF[c.dtype] * p, LEAST[c.dtype] * p.amax(-1, keepdim=True)) * live
+        tol = HALF[c.dtype] * o.abs() + rounded @ v.abs() + (2 * logit[:, None] + 2 * sums) * spread + TINY[c.dtype]
+        assert torch.isfinite(out[b]).all()
+        off = (out[b].double() - o).abs()
+        assert (off <= tol).all(), (b, (off / tol).max().item(), (off / tol).amax(-1).argmax().item())
+        ltol = logit + sums + 2.0 ** -22 * (want.abs() + 1)
+        off = (lse[b].double() - want).abs()
+        assert (off[~none] <= ltol[~none]).all(), (b, (off / ltol)[~none].max().item())
+
+
+# ----------------------------------------------------------------- scores of -inf
+
+LAYOUTS = {  # lengths, SMs
+    "whole": ([700, 100, 320], 1),      # one range: no sequence is split
+    "few": ([3000], None),              # a sequence over many SMs
+    "many": ([700, 64, 333] * 10, 60),  # split, and too many sequences for the other merge
+}
+
+
+def hidden_case(layout, heads, first, dtype, every, rising, value):
+    lens, sms = LAYOUTS[layout]
+    c = Cache(lens, dtype, seed=max(first, 0))
+    q = normal((len(lens), heads, 576), 1, dtype)
+    hides = torch.arange(heads, device=DEV) % every == 0
+    q[:, :, 575] = torch.where(hides, 4.0, 0.0).to(T16[dtype])
+    seen = []
+    for b, n in enumerate(lens):
+        at = rows_at(c.table, b, 0, n)
+        gone = torch.arange(n, device=DEV) < (n - 70 if first < 0 else first)
+        c.pool.view(-1, 576)[at, 575] = torch.where(gone, value, 0.0).to(T16[dtype])
+        if rising:
+            c.pool.view(-1, 576)[at, 574] = (torch.arange(n, device=DEV) // 50).to(T16[dtype])
+        seen.append(~(gone & hides[:, None]))
+    if rising:  # 2^1.5 every 50 keys: some columns' references change now and again
+        q[:, :, 574] = torch.where(torch.arange(heads, device=DEV) % 5 < 2, 14.0, 0.0).to(T16[dtype])
+    return c, q, seen, sms
+
+
+@pytest.mark.parametrize("rising", [False, True])
+@pytest.mark.parametrize("first", [64, 128, 130, -1])
+@pytest.mark.parametrize("heads", [5, 32, 64, 100])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_a_prefix_hidden_from_some_heads(layout, heads, first, rising):
+    """The first keys (-1: all but 70) at bf16's lowest value in one element, times 4: a product of -inf."""
+    c, q, seen, sms = hidden_case(layout, heads, first, "bf16", 3, rising, torch.finfo(torch.bfloat16).min)
+    check(c, q, SCALE, *decode(c, q, sms=sms), seen)
+
+
+@pytest.mark.parametrize("rising", [False, True])
+@pytest.mark.parametrize("first", [64, 130, -1, 10000])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_prefix_hidden_from_all_heads(dtype, layout, first, rising):
+    """Keys of -inf; with 10000 no key of any sequence is left."""
+    c, q, seen, sms = hidden_case(layout, 16, first, dtype, 1, rising, -math.inf)
+    check(c, q, SCALE, *decode(c, q, sms=sms), seen)
+
+
+@pytest.mark.parametrize("later", [-200.0, -3.0, 0.0, 5.0, 40.0])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_scores_behind_a_hidden_prefix(layout, later):
+    """Far below 1, near it and above it, in units of e."""
+    lens, sms = LAYOUTS[layout]
+    c = Cache(lens, "bf16", seed=2)
+    q = normal((len(lens), 20, 576), 1)
+    q[:, :, 575], q[:, :, 574] = 4.0, 1.0
+    seen = []
+    for b, n in enumerate(lens):
+        at = rows_at(c.table, b, 0, n)
+        gone = torch.arange(n, device=DEV) < min(200, n - 1)
+        c.pool.view(-1, 576)[at, 575] = torch.where(gone, -math.inf, 0.0).bfloat16()
+        c.pool.view(-1, 576)[at, 574] = later / SCALE
+        seen.append((~gone).expand(20, -1))
+    check(c, q, SCALE, *decode(c, q, sms=sms), seen)
+
+
+@pytest.mark.parametrize("q_len", [2, 4])
+def test_a_hidden_prefix_and_several_tokens(q_len):
+    """Hidden keys and those that a token does not see yet: each token as it is alone over its own keys."""
+    lens, heads = [500, 131, 70, 64 + q_len], 16
+    c = Cache(lens, "bf16", seed=3)
+    q = normal((len(lens) * q_len, heads, 576), 1)
+    q[:, :, 575] = 4.0
+    for b, n in enumerate(lens):
+        c.pool.view(-1, 576)[rows_at(c.table, b, 0, n), 575] = torch.where(torch.arange(n, device=DEV) < 64, -math.inf, 0.0).bfloat16()
+    out, lse = decode(c, q, q_len)
+    for i in range(q_len):
+        c.lens = [n - (q_len - 1 - i) for n in lens]
+        at = torch.arange(len(lens), device=DEV) * q_len + i
+        seen = [(torch.arange(n, device=DEV) >= 64).expand(heads, -1) for n in c.lens]
+        check(c, q[at], SCALE, out[at], lse[at], seen)
