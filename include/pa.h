@@ -752,7 +752,8 @@ typedef struct {
  * A length below 0 counts as 0, one past max_pages_per_seq * 64 as that many keys,
  * a page id outside the pool as page 0; each is recorded as PA_ERR_DEVICE_BOUNDS.
  * With fp16 and bf16 rows alike the softmax weights are rounded to the rows' type
- * before they are multiplied; sums are fp32.  A NaN or an infinity in a row that a
+ * before they are multiplied; fp16 ones are off by up to 2^-32 of the largest where
+ * they lie below 2^-21 of it.  Sums are fp32.  A NaN or an infinity in a row that a
  * sequence holds reaches the outputs of all its q_len tokens, of one that does not
  * see the row yet too (weight 0 times it).  num_q_heads * q_len <= 65536 and
  * batch * (max_pages_per_seq + 16) < 2^31.

@@ -40,8 +40,13 @@
 // workspace in fp32, with their references and sums, and are merged by a second
 // kernel.  Lengths are read on the device only.
 //
-// P is rounded to the rows' type (half a step, 2^-9 or 2^-12 of a weight), as an
-// operand of the second product has to be; its sum is taken before, in fp32.
+// P is rounded to the rows' type, as an operand of the second product has to be;
+// its sum is taken before, in fp32.  That is half a step of bf16, 2^-8 of a weight,
+// or of fp16, 2^-11 of one.  fp16 has few exponents: there P is 2^7 times the weight
+// beside the reference, so that a weight keeps all its bits down to 2^-21 of the
+// reference's, half a step is 2^-32 of that below, and what is less than 2^-32 of it
+// vanishes (without the factor 2^-14 and 2^-25: 131072 keys at 2^-25 of one lost
+// their 0.4% of the output).
 //
 // What bounds it.  A byte of a row meets 2 x heads x 1.9 operations: with 128
 // heads more than the memory's rate asks of the tensor cores at N = 64, where an
@@ -73,6 +78,8 @@ constexpr int kThreads = 96 + 32 * kSoftmaxWarps;
 // 13.0 with 2, 13.3 with 1, of which the output and the merge took one more than now).
 constexpr int kFixed = 3;
 constexpr int kMinShare = 2;
+// fp16 weights are held as 2^7 times those beside the reference: at most 2^15, and whole steps of fp16 down to 2^-21 of it.
+constexpr float kShiftF16 = 7.f;
 
 template <int N>
 struct Layout {
@@ -179,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap map_latent, const __grid_constant__ CUtensorMap map_rope) {
     using L = Layout<N>;
     constexpr int kHalf = L::kHalf, kQuarter = L::kQuarter, kStages = L::kStages;
+    constexpr float kShift = kF16 ? kShiftF16 : 0.f;
     struct Small {
         uint64_t bars[B_COUNT];
         Walk start;            // where the walk goes on behind the pieces listed here
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         while (next_piece()) {
             const int n = pc.hi - pc.lo;
-            float ref = -INFINITY;  // of the column to keep
+            float ref = -INFINITY;  // of the column to keep: what its weights are in units of (2^kShift below the maximum it was set by)
             bool open = false;      // a column of the half has no reference yet: its scores so far were all -inf
             if (n > 0) {
                 if (tid < kHalf) {
@@ -570,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (columns > 0 && __all_sync(0xffffffffu, !bad)) write_p();
                     fence_proxy_async_smem();
                     tc_fence_before();
-                    change = bar_or(bar_id, 128, bad || top > kRescaleThreshold);
+                    change = bar_or(bar_id, 128, bad || top > kRescaleThreshold + kShift);
                 }
                 if (change) {
                     // ---- the columns' maxima over the page, new references, O rescaled, P with those
@@ -591,9 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float most = fmaxf(fmaxf(sh.part[0][column], sh.part[1][column]),
                                                  fmaxf(sh.part[2][column], sh.part[3][column]));
                         float factor = 1.f;
-                        if (most > ref + kRescaleThreshold) {
-                            if (ref != -INFINITY) factor = ex2(ref - most);
-                            ref = most;
+                        if (most - ref > kRescaleThreshold + kShift) {  // (not where both are infinite)
+                            if (ref != -INFINITY) factor = ex2(ref - (most - kShift));
+                            ref = most - kShift;
                         }
                         sh.minus_ref[column] = ref == -INFINITY ? 0.f : -ref;
                         sh.factor[column] = factor;

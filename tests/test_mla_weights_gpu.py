@@ -14,8 +14,8 @@ from .test_mla_gpu import DEV, HALF, SCALE, T16, TINY, Cache, decode, gen, gpu, 
 
 pytestmark = pytest.mark.gpu
 
-# The least step of a weight, half of it, relative to the largest weight: fp16's 2^-25
-LEAST = {"bf16": 0.0, "f16": 2.0 ** -25}
+# Half the least step of a weight, relative to the largest weight: fp16's 2^-25, of weights held 2^7 times larger
+LEAST = {"bf16": 0.0, "f16": 2.0 ** -32}
 
 
 def check(c, q, scale, out, lse, seen, terms=576, depth=None):
@@ -127,3 +127,79 @@ def test_a_hidden_prefix_and_several_tokens(q_len):
         at = torch.arange(len(lens), device=DEV) * q_len + i
         seen = [(torch.arange(n, device=DEV) >= 64).expand(heads, -1) for n in c.lens]
         check(c, q[at], SCALE, out[at], lse[at], seen)
+
+
+# ----------------------------------------------------------------- light weights
+
+def sink_case(n, step, sink_value, dtype, heads=16, at=317):
+    """One key at score 0 and n - 1 others at `step` (in units of 2, rounded to the type), whose values are 1 and a little."""
+    c = Cache([n], dtype, seed=5)
+    rows = rows_at(c.table, 0, 0, n)
+    x = 1 + 0.25 * torch.randn((n, 576), generator=gen(3), device=DEV)
+    x[:, 512:] = 0.0
+    x[:, 512] = step * math.log(2.0)
+    x[at, :512], x[at, 512] = sink_value, 0.0
+    c.pool.view(-1, 576)[rows] = x.to(T16[dtype])
+    q = torch.zeros((1, heads, 576), dtype=T16[dtype], device=DEV)
+    q[..., 512] = 1.0
+    return c, q, [torch.ones((heads, n), dtype=torch.bool, device=DEV)]
+
+
+def share_depth(n, sms):
+    """Additions that a key of a sequence over all SMs goes through: its piece's keys and a page more, and the pieces."""
+    return n // sms + 128 + sms
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("step", [-25.0, -24.6, -20.3])
+@pytest.mark.parametrize("at", [0, 317])
+def test_many_keys_far_below_one(dtype, step, at):
+    n, sms = 131073, ops.num_sms()
+    c, q, seen = sink_case(n, step, 1.0, dtype, at=at)
+    out, lse = decode(c, q, scale=1.0)
+    check(c, q, 1.0, out, lse, seen, 1, share_depth(n, sms))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("step", [-25.0, -24.6])
+def test_many_keys_of_larger_values_far_below_one_in_one_piece(dtype, step):
+    """A sixth of the output comes from keys at 2^-25 of the one beside them, all in one CTA's piece."""
+    n = 131073
+    c, q, seen = sink_case(n, step, 1.0, dtype)
+    rows = rows_at(c.table, 0, 0, n)
+    c.pool.view(-1, 576)[rows[torch.arange(n, device=DEV) != 317], :512] *= 50.0
+    out, lse = decode(c, q, scale=1.0, sms=1)
+    check(c, q, 1.0, out, lse, seen, 1, n // 8)  # (two roundings for each 16 keys)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("share", [0.01, 0.003])
+@pytest.mark.parametrize("sms", [1, 20, None])
+def test_a_long_light_tail_beside_a_key_of_no_value(dtype, share, sms):
+    """The tail's values are all that is left in the output."""
+    n = 65537 if sms is None else 20000
+    c, q, seen = sink_case(n, math.log2(share / (n - 1)), 0.0, dtype)
+    out, lse = decode(c, q, scale=1.0, sms=sms)
+    check(c, q, 1.0, out, lse, seen, 1, share_depth(n, sms or ops.num_sms()))
+
+
+# ----------------------------------------------------------------- long sequences, page by page
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("heads", [8, 20, 128])
+def test_every_page_of_a_long_sequence_shows(dtype, heads):
+    """Page p is all that column p % 512 holds but for pages a multiple of 512 away, whose values are others: a page lost,
+    doubled or taken for another one is off by at least a sixth of its column."""
+    n, sms = 70000, ops.num_sms()
+    c = Cache([n], dtype, seed=6)
+    rows = rows_at(c.table, 0, 0, n)
+    x = torch.zeros((n, 576), device=DEV)
+    page = torch.arange(n, device=DEV) // 64
+    x[torch.arange(n, device=DEV), page % 512] = 2.0 + page // 512
+    x[:, 512:] = torch.randn((n, 64), generator=gen(4), device=DEV)
+    c.pool.view(-1, 576)[rows] = x.to(T16[dtype])
+    q = normal((1, heads, 576), 2, dtype)
+    q[..., :512] = 0.0
+    blocks = -(-heads // (16 if heads <= 16 else 32 if heads <= 32 else 64))
+    seen = [torch.ones((heads, n), dtype=torch.bool, device=DEV)]
+    check(c, q, SCALE, *decode(c, q), seen, 64, share_depth(n, sms // blocks))
