@@ -114,8 +114,9 @@ pa_status check_cache_sizes(const pa_mla_cache_shapes* sh) {
 
 // ------------------------------------------------------------ products
 
-// Checks of both products; fills `a` and the three maps.  in_row, out_row: a
-// head's elements of the input and the output; in_tokens: loaded by one copy.
+// Checks of both products; fills `a` and the maps of the input and the weights.
+// in_row, out_row: a head's elements of the input and the output; in_tokens:
+// loaded by one copy.
 pa_status fill_project(const pa_mla_project_shapes* sh, int in_row, int out_row, uint32_t in_tokens, const void* in,
                        const void* w, void* out, void* workspace, size_t workspace_bytes, pa::MlaProjectArgs* a, CUtensorMap* maps) {
     pa_status st = check_row(sh->latent_dim, sh->rope_dim, sh->dtype);
@@ -150,15 +151,12 @@ pa_status fill_project(const pa_mla_project_shapes* sh, int in_row, int out_row,
     const uint64_t heads = (uint64_t)sh->num_heads;
     const uint64_t id[3] = {(uint64_t)in_row, heads, (uint64_t)sh->total_tokens};
     const uint64_t is[2] = {(uint64_t)in_row * 2, (uint64_t)sh->in_stride * 2};
-    const uint32_t ib[3] = {64, 1, in_tokens}, ob[3] = {64, 1, 128};
+    const uint32_t ib[3] = {64, 1, in_tokens};
     const uint64_t wd[3] = {(uint64_t)pa::kMlaLatent, 128, heads};
     const uint64_t ws[2] = {(uint64_t)pa::kMlaLatent * 2, (uint64_t)sh->w_stride * 2};
     const uint32_t wb[3] = {64, 128, 1};
-    const uint64_t od[3] = {(uint64_t)out_row, heads, (uint64_t)sh->total_tokens};
-    const uint64_t os[2] = {(uint64_t)out_row * 2, (uint64_t)sh->out_stride * 2};
     st = pa::host_map_16(a->f16, &maps[0], in, 3, id, is, ib);
     if (st == PA_OK) st = pa::host_map_16(a->f16, &maps[1], w, 3, wd, ws, wb);
-    if (st == PA_OK) st = pa::host_map_16(a->f16, &maps[2], out, 3, od, os, ob);
     return st;
 }
 
@@ -280,6 +278,10 @@ pa_status pa_mla_query(const pa_mla_project_shapes* sh, const void* q, const voi
     CUtensorMap maps[3];
     pa_status st = fill_project(sh, pa::kMlaNope + pa::kMlaRope, pa::kMlaRow, 128, q, w_uk, q_out, workspace, workspace_bytes,
                                 &a, maps);
+    const uint64_t od[3] = {(uint64_t)pa::kMlaRow, (uint64_t)sh->num_heads, (uint64_t)sh->total_tokens};
+    const uint64_t os[2] = {(uint64_t)pa::kMlaRow * 2, (uint64_t)sh->out_stride * 2};
+    const uint32_t ob[3] = {64, 1, 128};
+    if (st == PA_OK) st = pa::host_map_16(a.f16, &maps[2], q_out, 3, od, os, ob);
     if (st != PA_OK) return st;
     a.positions = positions;
     a.cos_sin = cos_sin;
@@ -293,7 +295,7 @@ pa_status pa_mla_output(const pa_mla_project_shapes* sh, const void* o, const vo
     if (sh->total_tokens < 0) return host_fail(PA_ERR_INVALID_ARG, "total_tokens must be >= 0");
     if (sh->total_tokens == 0) return PA_OK;
     pa::MlaProjectArgs a;
-    CUtensorMap maps[3];
+    CUtensorMap maps[2];
     pa_status st = fill_project(sh, pa::kMlaLatent, pa::kMlaValue, pa::kMlaOutputGroup, o, w_uv, out, workspace, workspace_bytes, &a, maps);
     if (st != PA_OK) return st;
     return launched(pa::launch_mla_output(a, maps, stream), "latent output launch");

@@ -75,8 +75,8 @@ struct MlaProjectArgs {
     int32_t total, heads, interleaved, max_position, f16;
     uint64_t wait_ns;
 };
-// maps: the input as [tokens, heads, elements] in boxes of 64 elements of 128 tokens, the weights as [heads, 128, 512] in
-// boxes of 64 elements of 128 rows, the output like the input
+// maps: the input as [tokens, heads, elements] in boxes of 64 elements of 128 tokens (query) or kMlaOutputGroup (output),
+// the weights as [heads, 128, 512] in boxes of 64 elements of 128 rows, the query's output like its input
 cudaError_t launch_mla_query(const MlaProjectArgs& a, const CUtensorMap* maps, cudaStream_t stream);
 cudaError_t launch_mla_output(const MlaProjectArgs& a, const CUtensorMap* maps, cudaStream_t stream);
 
