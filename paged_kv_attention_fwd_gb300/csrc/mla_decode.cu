@@ -32,7 +32,8 @@
 // agree whether one was exceeded; if so, in an item's first page, and as long as a
 // column has seen scores of -inf only, the columns' maxima over the page are found,
 // the accumulators rescaled and P written again (with the vote before P a call took
-// 61.2 us, with it after 60.0).
+// 61.2 us, with it after 60.0; with the first half of every sequence at -inf one of
+// 64 sequences and 128 heads takes 66.7 against 59.1, one of 16 heads 39.2 as without).
 //
 // The sequences' costs (pages and a constant) are laid end to end and cut into
 // equal ranges, as many as there are CTAs a block: a CTA takes what lies in its
@@ -51,13 +52,16 @@
 // What bounds it.  A byte of a row meets 2 x heads x 1.9 operations: with 128
 // heads more than the memory's rate asks of the tensor cores at N = 64, where an
 // MMA reads 6 KB of shared memory for 34 cycles of products (48 at 128 B a
-// cycle): 1920 cycles a page and block, against 1500 for the memory's share of an
-// SM.  Measured, 64 sequences of 1-4096 keys, 128 heads, bf16: 58.7 us, 6 of them
-// the merge, 6 the start (launch, dealing, first page), about 2400 cycles a page
-// (shared memory has room for two, and two take 4800: load 1150, S, softmax 1000,
-// O) and the outputs of pieces.  32 sequences of 64-16384 keys, 16 heads, two
-// tokens each: 59 us (287 MB, 4.9 TB/s; 6.6, the memory's copy rate, while pages
-// stream).  One sequence of 777 keys, 128 heads: 11.8 us.
+// cycle): 1920 cycles a page and block, against 1640 for the memory's share of an
+// SM (73.7 KB for two of them, at the 1.95 GHz that they run at).  Measured, 64
+// sequences of 1-4096 keys, 128 heads, bf16: 58.8 us.  A page takes about 2400
+// cycles (shared memory has room for two, and two take 4800: load 1150, S, softmax
+// 1000, O), so an SM's 28 pages take 67 thousand of the 108 thousand cycles of this
+// kernel, 35 us of 55; the other 20 are the start (6: launch, dealing, first page),
+// the outputs of pieces and the wait for the last CTA, and then there is the merge.
+// 32 sequences of 64-16384 keys, 16 heads, two tokens each: 59 us (287 MB, 4.9 TB/s;
+// 6.6, the memory's copy rate, while pages stream).  One sequence of 777 keys, 128
+// heads: 11.8 us.
 #include "pa_launch.h"
 #include "pa_mla.h"
 #include "pa_ptx.cuh"
@@ -75,7 +79,8 @@ constexpr int kListed = 16;  // sequences of a CTA's range whose pieces are foun
 constexpr int kThreads = 96 + 32 * kSoftmaxWarps;
 // What an item costs besides its pages, in pages (64 sequences of 1-4096 keys: 58.7 us a call with 3, 58.3 with 4, 59.5
 // with 5; one of 777: 11.8, 13.1 and 11.8), and the shortest range (one sequence of 777 keys: 17.1 us with 6, 14.0 with 3,
-// 13.0 with 2, 13.3 with 1, of which the output and the merge took one more than now).
+// 13.0 with 2, 13.3 with 1, of which the output and the merge took one more than now).  All at 64 columns; narrower
+// blocks, whose items cost less besides their pages, share both.
 constexpr int kFixed = 3;
 constexpr int kMinShare = 2;
 // fp16 weights are held as 2^7 times those beside the reference: at most 2^15, and whole steps of fp16 down to 2^-21 of it.
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Bound by the partials, 2 KB a row and piece out of L2, and by its launch: 40 MB in 6 us for 64 sequences and 128 heads.
 // A warp takes a row, a CTA four; blockIdx.y is the attention kernel's CTA.  Where sequences are few (kFew) their pieces
 // are many: the CTA's warps share the pieces of a quarter of a row, and blockIdx.y is (sequence, block).  One sequence of
-// 131072 keys, 16 heads, is 152 pieces a row: a call takes 41 us, with a warp a quarter of a row 58.  64 sequences take
+// 131072 keys, 16 heads, is 152 pieces a row: a call takes 40 us, with a warp a quarter of a row 58.  64 sequences take
 // 65 us that way against 60, with four pieces ahead instead of two 60.8.
 constexpr int kMergeWarps = 4;
 template <int N, bool kF16, bool kFew>
@@ -868,7 +873,10 @@ cudaError_t launch(MlaDecodeArgs& a, int sms, const CUtensorMap* maps, cudaStrea
     // as many ranges as there are SMs for them, and no more than the longest lengths could give one each
     const long long most = ((long long)a.batch * (kFixed + a.max_pages) + kMinShare - 1) / kMinShare;
     a.ranges = (int)max(1ll, min((long long)sms / blocks, most));
-    a.few = 8ll * a.batch <= a.ranges;  // (an item may then have more than 8 pieces, and entries by sequence fit)
+    // (The choice of the merge knows the batch and not the lengths.  Up to here entries by sequence fit into the list, and
+    // pieces may be more than 8 on average.  A long sequence among more short ones pays for it: one of 131072 keys and 18
+    // of 100, 16 heads, take 41.1 us, with a nineteenth of 100 52.2.)
+    a.few = 8ll * a.batch <= a.ranges;
     const unsigned ctas = (unsigned)(a.ranges * blocks);
     e = launch_overlapped(kernel, dim3(ctas), dim3(kThreads), smem, stream, a, maps[0], maps[1], maps[2]);
     if (e != cudaSuccess || a.ranges == 1) return e;

@@ -85,7 +85,7 @@ __device__ __forceinline__ void turn_rows(const MlaProjectArgs& a, int h, int to
 //
 // Bound by memory: 1 token x 128 heads is 17 MB of weights in 5.7 us (2.9 TB/s, of which the launch and the first
 // loads' latency are over half), 64 x 128 29 MB in 7.3 us (4.0 TB/s), 1999 x 64 205 MB in 40.7 us, 147 MB of them
-// written: a plain fill of as many bytes takes 41 us, one of 1 GB runs at 4.0 TB/s.  Tiles of 128 columns, three CTAs an
+// written: a plain fill of as many bytes takes 39 us (3.8 TB/s), one of 1 GB runs at 4.0 TB/s.  Tiles of 128 columns, three CTAs an
 // SM, took 7.1 and 9.8 us for the first two; three groups of one buffer and a token tile ahead 42 us for the third,
 // weights loaded for every tile and heads side by side in time 45.
 template <bool kLarge>
