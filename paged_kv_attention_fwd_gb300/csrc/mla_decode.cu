@@ -30,8 +30,9 @@
 // column, which changes only when a score exceeds it by more than 2^8.  P is
 // written with the references as they are, and then the four warps of a column
 // agree whether one was exceeded; if so, in an item's first page, and as long as a
-// column has seen scores of -inf only, the columns' maxima over the page are found,
-// the accumulators rescaled and P written again (with the vote before P a call took
+// column has seen scores of -inf only or has a reference beyond 2^14, the columns'
+// maxima over the page are found, the accumulators rescaled and P written again
+// (with the vote before P a call took
 // 61.2 us, with it after 60.0; with the first half of every sequence at -inf one of
 // 64 sequences and 128 heads takes 66.7 against 59.1, one of 16 heads 39.2 as without).
 //
@@ -85,6 +86,9 @@ constexpr int kFixed = 3;
 constexpr int kMinShare = 2;
 // fp16 weights are held as 2^7 times those beside the reference: at most 2^15, and whole steps of fp16 down to 2^-21 of it.
 constexpr float kShiftF16 = 7.f;
+// From here on (in bits) a column's weights are made of its products with the scale as they are rounded, page by page: up
+// to here the rounding is 2^-11 of a weight at most.
+constexpr float kFarReference = 16384.f;
 
 template <int N>
 struct Layout {
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (next_piece()) {
             const int n = pc.hi - pc.lo;
             float ref = -INFINITY;  // of the column to keep: what its weights are in units of (2^kShift below the maximum it was set by)
-            bool open = false;      // a column of the half has no reference yet: its scores so far were all -inf
+            bool open = false;      // a column of the half has no reference yet (its scores so far were all -inf), or a far one
             if (n > 0) {
                 if (tid < kHalf) {
                     const int tok = min(blk * N + column, a.rows - 1) / a.num_heads;
@@ -560,8 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto passed = [&](uint32_t behind) {  // O's MMAs of the page that many before this one
                     return g < behind || wait(&bars[B_OD + ((g - behind) & 1)], ((g - behind) >> 1) & 1);
                 };
-                // ---- P with the references as they are, and then: did a score exceed its own?  (With a column that has none,
-                // any score above -inf does: the page's maxima are looked at without asking.)
+                // ---- P with the references as they are, and then: did a score exceed its own?  With a column that has none,
+                // any score above -inf does: the page's maxima are looked at without asking.  With a far one too, as a
+                // product with the scale that is not rounded differs from its reference, one that was, by up to 2^-24 of
+                // it: nothing near 0, and more than all that weights depend on where masks add the type's lowest value.
                 bool change = p == pc.lo || open;
                 if (!change) {
                     float top = -INFINITY;
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (columns > 0 && __all_sync(0xffffffffu, !bad)) {
                         load_scores();
 #pragma unroll
-                        for (int c = 0; c < kQuarter; ++c) s[c] *= sl2;
+                        for (int c = 0; c < kQuarter; ++c) s[c] = __fmul_rn(s[c], sl2);
                         mask();
                         float v[kQuarter];
 #pragma unroll
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sh.minus_ref[column] = ref == -INFINITY ? 0.f : -ref;
                         sh.factor[column] = factor;
                     }
-                    open = bar_or(bar_id, 128, tid < columns && ref == -INFINITY);
+                    open = bar_or(bar_id, 128, tid < columns && !(fabsf(ref) < kFarReference));
                     const bool rescale = p > pc.lo;
                     bad = !passed(rescale ? 1 : L::kPBuffers);
                     if (columns > 0 && __all_sync(0xffffffffu, !bad)) {

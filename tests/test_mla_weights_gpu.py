@@ -18,10 +18,12 @@ pytestmark = pytest.mark.gpu
 LEAST = {"bf16": 0.0, "f16": 2.0 ** -32}
 
 
-def check(c, q, scale, out, lse, seen, terms=576, depth=None):
+def check(c, q, scale, out, lse, seen, terms=576, depth=None, skip=()):
     """One token a sequence.  seen[b]: [heads, keys], which keys have a score above -inf; terms: products of a score that
     are not zero; depth: additions that a key's share goes through (all keys of a sequence at most)."""
     for b, n in enumerate(c.lens):
+        if b in skip:
+            continue
         k, live = c.rows(b), seen[b]
         k = torch.where(torch.isfinite(k), k, 0.0)
         v = k[:, :512]
@@ -112,6 +114,25 @@ def test_scores_behind_a_hidden_prefix(layout, later):
     check(c, q, SCALE, *decode(c, q, sms=sms), seen)
 
 
+@pytest.mark.parametrize("first", [64, 130, -1])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_a_prefix_at_the_lowest_finite_value(layout, first):
+    """Times 0.5: scores of -1.2e37, finite references that later pages leave far below.  Where they are all that a head has,
+    they are all the same, in 64 bits too (what differs, 100 at most, is far below half a step), and weigh the same."""
+    c, q, seen, sms = hidden_case(layout, 20, first, "bf16", 2, True, torch.finfo(torch.bfloat16).min)
+    q[:, :, 575] *= 0.125
+    out, lse = decode(c, q, sms=sms)
+    same = [b for b, n in enumerate(c.lens) if n <= first]
+    check(c, q, SCALE, out, lse, seen, skip=same)
+    for b in same:
+        n, v, heads = c.lens[b], c.rows(b)[:, :512], ~seen[b].any(-1)
+        mean, spread = v.mean(0), v.abs().mean(0)
+        off = (out[b, heads].double() - mean).abs()
+        assert (off <= HALF["bf16"] * mean.abs() + 2 * n * 2.0 ** -23 * spread + TINY["bf16"]).all(), b
+        want = 0.5 * torch.finfo(torch.bfloat16).min * SCALE
+        assert ((lse[b, heads].double() / want - 1).abs() <= 2.0 ** -20).all(), b
+
+
 @pytest.mark.parametrize("q_len", [2, 4])
 def test_a_hidden_prefix_and_several_tokens(q_len):
     """Hidden keys and those that a token does not see yet: each token as it is alone over its own keys."""
@@ -127,6 +148,37 @@ def test_a_hidden_prefix_and_several_tokens(q_len):
         at = torch.arange(len(lens), device=DEV) * q_len + i
         seen = [(torch.arange(n, device=DEV) >= 64).expand(heads, -1) for n in c.lens]
         check(c, q[at], SCALE, out[at], lse[at], seen)
+
+
+@pytest.mark.parametrize("size", [3.0, 1e3, 1e4, 3e5, 1e9, 1e37])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_equal_scores_of_any_size(dtype, layout, sign, size):
+    """All keys of a sequence have the same score: they weigh the same, whatever it is and in whichever page they lie."""
+    lens, sms = LAYOUTS[layout]
+    c = Cache(lens, dtype, seed=8)
+    top = 6e4 if dtype == "f16" else 1e38
+    q = torch.zeros((len(lens), 20, 576), dtype=T16[dtype], device=DEV)
+    q[..., 512] = torch.linspace(0.7, 1.0, 20, device=DEV) * min(size, 100.0)
+    for b, n in enumerate(lens):
+        at = rows_at(c.table, b, 0, n)
+        x = c.rows(b).float()
+        x[:, :512] += (torch.arange(n, device=DEV) // 64)[:, None] * 0.25  # pages apart from one another
+        x[:, 512:] = 0.0
+        x[:, 512] = sign * min(size / min(size, 100.0), top)
+        c.pool.view(-1, 576)[at] = x.to(T16[dtype])
+    out, lse = decode(c, q, scale=1.0, sms=sms)
+    for b, n in enumerate(lens):
+        k = c.rows(b)
+        v, s = k[:, :512], q[b, :, 512].double() * k[0, 512]
+        mean, spread = v.mean(0), v.abs().mean(0)
+        # a weight: its rounding, and that of a score with the scale, 2^-11 at most; fp32 sums
+        tol = HALF[dtype] * mean.abs() + (HALF[dtype] + 2.0 ** -10 + 2 * n * 2.0 ** -23) * spread
+        off = (out[b].double() - mean).abs()
+        assert (off <= tol).all(), (b, (off / tol).max().item())
+        want = s + math.log(n)
+        assert ((lse[b].double() - want).abs() <= 2.0 ** -21 * want.abs() + 2.0 ** -10).all(), b
 
 
 # ----------------------------------------------------------------- light weights
