@@ -54,11 +54,11 @@
 // heads more than the memory's rate asks of the tensor cores at N = 64, where an
 // MMA reads 6 KB of shared memory for 34 cycles of products (48 at 128 B a
 // cycle): 1920 cycles a page and block, against 1640 for the memory's share of an
-// SM (73.7 KB for two of them, at the 1.95 GHz that they run at).  Measured, 64
+// SM (73.7 KB for two of them, at the 1.96 GHz that they run at).  Measured, 64
 // sequences of 1-4096 keys, 128 heads, bf16: 58.8 us.  A page takes about 2400
 // cycles (shared memory has room for two, and two take 4800: load 1150, S, softmax
-// 1000, O), so an SM's 28 pages take 67 thousand of the 108 thousand cycles of this
-// kernel, 35 us of 55; the other 20 are the start (6: launch, dealing, first page),
+// 1000, O), so an SM's 28 pages take 67 thousand of the 107 thousand cycles of this
+// kernel, 34 us of 54; the other 20 are the start (6: launch, dealing, first page),
 // the outputs of pieces and the wait for the last CTA, and then there is the merge.
 // 32 sequences of 64-16384 keys, 16 heads, two tokens each: 59 us (287 MB, 4.9 TB/s;
 // 6.6, the memory's copy rate, while pages stream).  One sequence of 777 keys, 128
