@@ -32,9 +32,9 @@
 // agree whether one was exceeded; if so, in an item's first page, and as long as a
 // column has seen scores of -inf only or has a reference beyond 2^14, the columns'
 // maxima over the page are found, the accumulators rescaled and P written again
-// (with the vote before P a call took
-// 61.2 us, with it after 60.0; with the first half of every sequence at -inf one of
-// 64 sequences and 128 heads takes 66.7 against 59.1, one of 16 heads 39.2 as without).
+// (with the vote before P a call took 61.2 us, with it after 60.0; with the first
+// half of every sequence at -inf one of 64 sequences and 128 heads takes 66.7
+// against 59.1, one of 16 heads 39.2 as without).
 //
 // The sequences' costs (pages and a constant) are laid end to end and cut into
 // equal ranges, as many as there are CTAs a block: a CTA takes what lies in its
